@@ -371,7 +371,7 @@ def _attend(s, case):
     total = p.sum(-1, keepdim=True)
     lse = (top + torch.log(total))[..., 0]
     o = torch.matmul(p.reshape(b, hk, q_max * group, n), v).reshape(b, hk, q_max, group, d)
-    o = torch.where(total > 0, o / total, 0.0)
+    o = torch.where(total == 0, 0.0, o / total)
     token = torch.arange(s["q"].shape[0], device=k.device)
     seq = torch.bucketize(token, start[1:], right=True)
     at = token - start[seq]
