@@ -273,6 +273,141 @@ int ar_packet_recv(ar_ptrs scratch, ar_ptrs out, int P, int rank_lo, int rank_hi
                    uint32_t flag, void *ctrl, uint64_t max_spins, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * Attention between the q/k/v projection and the output projection whose
+ * partial sums the calls above add up: one rank's heads.  Three operators that
+ * a decode step calls one after another: ar_qk_norm_rope, ar_kv4_write and
+ * ar_kv4_attention.
+ *
+ * Rows.  Queries, keys, values and outputs are arrays (tokens, heads, dim) of
+ * bf16 with the caller's strides, in elements and none negative, and with
+ * contiguous channels: the three parts of one projection's output are passed
+ * as they lie.  16-byte vectors are used where every row of a call starts on
+ * 16 bytes, single elements otherwise.  dim is 64, 128 or 256.  Rows of an
+ * array that is written must not share elements (AR_EINVAL).
+ *
+ * Alignment: weights 2 bytes, float and int32 arrays 4, int64 arrays 8, the
+ * cache and workspaces 16.  Buffers that are written must not overlap any
+ * other (AR_EALIAS) except where a call says so.
+ * ------------------------------------------------------------------------- */
+typedef struct ar_rows {
+    void *p;
+    int64_t token_stride; /* elements from one token to the next */
+    int64_t head_stride;  /* elements from one head to the next */
+} ar_rows;
+
+/* ---------------------------------------------------------------------------
+ * ar_qk_norm_rope -- norm of each query's and key's head with the position
+ * rotation in the same pass.  For a row x, with binary32 arithmetic and one
+ * rounding at the end:
+ *     z = x / sqrt(mean(x^2) + eps) * weight
+ *     y_a = z_a cos_i - z_b sin_i,  y_b = z_b cos_i + z_a sin_i
+ * for pair i < rotated / 2 of channels (a, b): (i, i + rotated / 2), or
+ * (2 i, 2 i + 1) where `interleaved` is not 0.  Channels from `rotated` on do
+ * not turn.
+ *   q, k       (tokens, heads, dim) and (tokens, kv_heads, dim); either count
+ *              of heads may be 0 (its pointers are not looked at).
+ *   q_weight, k_weight   dim bf16 each.
+ *   cos_sin    (table, rotated) floats: a position's cosines, then its sines.
+ *   positions  tokens int64.  A position outside [0, table) makes the token's
+ *              rows NaN; the table is not read there.
+ *   q_out, k_out   may be q and k exactly (in place).
+ *   rotated    a multiple of 16 in [16, dim].
+ *   eps        >= 0.
+ * ------------------------------------------------------------------------- */
+int ar_qk_norm_rope(ar_rows q, ar_rows k, const void *q_weight, const void *k_weight,
+                    const void *cos_sin, const void *positions, ar_rows q_out, ar_rows k_out,
+                    int64_t tokens, int heads, int kv_heads, int dim, int rotated, int64_t table,
+                    float eps, int interleaved, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * ar_qk_norm_rope_bwd -- the gradient of ar_qk_norm_rope: dq and dk (bf16) for
+ * q_grad and k_grad, and the weights' gradients (dim floats each, sums over
+ * tokens and heads in binary32, in an order that depends on the sizes alone).
+ *   dq, dk     may be q_grad or q, and k_grad or k, exactly.
+ *   workspace  ar_qk_norm_rope_bwd_workspace bytes, zeroed once; every call
+ *              leaves it fit for the next, of any sizes that it is large
+ *              enough for.  Two calls in flight on one workspace are not
+ *              allowed.
+ * tokens == 0 sets the weights' gradients to 0.
+ * ------------------------------------------------------------------------- */
+int64_t ar_qk_norm_rope_bwd_workspace(int64_t tokens, int heads, int kv_heads, int dim);
+int ar_qk_norm_rope_bwd(ar_rows q_grad, ar_rows k_grad, ar_rows q, ar_rows k, const void *q_weight,
+                        const void *k_weight, const void *cos_sin, const void *positions, ar_rows dq,
+                        ar_rows dk, void *dq_weight, void *dk_weight, void *workspace,
+                        int64_t tokens, int heads, int kv_heads, int dim, int rotated, int64_t table,
+                        float eps, int interleaved, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The 4-bit cache of keys and values: (pages, kv_heads, page_size / 32) tiles
+ * of 34 dim bytes, each 32 tokens of one head: K codes (16 dim bytes), V codes
+ * (16 dim), K scales (dim), V scales (dim).  page_size is a power of two from
+ * 32 to 65536, and pages * page_size < 2^31.
+ *
+ * Codes are E2M1 (values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), two in a
+ * byte, the even channel in the low half.  32 channels of a token share the
+ * scale 2^(byte - 127); 255 stands for a group that held an infinity or a NaN:
+ * all its values are NaN (and ar_kv4_write leaves zeros for its codes).  Places in a tile, for token t, channel c, group
+ * g = c / 32, W = dim / 16 and G = dim / 32:
+ *     K code byte   t dim/2 + c/2
+ *     V code byte   16 dim + ((t/8 16 + c/W) 8 + t%8) W/2 + c%W/2
+ *     K scale byte  32 dim + (g 16 + t/8 4 + t%4) 2 + t%8/4
+ *     V scale byte  33 dim + (t/8 G + g) 8 + t%8
+ * which is the order that the matrix instructions of ar_kv4_attention take
+ * them in.
+ *
+ * ar_kv4_write quantises: the byte is the least from 2 on (at most 252) whose
+ * scale leaves the group's largest magnitude below 7; each value becomes the
+ * nearest one, ties to the even code.  ar_kv4_read gives the values back,
+ * exact in bf16.
+ *   k, v    (tokens, kv_heads, dim).
+ *   slots   tokens int64: page * page_size + place in the page.  A write to a
+ *           slot outside the cache is left out, a read of one gives zeros.  A
+ *           slot that is named twice in one write gets either token's bytes.
+ *   cache   16-byte aligned.
+ * ------------------------------------------------------------------------- */
+int64_t ar_kv4_cache_bytes(int64_t pages, int kv_heads, int dim, int page_size);
+int ar_kv4_write(ar_rows k, ar_rows v, const void *slots, void *cache, int64_t tokens, int kv_heads,
+                 int dim, int64_t pages, int page_size, void *stream);
+int ar_kv4_read(const void *cache, const void *slots, ar_rows k_out, ar_rows v_out, int64_t tokens,
+                int kv_heads, int dim, int64_t pages, int page_size, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * ar_kv4_attention -- attention of each sequence's queries over its cached
+ * keys and values.  Sequence b has queries [q_start[b], q_start[b + 1]) and
+ * kv_len[b] cached tokens, the queries' own the last of them: query i of m is
+ * at position p = kv_len[b] - m + i and sees tokens j <= p, with a window only
+ * those of j > p - window.
+ *     out = sum_j softmax_j(scale q . k_j) v_j,  lse = log sum_j exp(scale q . k_j)
+ * A query that sees nothing gets zeros and -infinity.  A token that a query
+ * does not see adds nothing to it, whatever the cache holds there.  A query
+ * row that is not finite gives NaN.
+ *   q, out      (tokens, heads, dim); query head h reads key head
+ *               h / (heads / kv_heads).
+ *   page_table  (batch, pages_per_seq) int32 with rows table_stride apart:
+ *               token j of a sequence is on the page of entry j / page_size.
+ *               Tokens past the last entry, or on a page outside the cache,
+ *               are not seen.  Entries past a sequence's tokens are not read.
+ *   q_start     batch + 1 int32, rising; kv_len batch int32.
+ *   lse         (tokens, heads) floats.
+ *   workspace   ar_kv4_attention_workspace bytes, zeroed once; every call
+ *               leaves it fit for the next, of any sizes that it is large
+ *               enough for.  Two calls in flight on one workspace are not
+ *               allowed.
+ *   max_q       at least the largest number of queries of a sequence (those
+ *               past it get no output); max_kv the largest kv_len, or any
+ *               bound on it: it only says how the work is split.
+ *   window      0: none.
+ *   scale       > 0.
+ * ------------------------------------------------------------------------- */
+int64_t ar_kv4_attention_workspace(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv,
+                                   int heads, int kv_heads, int dim);
+int ar_kv4_attention(ar_rows q, const void *cache, const void *page_table, int64_t table_stride,
+                     const void *q_start, const void *kv_len, ar_rows out, void *lse, void *workspace,
+                     int64_t tokens, int64_t batch, int heads, int kv_heads, int dim, int64_t pages,
+                     int page_size, int64_t pages_per_seq, int64_t max_q, int64_t max_kv,
+                     int64_t window, float scale, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Host-only helpers: no GPU needed, no HIP call made.
  * ------------------------------------------------------------------------- */
 
