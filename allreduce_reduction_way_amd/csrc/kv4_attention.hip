@@ -10,13 +10,11 @@
 // head, sixteen to a row tile, and one wave holds R row tiles.  All products
 // are done by the matrix unit in tiles of 16 rows x 32 tokens:
 //
-// Scores, transposed: S^T = K Q^T.  K goes in as it is stored, E2M1 codes with
-// their scales, without any conversion.  Q is split into two e4m3 parts,
-// q = h 2^x + l 2^(x-5) with one x for the row: h is q rounded to four bits
-// and l what is left, which for a bf16 of eight bits is exact until l falls
-// below the smallest e4m3 number, 2^-21 of the row's largest element.  So the
-// scores are as good as a product in binary32, for two products of the fast
-// kind.
+// Scores, transposed: S^T = K Q^T, with K's codes turned into bf16, which is
+// exact.  (The scaled instructions take codes as they are, against a query in
+// two e4m3 parts, for the same time in the matrix unit.  But they align the
+// terms of a product to its largest and drop what lies 2^-20 below: scores
+// were off by 4e-6 where these are by 3e-8.)
 //
 // Output, transposed: O^T = V^T P^T with P rounded to bf16 (half a step, 2^-8,
 // of each weight; the sum of weights is kept unrounded) and V's codes turned
@@ -38,7 +36,6 @@
 namespace ar {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -63,155 +60,57 @@ struct AttnArgs {
     float c;  // scale log2(e)
 };
 
-// The codes and scales that a lane takes of one tile.
+// The codes and scales that a lane takes of one tile.  With r = lane % 16 and
+// a = lane / 16, of K: D/4 channels of tokens r / 4 * 8 + r % 4 and four on,
+// which lie in one group of channels (in two blocks of 128 at D = 256, half a
+// group at 64); of V: channels r W .. r W + W - 1 of tokens 8 a .. 8 a + 7.
 template <int D>
 struct Tile {
-    static constexpr int kBlocks = D > 128 ? D / 128 : 1;  // K = 128 products along D
-    u32x4 k[2][kBlocks];
-    uint32_t ks[kBlocks];
+    static constexpr int kBlocks = D > 128 ? D / 128 : 1;
+    static constexpr int kWords = D / 32 / kBlocks;  // words of K codes in a block
+    uint32_t k[2][kBlocks][kWords];
+    uint32_t ks[kBlocks];  // scale bytes of the two tokens
     uint32_t v[D / 16];
     uint32_t vs[2];
-    int index;   // tile of the sequence
-    bool known;  // its page is one of the cache's
 };
 
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p) {
+    if (N == 2) {
+        const uint2 t = *reinterpret_cast<const uint2 *>(p);
+        w[0] = t.x, w[1] = t.y;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        const u32x4 t = reinterpret_cast<const u32x4 *>(p)[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[i * 4 + j] = t[j];
+    }
+}
+
 template <int D>
-__device__ __forceinline__ void load_tile(Tile<D> &t, const AttnArgs &a, const int32_t *pages, int h,
-                                          int index, int lane) {
+__device__ __forceinline__ void load_tile(Tile<D> &t, const uint8_t *p, int lane) {
     using L = Kv4<D>;
     const int r = lane % 16, q = lane / 16;
-    const int page = pages[index >> a.shift];
-    t.index = index;
-    t.known = page >= 0 && page < a.pages;
-    const int64_t at = (((int64_t)(t.known ? page : 0) * a.kv_heads + h) << a.shift) + (index & ((1 << a.shift) - 1));
-    const uint8_t *p = a.cache + at * L::kBytes;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int tok = r / 4 * 8 + i * 4 + r % 4;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int b = 0; b < Tile<D>::kBlocks; ++b)
-            t.k[i][b] = *reinterpret_cast<const u32x4 *>(p + L::k_code(tok, D == 64 ? q % 2 * 32 : b * 128 + q * 32));
-    }
+            load_words(t.k[i][b], p + L::k_code(r / 4 * 8 + i * 4 + r % 4, D == 64 ? q * 16 : b * 128 + q * 32));
 #pragma unroll
     for (int b = 0; b < Tile<D>::kBlocks; ++b)
-        t.ks[b] = *reinterpret_cast<const uint16_t *>(p + L::kKScale + ((D == 64 ? q % 2 : b * 4 + q) * 16 + r) * 2);
-    const u32x4 *v = reinterpret_cast<const u32x4 *>(p + L::kV + lane % 16 * (4 * L::W) + q * (64 * L::W));
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        const u32x4 w = v[i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) t.v[i * 4 + j] = w[j];
-    }
-    const uint2 s = *reinterpret_cast<const uint2 *>(p + L::kVScale + (q * L::G + r * L::W / kGroup) * 8);
-    t.vs[0] = s.x, t.vs[1] = s.y;
+        t.ks[b] = *reinterpret_cast<const uint16_t *>(p + L::kKScale + ((D == 64 ? q / 2 : b * 4 + q) * 16 + r) * 2);
+    load_words(t.v, p + L::kV + lane * (4 * L::W));
+    load_words(t.vs, p + L::kVScale + (q * L::G + r * L::W / kGroup) * 8);
 }
 
-// Sixteen rows of queries as the score product takes them: D/4 channels of row
-// lane % 16 in each lane, in two e4m3 parts.
-template <int D>
-struct Query {
-    static constexpr int kWords = D / 16;  // words of each part
-    uint32_t hi[kWords], lo[kWords];
-    uint32_t scale;  // the parts' scale bytes: hi in byte 0, lo in byte 1
-
-    __device__ __forceinline__ void load(const uint16_t *row, int lane, bool vec) {
-        const int q = lane / 16;
-        float x[D / 4];
-        uint32_t most = 0;
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {  // runs of sixteen channels
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint16_t *p = row + i * 64 + q * 16 + j * 8;
-                const u32x4 w = vec ? load8<true>(p) : load8<false>(p);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    most = max(most, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
-                    x[i * 16 + j * 8 + 2 * e] = lo_f32(w[e]);
-                    x[i * 16 + j * 8 + 2 * e + 1] = hi_f32(w[e]);
-                }
-            }
-        }
-        most = max(most, (uint32_t)__shfl_xor((int)most, 16));
-        most = max(most, (uint32_t)__shfl_xor((int)most, 32));
-        // the largest lands in [128, 256) of 448; tiny rows keep a scale that
-        // the lower part's can follow
-        const uint32_t e = max(most >> 23, 12u);
-        const float up = __uint_as_float((254u + 7u - min(e, 254u)) << 23);
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-            float y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = x[4 * i + j] * up;
-            int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-            w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
-            hi[i] = (uint32_t)w;
-            y[0] = (y[0] - __builtin_amdgcn_cvt_f32_fp8(w, 0)) * 32.0f;
-            y[1] = (y[1] - __builtin_amdgcn_cvt_f32_fp8(w, 1)) * 32.0f;
-            y[2] = (y[2] - __builtin_amdgcn_cvt_f32_fp8(w, 2)) * 32.0f;
-            y[3] = (y[3] - __builtin_amdgcn_cvt_f32_fp8(w, 3)) * 32.0f;
-            w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-            w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
-            lo[i] = (uint32_t)w;
-        }
-        // a row that is not finite has no scores: NaN
-        scale = most >= 0x7F800000u ? 0xFFFFu : (e - 7u) | (e - 12u) << 8;
-        // at 64 channels one product takes both parts, a K of 64 each: its
-        // scales are the lanes' halves
-        if (D == 64) scale = q < 2 ? scale & 0xFFu : scale >> 8;
-    }
-};
-
-__device__ __forceinline__ i32x8 codes8(u32x4 v) {
-    return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+// Byte n of the scales as a scale.  The conversions take the exponent's bits
+// alone, so what else a shift leaves in the word does no harm.
+template <int N>
+__device__ __forceinline__ float scale_at(const uint32_t (&w)[N], int n) {
+    return n % 4 == 3 ? __uint_as_float(w[n / 4] >> 1) : __uint_as_float(w[n / 4] << (23 - n % 4 * 8));
 }
-
-__device__ __forceinline__ i32x8 words8(const uint32_t *a, const uint32_t *b) {
-    return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-}
-
-constexpr int kFp4 = 4, kFp8 = 0;  // operand formats of the scaled product
-
-template <int H, int PART>
-__device__ __forceinline__ f32x4 score_step(i32x8 k, i32x8 q, f32x4 s, uint32_t ks, uint32_t qs) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, q, s, kFp4, kFp8, H, (int)ks, PART, (int)qs);
-}
-
-// Scores of a row tile against tokens 8 a + 4 H + i of a tile, i = 0..3.
-template <int D, int H>
-__device__ __forceinline__ f32x4 scores(const Tile<D> &t, const Query<D> &q) {
-    f32x4 s = {0, 0, 0, 0};
-    if (D == 64) return score_step<H, 0>(codes8(t.k[H][0]), words8(q.hi, q.lo), s, t.ks[0], q.scale);
-#pragma unroll
-    for (int b = 0; b < Tile<D>::kBlocks; ++b) {
-        s = score_step<H, 0>(codes8(t.k[H][b]), words8(q.hi + 8 * b, q.hi + 8 * b + 4), s, t.ks[b], q.scale);
-        s = score_step<H, 1>(codes8(t.k[H][b]), words8(q.lo + 8 * b, q.lo + 8 * b + 4), s, t.ks[b], q.scale);
-    }
-    return s;
-}
-
-// V of a tile as the output product takes it: block j holds channel r W + j of
-// tokens 8 a .. 8 a + 7.
-template <int D>
-struct Values {
-    uint32_t w[Kv4<D>::W][4];
-
-    __device__ __forceinline__ void load(const Tile<D> &t) {
-        constexpr int W = Kv4<D>::W;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {  // tokens 2 n and 2 n + 1
-            const float s0 = kv4_scale((t.vs[n / 2] >> (n % 2 * 16)) & 255u);
-            const float s1 = kv4_scale((t.vs[n / 2] >> (n % 2 * 16 + 8)) & 255u);
-#pragma unroll
-            for (int j = 0; j < W; j += 2) {
-                const int b0 = (2 * n * W + j) / 2, b1 = b0 + W / 2;
-                const uint32_t x = kv4_pair(t.v[b0 / 4], s0, b0 % 4), y = kv4_pair(t.v[b1 / 4], s1, b1 % 4);
-                w[j][n] = __builtin_amdgcn_perm(y, x, 0x05040100u);
-                w[j + 1][n] = __builtin_amdgcn_perm(y, x, 0x07060302u);
-            }
-        }
-    }
-};
 
 __device__ __forceinline__ bf16x8 as_bf16(const uint32_t (&w)[4]) {
     return __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
@@ -258,17 +157,28 @@ struct RowTile {
 template <int D, int R>
 struct State {
     RowTile<D> row[R];
-    Query<D> q[R];
-    int pos[R];  // position of this lane's row
+    uint32_t q[R][D / 32][4];  // D/4 channels of row lane % 16, in K's order
+    int pos[R];                // position of this lane's row
 };
 
-// One tile.  MASKED: some of its tokens are unseen by some rows.
-template <int D, int R, bool MASKED>
-__device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, const AttnArgs &a, int lane) {
+// How far the weights may outgrow 1 (in units of log2) before a new maximum is
+// taken: bf16 and binary32 lose nothing up to there, and most tiles move the
+// maximum by less, so that rescaling the output is rare.
+constexpr float kSlack = 8.0f;
+
+__device__ __forceinline__ bool sees(int pos, int token, int window) {
+    return token <= pos && (window == 0 || pos - token < window);
+}
+
+// One tile.  `masked` (the same in all lanes): some of its tokens are unseen by
+// some rows.
+template <int D, int R>
+__device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, bool masked, const AttnArgs &a, int lane) {
     constexpr int W = Kv4<D>::W;
+    using T = Tile<D>;
     bool nan_values = false;
     uint32_t flag[4] = {0, 0, 0, 0};  // 1 for each token whose V scale stands for NaN
-    if (MASKED) {
+    if (masked) {
         // a token that a row does not see adds nothing to it, whatever V holds:
         // NaNs are taken out here and given to the rows that see them
         nan_values = __any(any_nan_scale(t.vs[0]) || any_nan_scale(t.vs[1]));
@@ -281,51 +191,84 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, const AttnArgs
                 }
         }
     }
-    Values<D> v;
-    v.load(t);
+    f32x4 s[R][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[r][h] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n) {
+            const uint32_t ks[1] = {t.ks[n / T::kWords]};
+            const float scale = scale_at(ks, h);
+            uint32_t k[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) k[e] = kv4_pair(t.k[h][n / T::kWords][n % T::kWords], scale, e);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(k), as_bf16(st.q[r][n]), s[r][h], 0, 0, 0);
+        }
+    }
+    uint32_t p[R][4];
+    const int first = index * kTile + lane / 16 * 8;  // this lane's first token
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         RowTile<D> &o = st.row[r];
-        f32x4 s[2] = {scores<D, 0>(t, st.q[r]), scores<D, 1>(t, st.q[r])};
-        uint32_t seen[4] = {0, 0, 0, 0};
-        if (MASKED) {
-            const int first = t.index * kTile + lane / 16 * 8;
+        if (masked) {
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                const int j = first + n;
-                const bool see = j <= st.pos[r] && (a.window == 0 || st.pos[r] - j < a.window);
-                if (!see) s[n / 4][n % 4] = kNegInf;
-                if (see) seen[n / 2] |= 0x3F80u << (n % 2 * 16);
-            }
+            for (int n = 0; n < 8; ++n)
+                if (!sees(st.pos[r], first + n, a.window)) s[r][n / 4][n % 4] = kNegInf;
         }
-        float top = s[0][0];
+        float top = s[r][0][0];
 #pragma unroll
-        for (int n = 1; n < 8; ++n) top = fmaxf(top, s[n / 4][n % 4]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float m = fmaxf(o.m, top * a.c);
-        const float base = m == kNegInf ? 0.0f : m;
-        o.rescale(__builtin_amdgcn_exp2f(o.m - base));
-        o.m = m;
-        float p[8];
+        for (int n = 1; n < 8; ++n) top = fmaxf(top, s[r][n / 4][n % 4]);
+        if (__any(top * a.c > o.m + kSlack)) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float m = fmaxf(o.m, top * a.c);
+            o.rescale(o.weight(o.m, m));
+            o.m = m;
+        }
+        const float base = o.m == kNegInf ? 0.0f : o.m;
+        float w[8];
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-            p[n] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n / 4][n % 4], a.c, -base));
-            o.l += p[n];
+            w[n] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][n / 4][n % 4], a.c, -base));
+            o.l += w[n];
         }
-        const uint32_t w[4] = {bf16_pair(p[0], p[1]), bf16_pair(p[2], p[3]), bf16_pair(p[4], p[5]), bf16_pair(p[6], p[7])};
-        const bf16x8 pb = as_bf16(w);
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            o.acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(v.w[j]), pb, o.acc[j], 0, 0, 0);
-        if (MASKED && nan_values) {
+        for (int n = 0; n < 4; ++n) p[r][n] = bf16_pair(w[2 * n], w[2 * n + 1]);
+    }
+#pragma unroll
+    for (int j = 0; j < W; j += 2) {
+        uint32_t v[2][4];  // channels j and j + 1 of eight tokens
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int b0 = (2 * n * W + j) / 2, b1 = b0 + W / 2;
+            const uint32_t x = kv4_pair(t.v[b0 / 4], scale_at(t.vs, 2 * n), b0 % 4);
+            const uint32_t y = kv4_pair(t.v[b1 / 4], scale_at(t.vs, 2 * n + 1), b1 % 4);
+            v[0][n] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+            v[1][n] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                st.row[r].acc[j + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(v[i]), as_bf16(p[r]), st.row[r].acc[j + i], 0, 0, 0);
+    }
+    if (nan_values) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint32_t seen[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+                if (sees(st.pos[r], first + n, a.window)) seen[n / 2] |= 0x3F80u << (n % 2 * 16);
             const f32x4 z = {0, 0, 0, 0};
             const f32x4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(flag), as_bf16(seen), z, 0, 0, 0);
 #pragma unroll
             for (int j = 0; j < W; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (n[i] > 0) o.acc[j][i] = __uint_as_float(0x7FC00000u);
+                    if (n[i] > 0) st.row[r].acc[j][i] = __uint_as_float(0x7FC00000u);
         }
     }
 }
@@ -361,32 +304,51 @@ __device__ __forceinline__ bool locate(Block &b, const AttnArgs &a, int seq, int
 
 template <int D, int R>
 __device__ __forceinline__ void begin(State<D, R> &st, const AttnArgs &a, const Block &b, int lane) {
+    constexpr int kRun = D == 64 ? 16 : 32;  // channels of a lane that lie side by side
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int row = min(b.first + r * 16 + lane % 16, b.rows - 1);  // rows past the last repeat it
         const int i = row / a.group, h = b.head * a.group + row % a.group;
-        st.q[r].load(a.q.p + (int64_t)(b.q0 + i) * a.q.ts + (int64_t)h * a.q.hs, lane, a.vec);
+        const uint16_t *p = a.q.p + (int64_t)(b.q0 + i) * a.q.ts + (int64_t)h * a.q.hs + lane / 16 * kRun;
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n) {
+            const uint16_t *at = p + n / (kRun / 8) * 128 + n % (kRun / 8) * 8;
+            const u32x4 w = a.vec ? load8<true>(at) : load8<false>(at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st.q[r][n][e] = w[e];
+        }
         st.pos[r] = b.n - b.len + i;
         st.row[r].clear();
     }
 }
 
-// Tiles lo, lo + by, ... below hi.
+// Tiles lo, lo + by, ... below hi.  While a tile is worked on, the next one is
+// on its way; the pages of 64 tiles are looked up at once, one in each lane.
 template <int D, int R>
 __device__ __forceinline__ void sweep(State<D, R> &st, const AttnArgs &a, const Block &b, int lo, int hi, int by, int lane) {
-    if (lo >= hi) return;
     const int32_t *pages = a.table + (int64_t)b.seq * a.table_stride;
-    Tile<D> now, next;
-    load_tile(now, a, pages, b.head, lo, lane);
-    for (int t = lo; t < hi; t += by) {
-        load_tile(next, a, pages, b.head, t + by < hi ? t + by : t, lane);
-        if (now.known) {
-            if (t * kTile >= b.seen_lo && (t + 1) * kTile <= b.seen_hi)
-                step<D, R, false>(st, now, a, lane);
-            else
-                step<D, R, true>(st, now, a, lane);
+    for (int t = lo; t < hi; t += 64 * by) {
+        const int count = min(64, (hi - t + by - 1) / by);
+        const int page = pages[(t + min(lane, count - 1) * by) >> a.shift];
+        Tile<D> now, next;
+        const auto at = [&](int i, bool &known) {
+            const int pg = __builtin_amdgcn_readlane(page, i);
+            known = pg >= 0 && pg < a.pages;
+            const int64_t tile = (((int64_t)(known ? pg : 0) * a.kv_heads + b.head) << a.shift) + ((t + i * by) & ((1 << a.shift) - 1));
+            return a.cache + tile * Kv4<D>::kBytes;
+        };
+        bool known, known_next;
+        load_tile(now, at(0, known), lane);
+        for (int i = 0; i < count; ++i) {
+            load_tile(next, at(min(i + 1, count - 1), known_next), lane);
+            const int index = t + i * by;
+            if (known) {
+                const bool masked = index * kTile < b.seen_lo || (index + 1) * kTile > b.seen_hi;
+                step<D, R>(st, now, index, masked, a, lane);
+            }
+            now = next;
+            known = known_next;
         }
-        now = next;
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {  // each lane has added its own tokens
@@ -423,9 +385,69 @@ __device__ __forceinline__ void finish(const RowTile<D> &o, const AttnArgs &a, c
     if (lane < 16) a.lse[token * a.heads + h] = log_sum(o.m, o.l);
 }
 
+constexpr int kJoinSplits = 16;  // results that one workgroup joins
+
+// Joins `count` results that lie `stride` floats apart: into the output (LAST),
+// or into the first of them.  A wave takes pairs of channels of all rows.
+template <int D, int R, bool LAST>
+__device__ __forceinline__ void join(float *base, int64_t stride, int count, const AttnArgs &a, const Block &b, float *lds, int lane, int wave) {
+    constexpr int W = Kv4<D>::W, kStats = R * W * 256;
+    float *ms = lds, *ls = lds + kJoinSplits * 16;
+    static_assert(kJoinSplits * 32 <= kWaves / 2 * W * 256, "the maxima and sums fit the exchange memory");
+    for (int r = 0; r < R; ++r) {
+        if (b.first + r * 16 >= b.rows) break;
+        __syncthreads();
+        for (int i = threadIdx.x; i < count * 16; i += kThreads) {
+            const float *p = base + i / 16 * stride + kStats + r * 32 + i % 16;
+            const bool used = b.first + r * 16 + i % 16 < b.rows;
+            ms[i] = used ? load_shared(p) : kNegInf;
+            ls[i] = used ? load_shared(p + 16) : 0.0f;
+        }
+        __syncthreads();
+        const int row = b.first + r * 16 + lane % 16;
+        float m = kNegInf, l = 0;
+        for (int s = 0; s < count; ++s) m = fmaxf(m, ms[s * 16 + lane % 16]);
+        for (int s = 0; s < count; ++s) l += ls[s * 16 + lane % 16] * RowTile<D>::weight(ms[s * 16 + lane % 16], m);
+        if (row >= b.rows) continue;
+        for (int j = wave * 2; j < W; j += kWaves * 2) {
+            float *p = base + ((r * W + j) * 64 + lane) * 4;
+            f32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll 8
+            for (int s = 0; s < count; ++s) {
+                const float w = RowTile<D>::weight(ms[s * 16 + lane % 16], m);
+                sum[0] += load_shared4(p + s * stride) * w;
+                sum[1] += load_shared4(p + s * stride + 256) * w;
+            }
+            if (LAST) {
+                const int i = row / a.group, h = b.head * a.group + row % a.group;
+                const float inv = l == 0 ? 0.0f : 1.0f / l;
+                uint16_t *o = const_cast<uint16_t *>(a.out.p) + (int64_t)(b.q0 + i) * a.out.ts + (int64_t)h * a.out.hs + lane / 16 * (4 * W) + j;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t w = pack_bf16x2(sum[0][e] * inv, sum[1][e] * inv);
+                    if (a.vec) {
+                        *reinterpret_cast<uint32_t *>(o + e * W) = w;
+                    } else {
+                        o[e * W] = (uint16_t)w;
+                        o[e * W + 1] = (uint16_t)(w >> 16);
+                    }
+                }
+                if (wave == 0 && j == 0 && lane < 16) a.lse[(int64_t)(b.q0 + i) * a.heads + h] = log_sum(m, l);
+            } else {
+                store_shared(p, sum[0]);
+                store_shared(p + 256, sum[1]);
+                if (wave == 0 && j == 0 && lane < 16) {
+                    store_shared(base + kStats + r * 32 + lane, m);
+                    store_shared(base + kStats + r * 32 + 16 + lane, l);
+                }
+            }
+        }
+    }
+}
+
 // Many rows: every wave has a row block of its own and sweeps all its tiles.
 template <int D, int R>
-__global__ __launch_bounds__(kThreads) void k_kv4_attention_wide(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) {
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int per = (a.blocks + kWaves - 1) / kWaves;
     const int id = blockIdx.x;
@@ -441,7 +463,7 @@ __global__ __launch_bounds__(kThreads) void k_kv4_attention_wide(AttnArgs a) {
 
 // Few rows: the waves of a workgroup share a row block.
 template <int D, int R>
-__global__ __launch_bounds__(kThreads) void k_kv4_attention(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void k_kv4_attention(AttnArgs a) {
     constexpr int W = Kv4<D>::W;
     __shared__ f32x4 acc[kWaves / 2][R][W][64];
     __shared__ float ml[kWaves / 2][R][2][16];
@@ -495,45 +517,43 @@ __global__ __launch_bounds__(kThreads) void k_kv4_attention(AttnArgs a) {
         return;
     }
 
-    // results of a split: R W 64 vectors as the lanes hold them, then the
-    // maxima and sums
+    // A split's result: R W vectors as the lanes hold them, then maxima and
+    // sums.  Up to kJoinSplits of them are joined at once; more, in two levels.
     constexpr int kPart = R * W * 256 + R * 32;
     float *base = a.part + (int64_t)unit * a.splits * kPart;
+    uint32_t *counter = a.counters + unit * (1 + kJoinSplits);
     if (wave == 0) {
         float *p = base + (int64_t)split * kPart;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (b.first + r * 16 + lane % 16 < b.rows) {
 #pragma unroll
-                for (int j = 0; j < W; ++j) reinterpret_cast<f32x4 *>(p)[(r * W + j) * 64 + lane] = st.row[r].acc[j];
+                for (int j = 0; j < W; ++j) store_shared(p + ((r * W + j) * 64 + lane) * 4, st.row[r].acc[j]);
                 if (lane < 16) {
-                    p[R * W * 256 + r * 32 + lane] = st.row[r].m;
-                    p[R * W * 256 + r * 32 + 16 + lane] = st.row[r].l;
+                    store_shared(p + R * W * 256 + r * 32 + lane, st.row[r].m);
+                    store_shared(p + R * W * 256 + r * 32 + 16 + lane, st.row[r].l);
                 }
             }
         }
     }
-    if (!arrive_last(a.counters + unit, count, &order)) return;
-    for (int r = wave; r < R; r += kWaves) {
-        if (b.first + r * 16 + lane % 16 >= b.rows) continue;
-        RowTile<D> o;
-        o.clear();
-        for (int s = 0; s < count; ++s) {
-            const float *p = base + (int64_t)s * kPart;
-            const float m2 = p[R * W * 256 + r * 32 + lane % 16], l2 = p[R * W * 256 + r * 32 + 16 + lane % 16];
-            const float m = fmaxf(o.m, m2), w1 = o.weight(o.m, m), w2 = o.weight(m2, m);
-            o.m = m;
-            o.l = o.l * w1 + l2 * w2;
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-                o.acc[j] = o.acc[j] * w1 + reinterpret_cast<const f32x4 *>(p)[(r * W + j) * 64 + lane] * w2;
-        }
-        finish(o, a, b, r, lane);
+    const int groups = (count + kJoinSplits - 1) / kJoinSplits;
+    float *scratch = reinterpret_cast<float *>(&acc[0][0][0][0]);
+    if (groups > 1) {
+        const int g = split / kJoinSplits;
+        const int size = min(kJoinSplits, count - g * kJoinSplits);
+        if (!arrive_last(counter + 1 + g, size, &order)) return;
+        float *p = base + (int64_t)g * kJoinSplits * kPart;
+        join<D, R, false>(p, kPart, size, a, b, scratch, lane, wave);
+        if (!arrive_last(counter, groups, &order)) return;
+        join<D, R, true>(base, (int64_t)kJoinSplits * kPart, groups, a, b, scratch, lane, wave);
+    } else {
+        if (!arrive_last(counter, count, &order)) return;
+        join<D, R, true>(base, kPart, count, a, b, scratch, lane, wave);
     }
 }
 
 constexpr int kCounters = 16384;  // counters at the start of the workspace
-constexpr int kSplits = 32;       // workgroups that share a row block, at most
+constexpr int kSplits = kJoinSplits * kJoinSplits;  // workgroups that share a row block, at most
 constexpr int kFill = 1024;       // workgroups that fill the device: four on each compute unit
 
 // How a call is laid out, by its sizes alone.
@@ -547,13 +567,13 @@ struct Plan {
 Plan plan(int batch, int max_q, int64_t max_kv, int group, int kv_heads, int dim) {
     Plan p = {};
     const int64_t rows = (int64_t)max_q * group, tiles = (rows + 15) / 16;
-    const int most = dim > 128 ? 1 : 4;
+    const int most = dim == 64 ? 3 : dim == 128 ? 2 : 1;
     p.tiles = (int)(tiles < most ? tiles : most);
     p.blocks = (int)((tiles + p.tiles - 1) / p.tiles);
     p.units = (int64_t)batch * kv_heads * p.blocks;
     p.wide = p.blocks >= kWaves && p.units >= kFill;
     p.splits = 1;
-    if (p.wide || p.units >= kFill) return p;
+    if (p.wide || p.units >= kFill || p.units * (1 + kJoinSplits) > kCounters) return p;
     const int64_t steps = (max_kv + kTile - 1) / kTile;
     int64_t s = (kFill + p.units - 1) / p.units;
     if (s > steps / (2 * kWaves)) s = steps / (2 * kWaves);
@@ -578,17 +598,17 @@ bool valid_sizes(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, i
 const void *pick(const Plan &p, int dim) {
     if (p.wide) {
         switch (dim) {
-            case 64: return reinterpret_cast<const void *>(&k_kv4_attention_wide<64, 4>);
-            case 128: return reinterpret_cast<const void *>(&k_kv4_attention_wide<128, 4>);
+            case 64: return reinterpret_cast<const void *>(&k_kv4_attention_wide<64, 3>);
+            case 128: return reinterpret_cast<const void *>(&k_kv4_attention_wide<128, 2>);
             default: return reinterpret_cast<const void *>(&k_kv4_attention_wide<256, 1>);
         }
     }
     switch (dim) {
         case 64:
-            switch (p.tiles) { AR_NARROW(64, 1) AR_NARROW(64, 2) AR_NARROW(64, 3) AR_NARROW(64, 4) }
+            switch (p.tiles) { AR_NARROW(64, 1) AR_NARROW(64, 2) AR_NARROW(64, 3) }
             break;
         case 128:
-            switch (p.tiles) { AR_NARROW(128, 1) AR_NARROW(128, 2) AR_NARROW(128, 3) AR_NARROW(128, 4) }
+            switch (p.tiles) { AR_NARROW(128, 1) AR_NARROW(128, 2) }
             break;
         default:
             switch (p.tiles) { AR_NARROW(256, 1) }

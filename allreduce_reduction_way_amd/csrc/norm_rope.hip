@@ -283,7 +283,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_rope_grad(NormArgs a) {
         float t = part[0][c];
 #pragma unroll
         for (int i = 1; i < kWaves; ++i) t += part[i][c];
-        slot[c] = t;
+        store_shared(slot + c, t);
     }
     // groups of kJoin workgroups, then the groups: whoever comes last in a
     // group adds its slots up into the group's first, whoever comes last of
@@ -293,14 +293,16 @@ __global__ __launch_bounds__(kThreads) void k_norm_rope_grad(NormArgs a) {
     if (!arrive_last(a.counters + 1 + mine, size, &order)) return;
     float *base = a.slots + (int64_t)mine * kJoin * 2 * D;
     for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
-        float t = base[c];
-        for (int i = 1; i < size; ++i) t += base[(int64_t)i * 2 * D + c];
-        base[c] = t;
+        float t = 0;
+#pragma unroll 8
+        for (int i = 0; i < size; ++i) t += load_shared(base + (int64_t)i * 2 * D + c);
+        store_shared(base + c, t);
     }
     if (!arrive_last(a.counters, groups, &order)) return;
     for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
-        float t = a.slots[c];
-        for (int i = 1; i < groups; ++i) t += a.slots[(int64_t)i * kJoin * 2 * D + c];
+        float t = 0;
+#pragma unroll 8
+        for (int i = 0; i < groups; ++i) t += load_shared(a.slots + (int64_t)i * kJoin * 2 * D + c);
         if (c < D) {
             if (a.dwq) a.dwq[c] = t;
         } else if (a.dwk) {

@@ -379,8 +379,7 @@ int ar_kv4_read(const void *cache, const void *slots, ar_rows k_out, ar_rows v_o
  * those of j > p - window.
  *     out = sum_j softmax_j(scale q . k_j) v_j,  lse = log sum_j exp(scale q . k_j)
  * A query that sees nothing gets zeros and -infinity.  A token that a query
- * does not see adds nothing to it, whatever the cache holds there.  A query
- * row that is not finite gives NaN.
+ * does not see adds nothing to it, whatever the cache holds there.
  *   q, out      (tokens, heads, dim); query head h reads key head
  *               h / (heads / kv_heads).
  *   page_table  (batch, pages_per_seq) int32 with rows table_stride apart:
