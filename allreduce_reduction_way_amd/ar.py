@@ -353,56 +353,32 @@ def ar_packet_recv(scratch: Sequence, outputs: Sequence, flag: int, ctrl, rank_l
 
 # ------------------------------------------------ attention over a 4-bit cache
 #
-# The attention operators take tensors: their sizes and strides are read off
-# them, and every size is checked against the others before an address goes to
-# the C library.  Tensors must be on one GPU.
+# The attention operators take torch tensors: ar_tensors.so reads their sizes,
+# strides, types and devices, checks them against each other (ValueError, or
+# TypeError for what is no tensor on a GPU) and calls the C library.
 
-def _same_device(*bufs) -> None:
-    devices = {b.device for b in bufs if b is not None}
-    if len(devices) > 1:
-        raise ValueError(f"tensors on several devices: {sorted(map(str, devices))}")
+_tensors = None
 
 
-def _tensor(t, what: str, dtypes: Sequence[str], shape: tuple, contiguous: bool = True) -> None:
-    """Raises unless `t` is a tensor of one of `dtypes` and of `shape` (None: any size)."""
-    if not hasattr(t, "element_size"):
-        raise TypeError(f"{what}: expected a CUDA tensor, got {type(t).__name__}")
-    if str(t.dtype) not in dtypes:
-        raise ValueError(f"{what}: {' or '.join(dtypes)} expected, got {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{what}: shape {tuple('any' if n is None else n for n in shape)} "
-                         f"expected, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{what}: the tensor must be contiguous")
+def tensors():
+    """The loaded ar_tensors.so; raises if it has not been built."""
+    global _tensors
+    if _tensors is None:
+        lib()
+        path = LIB_PATH.with_name("ar_tensors.so")
+        if not path.exists():
+            raise ImportError(f"{path} is not built: run "
+                              "`python -c 'import __graft_entry__ as g; g.build()'`")
+        import importlib.machinery
+        import importlib.util
 
-
-def _row_tensor(t, what: str, shape: tuple) -> None:
-    _tensor(t, what, _ELEM_DTYPES, shape, contiguous=False)
-    if t.shape[2] > 1 and t.stride(2) != 1:
-        raise ValueError(f"{what}: channels must be contiguous")
-
-
-def _rows(t) -> ar_rows:
-    empty = t.numel() == 0
-    return ar_rows(0 if empty else _addr(t), t.stride(0), t.stride(1))
-
-
-def _byte_buffer(t, nbytes: int, what: str) -> None:
-    _require(t, nbytes, what)
-    if isinstance(t, int) or t is None:
-        raise TypeError(f"{what}: expected a CUDA tensor")
-
-
-def _norm_rope_args(q, k, q_weight, k_weight, cos_sin, positions):
-    _row_tensor(q, "q", (None, None, None))
-    tokens, heads, dim = q.shape
-    _row_tensor(k, "k", (tokens, None, dim))
-    _tensor(q_weight, "q_weight", _ELEM_DTYPES, (dim,))
-    _tensor(k_weight, "k_weight", _ELEM_DTYPES, (dim,))
-    _tensor(cos_sin, "cos_sin", ("torch.float32",), (None, None))
-    _tensor(positions, "positions", ("torch.int64",), (tokens,))
-    _same_device(q, k, q_weight, k_weight, cos_sin, positions)
-    return tokens, heads, k.shape[1], dim
+        import torch  # noqa: F401  (its libraries are loaded first)
+        loader = importlib.machinery.ExtensionFileLoader("ar_tensors", str(path))
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("ar_tensors", loader))
+        loader.exec_module(module)
+        _tensors = module
+    return _tensors
 
 
 def ar_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out=None, k_out=None,
@@ -410,16 +386,12 @@ def ar_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out=None, k_
     """Norms of the heads of q (tokens, heads, dim) and k (tokens, kv_heads,
     dim) with the rotation by cos_sin[positions], into q_out and k_out (in
     place where they are None)."""
-    tokens, heads, kv_heads, dim = _norm_rope_args(q, k, q_weight, k_weight, cos_sin, positions)
-    q_out = q if q_out is None else q_out
-    k_out = k if k_out is None else k_out
-    _row_tensor(q_out, "q_out", (tokens, heads, dim))
-    _row_tensor(k_out, "k_out", (tokens, kv_heads, dim))
-    _same_device(q, q_out, k_out)
-    _check(lib().ar_qk_norm_rope(_rows(q), _rows(k), _addr(q_weight), _addr(k_weight),
-                                 _addr(cos_sin), _addr(positions), _rows(q_out), _rows(k_out),
-                                 tokens, heads, kv_heads, dim, cos_sin.shape[1], cos_sin.shape[0],
-                                 eps, int(bool(interleaved)), _stream(stream)), "ar_qk_norm_rope")
+    rc = (_tensors or tensors()).qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions,
+                                              q if q_out is None else q_out,
+                                              k if k_out is None else k_out, eps,
+                                              1 if interleaved else 0, stream)
+    if rc:
+        raise ArError(rc, "ar_qk_norm_rope")
 
 
 def ar_qk_norm_rope_bwd_workspace(tokens: int, heads: int, kv_heads: int, dim: int) -> int:
@@ -433,21 +405,11 @@ def ar_qk_norm_rope_bwd(q_grad, k_grad, q, k, q_weight, k_weight, cos_sin, posit
                         interleaved: bool = False, stream=None) -> None:
     """The gradient of ar_qk_norm_rope: dq and dk from q_grad and k_grad, and
     the weights' gradients in binary32."""
-    tokens, heads, kv_heads, dim = _norm_rope_args(q, k, q_weight, k_weight, cos_sin, positions)
-    for t, what, n in ((q_grad, "q_grad", heads), (k_grad, "k_grad", kv_heads), (dq, "dq", heads),
-                       (dk, "dk", kv_heads)):
-        _row_tensor(t, what, (tokens, n, dim))
-    _tensor(dq_weight, "dq_weight", ("torch.float32",), (dim,))
-    _tensor(dk_weight, "dk_weight", ("torch.float32",), (dim,))
-    _byte_buffer(workspace, ar_qk_norm_rope_bwd_workspace(tokens, heads, kv_heads, dim), "workspace")
-    _same_device(q, q_grad, k_grad, dq, dk, dq_weight, dk_weight, workspace)
-    _check(lib().ar_qk_norm_rope_bwd(_rows(q_grad), _rows(k_grad), _rows(q), _rows(k),
-                                     _addr(q_weight), _addr(k_weight), _addr(cos_sin),
-                                     _addr(positions), _rows(dq), _rows(dk), _addr(dq_weight),
-                                     _addr(dk_weight), _addr(workspace), tokens, heads, kv_heads,
-                                     dim, cos_sin.shape[1], cos_sin.shape[0], eps,
-                                     int(bool(interleaved)), _stream(stream)),
-           "ar_qk_norm_rope_bwd")
+    rc = (_tensors or tensors()).qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions,
+                                                  q_grad, k_grad, dq, dk, dq_weight, dk_weight,
+                                                  workspace, eps, 1 if interleaved else 0, stream)
+    if rc:
+        raise ArError(rc, "ar_qk_norm_rope_bwd")
 
 
 def ar_kv4_cache_bytes(pages: int, kv_heads: int, dim: int, page_size: int) -> int:
@@ -456,35 +418,19 @@ def ar_kv4_cache_bytes(pages: int, kv_heads: int, dim: int, page_size: int) -> i
     return v
 
 
-def _kv4_cache(cache, kv_heads: int, dim: int, page_size: int) -> int:
-    """The pages of a cache tensor (pages, kv_heads, page_size / 32, 34 dim)."""
-    _tensor(cache, "cache", ("torch.uint8",), (None, kv_heads, page_size // 32, 34 * dim))
-    return cache.shape[0]
-
-
 def ar_kv4_write(k, v, slots, cache, page_size: int, stream=None) -> None:
     """Quantises the tokens of k and v (tokens, kv_heads, dim) into the slots
-    of a 4-bit cache."""
-    _row_tensor(k, "k", (None, None, None))
-    tokens, kv_heads, dim = k.shape
-    _row_tensor(v, "v", (tokens, kv_heads, dim))
-    _tensor(slots, "slots", ("torch.int64",), (tokens,))
-    pages = _kv4_cache(cache, kv_heads, dim, page_size)
-    _same_device(k, v, slots, cache)
-    _check(lib().ar_kv4_write(_rows(k), _rows(v), _addr(slots), _addr(cache), tokens, kv_heads, dim,
-                              pages, page_size, _stream(stream)), "ar_kv4_write")
+    of a 4-bit cache (pages, kv_heads, page_size / 32, 34 dim)."""
+    rc = (_tensors or tensors()).kv4_write(k, v, slots, cache, page_size, stream)
+    if rc:
+        raise ArError(rc, "ar_kv4_write")
 
 
 def ar_kv4_read(cache, slots, k_out, v_out, page_size: int, stream=None) -> None:
     """Reads the tokens of the slots of a 4-bit cache back."""
-    _row_tensor(k_out, "k_out", (None, None, None))
-    tokens, kv_heads, dim = k_out.shape
-    _row_tensor(v_out, "v_out", (tokens, kv_heads, dim))
-    _tensor(slots, "slots", ("torch.int64",), (tokens,))
-    pages = _kv4_cache(cache, kv_heads, dim, page_size)
-    _same_device(cache, slots, k_out, v_out)
-    _check(lib().ar_kv4_read(_addr(cache), _addr(slots), _rows(k_out), _rows(v_out), tokens,
-                             kv_heads, dim, pages, page_size, _stream(stream)), "ar_kv4_read")
+    rc = (_tensors or tensors()).kv4_read(k_out, v_out, slots, cache, page_size, stream)
+    if rc:
+        raise ArError(rc, "ar_kv4_read")
 
 
 def ar_kv4_attention_workspace(batch: int, tokens: int, max_q: int, max_kv: int, heads: int,
@@ -500,26 +446,11 @@ def ar_kv4_attention(q, cache, page_table, q_start, kv_len, out, lse, workspace,
     """Attention of q (tokens, heads, dim) over the 4-bit cache's pages that
     page_table (batch, pages of a sequence) names, into out and lse.  `scale`:
     dim ** -0.5 where it is None."""
-    _row_tensor(q, "q", (None, None, None))
-    tokens, heads, dim = q.shape
-    _row_tensor(out, "out", (tokens, heads, dim))
-    _tensor(lse, "lse", ("torch.float32",), (tokens, heads))
-    pages = _kv4_cache(cache, kv_heads, dim, page_size)
-    _tensor(page_table, "page_table", ("torch.int32",), (None, None), contiguous=False)
-    batch, per = page_table.shape
-    if per > 1 and page_table.stride(1) != 1:
-        raise ValueError("page_table: a sequence's entries must be contiguous")
-    _tensor(q_start, "q_start", ("torch.int32",), (batch + 1,))
-    _tensor(kv_len, "kv_len", ("torch.int32",), (batch,))
-    _byte_buffer(workspace, ar_kv4_attention_workspace(batch, tokens, max_q, max_kv, heads,
-                                                       kv_heads, dim), "workspace")
-    _same_device(q, cache, page_table, q_start, kv_len, out, lse, workspace)
-    _check(lib().ar_kv4_attention(_rows(q), _addr(cache), _addr(page_table), page_table.stride(0),
-                                  _addr(q_start), _addr(kv_len), _rows(out), _addr(lse),
-                                  _addr(workspace), tokens, batch, heads, kv_heads, dim, pages,
-                                  page_size, per, max_q, max_kv, window,
-                                  dim ** -0.5 if scale is None else scale, _stream(stream)),
-           "ar_kv4_attention")
+    rc = (_tensors or tensors()).kv4_attention(q, out, lse, cache, page_table, q_start, kv_len,
+                                               workspace, page_size, kv_heads, max_q, max_kv,
+                                               window, scale, stream)
+    if rc:
+        raise ArError(rc, "ar_kv4_attention")
 
 
 def ar_slice_range(P: int, rank: int, n: int) -> tuple:

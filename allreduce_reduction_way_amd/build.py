@@ -1,4 +1,5 @@
-"""Build libar.so: the HIP sources under csrc/ compiled for gfx950 with hipcc.
+"""Build libar.so, the HIP sources under csrc/ compiled for gfx950 with hipcc,
+and ar_tensors.so, its calls with torch tensors (host C++, gcc).
 
 Flags: -O3 for gfx950 only; packed-fp32 instructions disabled on the device
 pass (the host pass warns that it does not know the feature, which is
@@ -14,6 +15,7 @@ PKG = pathlib.Path(__file__).resolve().parent
 ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libar.so"
+TENSORS = PKG / "ar_tensors.so"
 RESOURCES = PKG / "libar.resources.txt"   # per-kernel register/scratch report of the last build
 SOURCES = ["host.hip", "reduce.hip", "packet.hip", "probe.hip", "norm_rope.hip", "kv4.hip",
            "kv4_attention.hip"]
@@ -48,6 +50,28 @@ def build(verbose: bool = False) -> pathlib.Path:
     return LIB
 
 
+def build_tensors(verbose: bool = False) -> pathlib.Path:
+    """The Python extension that takes torch tensors, linked against libar.so
+    beside it and against the installed torch."""
+    import sysconfig
+
+    import torch
+
+    root = pathlib.Path(torch.__file__).resolve().parent
+    tmp = TENSORS.with_suffix(".so.tmp")
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-Wextra",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-isystem{root / 'include'}", f"-isystem{root / 'include/torch/csrc/api/include'}",
+           f"-isystem{sysconfig.get_paths()['include']}", f"-I{ROOT / 'include'}",
+           str(CSRC / "tensors.cpp"), "-o", str(tmp), f"-L{PKG}", "-lar", f"-L{root / 'lib'}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{root / 'lib'}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    tmp.replace(TENSORS)
+    return TENSORS
+
+
 def build_c_program(src: pathlib.Path, exe: pathlib.Path, verbose: bool = False) -> pathlib.Path:
     """Compile a plain C program that calls libar.so through include/ar.h
     (gcc, C11, no HIP compiler): linked against libar.so and the HIP runtime,
@@ -66,3 +90,4 @@ def build_c_program(src: pathlib.Path, exe: pathlib.Path, verbose: bool = False)
 
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_tensors(verbose=True))
