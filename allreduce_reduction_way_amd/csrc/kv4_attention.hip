@@ -29,7 +29,6 @@
 // and join their results through LDS, several workgroups share a sequence, and
 // the last of them to arrive joins theirs.
 #include "host.h"
-#include "join.h"
 #include "kv4.h"
 #include "rows.h"
 
@@ -48,14 +47,15 @@ struct AttnArgs {
     const uint8_t *cache;
     const int32_t *table, *q_start, *kv_len;
     float *lse;
-    uint32_t *counters;
     float *part;
     int64_t table_stride;
     int tokens, batch, heads, kv_heads, group;
     int pages, per_seq, shift;  // pages of the cache, entries of a table row, log2 of tiles a page
     int window, max_q;
     int blocks;  // row blocks of a sequence's key head
-    int splits;  // workgroups that share a row block
+    int splits;  // workgroups that share a row block, at most
+    int chunk;   // tiles of such a workgroup, at least
+    int waves;   // of such a workgroup
     int vec;
     float c;  // scale log2(e)
 };
@@ -130,21 +130,24 @@ __device__ __forceinline__ bool any_nan_scale(uint32_t w) {
 }
 
 // A row tile's running result: the maximum (in units of log2) and the sum of
-// weights of row lane % 16, and its output: acc[j][i] is channel
-// (4 a + i) W + j.
+// weights of row lane % 16 (each lane's own tokens until the end of a sweep),
+// and its output: acc[j][i] is channel (4 a + i) W + j.
 template <int D>
 struct RowTile {
     static constexpr int W = Kv4<D>::W;
     float m, l;
+    f32x4 d;  // four times the same: the sum of the weights as they were rounded
     f32x4 acc[W];
 
     __device__ __forceinline__ void clear() {
         m = kNegInf, l = 0;
+        d = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < W; ++j) acc[j] = f32x4{0, 0, 0, 0};
     }
     __device__ __forceinline__ void rescale(float by) {
         l *= by;
+        d *= by;
 #pragma unroll
         for (int j = 0; j < W; ++j) acc[j] *= by;
     }
@@ -165,6 +168,10 @@ struct State {
 // taken: bf16 and binary32 lose nothing up to there, and most tiles move the
 // maximum by less, so that rescaling the output is rare.
 constexpr float kSlack = 8.0f;
+
+// Tiles that a wave of the split kernel has in its registers.
+template <int D, int R>
+constexpr int kRing = D == 64 ? 3 : 2;
 
 __device__ __forceinline__ bool sees(int pos, int token, int window) {
     return token <= pos && (window == 0 || pos - token < window);
@@ -255,6 +262,13 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, boo
             for (int i = 0; i < 2; ++i)
                 st.row[r].acc[j + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(v[i]), as_bf16(p[r]), st.row[r].acc[j + i], 0, 0, 0);
     }
+    // The output is divided by the sum of the rounded weights, so that a row
+    // that few tokens dominate keeps no error of their rounding; the matrix
+    // unit adds it up beside the output.  lse has the unrounded sum.
+    const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        st.row[r].d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(ones), as_bf16(p[r]), st.row[r].d, 0, 0, 0);
     if (nan_values) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -322,32 +336,36 @@ __device__ __forceinline__ void begin(State<D, R> &st, const AttnArgs &a, const 
     }
 }
 
-// Tiles lo, lo + by, ... below hi.  While a tile is worked on, the next one is
-// on its way; the pages of 64 tiles are looked up at once, one in each lane.
-template <int D, int R>
+// Tiles lo, lo + by, ... below hi.  While a tile is worked on, the next N - 1
+// are on their way; the pages of 64 tiles are looked up at once, one in each
+// lane.
+template <int D, int R, int N>
 __device__ __forceinline__ void sweep(State<D, R> &st, const AttnArgs &a, const Block &b, int lo, int hi, int by, int lane) {
     const int32_t *pages = a.table + (int64_t)b.seq * a.table_stride;
     for (int t = lo; t < hi; t += 64 * by) {
         const int count = min(64, (hi - t + by - 1) / by);
         const int page = pages[(t + min(lane, count - 1) * by) >> a.shift];
-        Tile<D> now, next;
-        const auto at = [&](int i, bool &known) {
+        Tile<D> ring[N];
+        bool known[N];
+        const auto load = [&](int i, int to) {
+            i = min(i, count - 1);  // past the last tile it is loaded again
             const int pg = __builtin_amdgcn_readlane(page, i);
-            known = pg >= 0 && pg < a.pages;
-            const int64_t tile = (((int64_t)(known ? pg : 0) * a.kv_heads + b.head) << a.shift) + ((t + i * by) & ((1 << a.shift) - 1));
-            return a.cache + tile * Kv4<D>::kBytes;
+            known[to] = pg >= 0 && pg < a.pages;
+            const int64_t tile = (((int64_t)(known[to] ? pg : 0) * a.kv_heads + b.head) << a.shift) + ((t + i * by) & ((1 << a.shift) - 1));
+            load_tile(ring[to], a.cache + tile * Kv4<D>::kBytes, lane);
         };
-        bool known, known_next;
-        load_tile(now, at(0, known), lane);
-        for (int i = 0; i < count; ++i) {
-            load_tile(next, at(min(i + 1, count - 1), known_next), lane);
-            const int index = t + i * by;
-            if (known) {
+#pragma unroll
+        for (int k = 0; k < N - 1; ++k) load(k, k);
+        for (int i = 0; i < count; i += N) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                if (i + k >= count) break;
+                load(i + k + N - 1, (k + N - 1) % N);
+                if (!known[k]) continue;
+                const int index = t + (i + k) * by;
                 const bool masked = index * kTile < b.seen_lo || (index + 1) * kTile > b.seen_hi;
-                step<D, R>(st, now, index, masked, a, lane);
+                step<D, R>(st, ring[k], index, masked, a, lane);
             }
-            now = next;
-            known = known_next;
         }
     }
 #pragma unroll
@@ -369,7 +387,7 @@ __device__ __forceinline__ void finish(const RowTile<D> &o, const AttnArgs &a, c
     if (row >= b.rows) return;
     const int i = row / a.group, h = b.head * a.group + row % a.group;
     const int64_t token = b.q0 + i;
-    const float inv = o.l == 0 ? 0.0f : 1.0f / o.l;
+    const float inv = o.d[0] == 0 ? 0.0f : 1.0f / o.d[0];
     uint16_t *p = const_cast<uint16_t *>(a.out.p) + token * a.out.ts + (int64_t)h * a.out.hs + lane / 16 * (4 * W);
 #pragma unroll
     for (int k = 0; k < W / 2; ++k) {  // eight channels each
@@ -385,65 +403,67 @@ __device__ __forceinline__ void finish(const RowTile<D> &o, const AttnArgs &a, c
     if (lane < 16) a.lse[token * a.heads + h] = log_sum(o.m, o.l);
 }
 
-constexpr int kJoinSplits = 16;  // results that one workgroup joins
-
-// Joins `count` results that lie `stride` floats apart: into the output (LAST),
-// or into the first of them.  A wave takes pairs of channels of all rows.
-template <int D, int R, bool LAST>
-__device__ __forceinline__ void join(float *base, int64_t stride, int count, const AttnArgs &a, const Block &b, float *lds, int lane, int wave) {
-    constexpr int W = Kv4<D>::W, kStats = R * W * 256;
-    float *ms = lds, *ls = lds + kJoinSplits * 16;
-    static_assert(kJoinSplits * 32 <= kWaves / 2 * W * 256, "the maxima and sums fit the exchange memory");
-    for (int r = 0; r < R; ++r) {
-        if (b.first + r * 16 >= b.rows) break;
-        __syncthreads();
-        for (int i = threadIdx.x; i < count * 16; i += kThreads) {
-            const float *p = base + i / 16 * stride + kStats + r * 32 + i % 16;
-            const bool used = b.first + r * 16 + i % 16 < b.rows;
-            ms[i] = used ? load_shared(p) : kNegInf;
-            ls[i] = used ? load_shared(p + 16) : 0.0f;
-        }
-        __syncthreads();
-        const int row = b.first + r * 16 + lane % 16;
-        float m = kNegInf, l = 0;
-        for (int s = 0; s < count; ++s) m = fmaxf(m, ms[s * 16 + lane % 16]);
-        for (int s = 0; s < count; ++s) l += ls[s * 16 + lane % 16] * RowTile<D>::weight(ms[s * 16 + lane % 16], m);
-        if (row >= b.rows) continue;
-        for (int j = wave * 2; j < W; j += kWaves * 2) {
-            float *p = base + ((r * W + j) * 64 + lane) * 4;
-            f32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-#pragma unroll 8
-            for (int s = 0; s < count; ++s) {
-                const float w = RowTile<D>::weight(ms[s * 16 + lane % 16], m);
-                sum[0] += load_shared4(p + s * stride) * w;
-                sum[1] += load_shared4(p + s * stride + 256) * w;
-            }
-            if (LAST) {
-                const int i = row / a.group, h = b.head * a.group + row % a.group;
-                const float inv = l == 0 ? 0.0f : 1.0f / l;
-                uint16_t *o = const_cast<uint16_t *>(a.out.p) + (int64_t)(b.q0 + i) * a.out.ts + (int64_t)h * a.out.hs + lane / 16 * (4 * W) + j;
+// Where a row's output goes: channels j and j + 1 of each of the lane's four
+// runs of W, and the row's lse.
+template <int D>
+__device__ __forceinline__ void put_pair(const AttnArgs &a, const Block &b, int r, int j, const f32x4 (&sum)[2], float m, float l, float d, int lane) {
+    constexpr int W = Kv4<D>::W;
+    const int row = b.first + r * 16 + lane % 16;
+    if (row >= b.rows) return;
+    const int i = row / a.group, h = b.head * a.group + row % a.group;
+    const float inv = d == 0 ? 0.0f : 1.0f / d;
+    uint16_t *o = const_cast<uint16_t *>(a.out.p) + (int64_t)(b.q0 + i) * a.out.ts + (int64_t)h * a.out.hs + lane / 16 * (4 * W) + j;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t w = pack_bf16x2(sum[0][e] * inv, sum[1][e] * inv);
-                    if (a.vec) {
-                        *reinterpret_cast<uint32_t *>(o + e * W) = w;
-                    } else {
-                        o[e * W] = (uint16_t)w;
-                        o[e * W + 1] = (uint16_t)(w >> 16);
-                    }
-                }
-                if (wave == 0 && j == 0 && lane < 16) a.lse[(int64_t)(b.q0 + i) * a.heads + h] = log_sum(m, l);
-            } else {
-                store_shared(p, sum[0]);
-                store_shared(p + 256, sum[1]);
-                if (wave == 0 && j == 0 && lane < 16) {
-                    store_shared(base + kStats + r * 32 + lane, m);
-                    store_shared(base + kStats + r * 32 + 16 + lane, l);
-                }
-            }
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t w = pack_bf16x2(sum[0][e] * inv, sum[1][e] * inv);
+        if (a.vec) {
+            *reinterpret_cast<uint32_t *>(o + e * W) = w;
+        } else {
+            o[e * W] = (uint16_t)w;
+            o[e * W + 1] = (uint16_t)(w >> 16);
         }
     }
+    if (j == 0 && lane < 16) a.lse[(int64_t)(b.q0 + i) * a.heads + h] = log_sum(m, l);
 }
+
+// Results that the waves of a workgroup leave in LDS, and joins there: a wave
+// takes pairs of channels of a row tile.
+template <int D, int R, int NW>
+struct Exchange {
+    static constexpr int W = Kv4<D>::W;
+    f32x4 acc[NW][R][W][64];
+    float m[NW][R][16], l[NW][R][16], d[NW][R][16];
+
+    __device__ __forceinline__ void leave(const RowTile<D> (&row)[R], int lane, int wave) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) acc[wave][r][j][lane] = row[r].acc[j];
+            if (lane < 16) m[wave][r][lane] = row[r].m, l[wave][r][lane] = row[r].l, d[wave][r][lane] = row[r].d[0];
+        }
+        __syncthreads();
+    }
+    template <typename Put>
+    __device__ __forceinline__ void join(int rows, int lane, int wave, Put put) const {
+        for (int item = wave; item < R * W / 2; item += NW) {
+            const int r = item / (W / 2), j = item % (W / 2) * 2, row = lane % 16;
+            if (r * 16 + row >= rows) continue;
+            float all = kNegInf, ls = 0, ds = 0;
+#pragma unroll
+            for (int s = 0; s < NW; ++s) all = fmaxf(all, m[s][r][row]);
+            f32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+            for (int s = 0; s < NW; ++s) {
+                const float w = RowTile<D>::weight(m[s][r][row], all);
+                ls += l[s][r][row] * w;
+                ds += d[s][r][row] * w;
+                sum[0] += acc[s][r][j][lane] * w;
+                sum[1] += acc[s][r][j + 1][lane] * w;
+            }
+            put(r, j, sum, all, ls, ds);
+        }
+    }
+};
 
 // Many rows: every wave has a row block of its own and sweeps all its tiles.
 template <int D, int R>
@@ -456,133 +476,194 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
     if (block >= a.blocks || !locate(b, a, unit % a.batch, unit / a.batch, block, 16 * R)) return;
     State<D, R> st;
     begin(st, a, b, lane);
-    sweep(st, a, b, b.lo, b.hi, 1, lane);
+    sweep<D, R, 2>(st, a, b, b.lo, b.hi, 1, lane);
 #pragma unroll
     for (int r = 0; r < R; ++r) finish(st.row[r], a, b, r, lane);
 }
 
-// Few rows: the waves of a workgroup share a row block.
+// How the tiles of a block are shared by workgroups: equal ranges, none shorter
+// than a tile for each wave.  At most a.splits ranges, and at least one.
+__device__ __forceinline__ int ranges(const AttnArgs &a, const Block &b, int waves, int &chunk) {
+    const int tiles = b.hi - b.lo;
+    chunk = max(max(waves, a.chunk), (tiles + a.splits - 1) / a.splits);
+    return max(1, (tiles + chunk - 1) / chunk);
+}
+
+// A range's result in the workspace: R W vectors as the lanes hold them, then
+// the statistics.
 template <int D, int R>
-__global__ __launch_bounds__(kThreads, 2) void k_kv4_attention(AttnArgs a) {
-    constexpr int W = Kv4<D>::W;
-    __shared__ f32x4 acc[kWaves / 2][R][W][64];
-    __shared__ float ml[kWaves / 2][R][2][16];
-    __shared__ uint32_t order;
+struct Part {
+    static constexpr int W = Kv4<D>::W, kStats = R * W * 256, kFloats = kStats + R * 48;
+};
+
+// Few rows: the NW waves of a workgroup share a row block, and several
+// workgroups do.
+template <int D, int R, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_kv4_attention(AttnArgs a) {
+    using P = Part<D, R>;
+    __shared__ Exchange<D, R, NW> ex;
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int split = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
     const int pair = unit / a.blocks;
     Block b;
     if (!locate(b, a, pair / a.kv_heads, pair % a.kv_heads, unit % a.blocks, 16 * R)) return;
-    // the tiles in equal ranges, none shorter than a tile for each wave
-    const int tiles = b.hi - b.lo;
-    const int chunk = max(kWaves, (tiles + a.splits - 1) / a.splits);
-    const int count = max(1, (tiles + chunk - 1) / chunk);
+    int chunk;
+    const int count = ranges(a, b, NW, chunk);
     if (split >= count) return;
-    State<D, R> st;
-    begin(st, a, b, lane);
-    const int lo = b.lo + split * chunk;
-    sweep(st, a, b, lo + wave, min(b.hi, lo + chunk), kWaves, lane);
-
-    // the upper half of the waves hands its results to the lower half
-#pragma unroll
-    for (int half = kWaves / 2; half > 0; half /= 2) {
-        if (wave >= half && wave < 2 * half) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-#pragma unroll
-                for (int j = 0; j < W; ++j) acc[wave - half][r][j][lane] = st.row[r].acc[j];
-                if (lane < 16) ml[wave - half][r][0][lane] = st.row[r].m, ml[wave - half][r][1][lane] = st.row[r].l;
-            }
-        }
-        __syncthreads();
-        if (wave < half) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                RowTile<D> &o = st.row[r];
-                const float m2 = ml[wave][r][0][lane % 16], l2 = ml[wave][r][1][lane % 16];
-                const float m = fmaxf(o.m, m2), w1 = o.weight(o.m, m), w2 = o.weight(m2, m);
-                o.m = m;
-                o.l = o.l * w1 + l2 * w2;
-#pragma unroll
-                for (int j = 0; j < W; ++j) o.acc[j] = o.acc[j] * w1 + acc[wave][r][j][lane] * w2;
-            }
-        }
-        __syncthreads();
+    {
+        State<D, R> st;
+        begin(st, a, b, lane);
+        const int lo = b.lo + split * chunk;
+        sweep<D, R, kRing<D, R>>(st, a, b, lo + wave, min(b.hi, lo + chunk), NW, lane);
+        ex.leave(st.row, lane, wave);
     }
+    const int rows = min(b.rows - b.first, 16 * R);
     if (count == 1) {
-        if (wave == 0) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) finish(st.row[r], a, b, r, lane);
-        }
+        ex.join(rows, lane, wave, [&](int r, int j, const f32x4(&sum)[2], float m, float l, float d) {
+            put_pair<D>(a, b, r, j, sum, m, l, d, lane);
+        });
         return;
     }
+    float *to = a.part + ((int64_t)unit * a.splits + split) * P::kFloats;
+    ex.join(rows, lane, wave, [&](int r, int j, const f32x4(&sum)[2], float m, float l, float d) {
+        f32x4 *v = reinterpret_cast<f32x4 *>(to) + (r * P::W + j) * 64 + lane;
+        v[0] = sum[0];
+        v[64] = sum[1];
+        float *p = to + P::kStats + r * 48 + lane;
+        if (j == 0 && lane < 16) p[0] = m, p[16] = l, p[32] = d;
+    });
+}
 
-    // A split's result: R W vectors as the lanes hold them, then maxima and
-    // sums.  Up to kJoinSplits of them are joined at once; more, in two levels.
-    constexpr int kPart = R * W * 256 + R * 32;
-    float *base = a.part + (int64_t)unit * a.splits * kPart;
-    uint32_t *counter = a.counters + unit * (1 + kJoinSplits);
-    if (wave == 0) {
-        float *p = base + (int64_t)split * kPart;
+// Joins the ranges of a row block: four channels of sixteen rows are an item of
+// one wave, or of the four of a workgroup.  Each sixteen lanes take a range of
+// their own, and a wave has 4 kBatch ranges in flight.  A launch of its own:
+// with the last workgroup to arrive joining them, stores that have to reach the
+// coherence point, an atomic and loads from there followed one another, twice
+// for 256 ranges, and took 10 us where this takes 4.6.
+template <int D, int R, int kBatch, int NW>
+__global__ __launch_bounds__(256) void k_kv4_join(AttnArgs a) {
+    using P = Part<D, R>;
+    constexpr int kItems = R * P::W * 4;  // of a row block
+    __shared__ f32x4 acc[NW][16];
+    __shared__ float stats[NW][3][16];
+    const int lane = threadIdx.x % 64, wave = NW > 1 ? uniform(threadIdx.x / 64) : 0, row = lane % 16;
+    const int id = NW > 1 ? blockIdx.x : blockIdx.x * 4 + uniform(threadIdx.x / 64);
+    const int item = id % kItems, unit = id / kItems;  // kItems is a multiple of 4
+    const int pair = unit / a.blocks, block = unit % a.blocks, r = item / (P::W * 4), j = item / 4 % P::W, q = item % 4;
+    const float *base = a.part + (int64_t)unit * a.splits * P::kFloats;
+    const int s0 = wave * 4 + lane / 16;
+    f32x4 v[kBatch];
+    float m[kBatch], l[kBatch], d[kBatch];
+    // on their way while the block is looked up; ranges past the last that
+    // there may be repeat it, and rows that no sequence has are left out
+    if ((block * R + r) * 16 + row < a.max_q * a.group) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (b.first + r * 16 + lane % 16 < b.rows) {
+        for (int k = 0; k < kBatch; ++k) {
+            const float *p = base + (int64_t)min(s0 + k * (NW * 4), a.splits - 1) * P::kFloats;
+            v[k] = reinterpret_cast<const f32x4 *>(p)[(r * P::W + j) * 64 + q * 16 + row];
+            const float *t = p + P::kStats + r * 48 + row;
+            m[k] = t[0], l[k] = t[16], d[k] = t[32];
+        }
+    }
+    Block b;
+    if (!locate(b, a, pair / a.kv_heads, pair % a.kv_heads, block, 16 * R)) return;
+    int chunk;
+    const int count = ranges(a, b, a.waves, chunk);
+    if (count == 1) return;
+    const bool used = b.first + r * 16 + row < b.rows;
+    float top = kNegInf, ls = 0, ds = 0;
+    f32x4 sum = {0, 0, 0, 0};
+    if (used) {
 #pragma unroll
-                for (int j = 0; j < W; ++j) store_shared(p + ((r * W + j) * 64 + lane) * 4, st.row[r].acc[j]);
-                if (lane < 16) {
-                    store_shared(p + R * W * 256 + r * 32 + lane, st.row[r].m);
-                    store_shared(p + R * W * 256 + r * 32 + 16 + lane, st.row[r].l);
-                }
+        for (int k = 0; k < kBatch; ++k)
+            if (s0 + k * (NW * 4) < count) top = fmaxf(top, m[k]);
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if (used) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (s0 + k * (NW * 4) < count) {  // the rest is memory that nothing was written to
+                const float w = RowTile<D>::weight(m[k], top);
+                ls += l[k] * w;
+                ds += d[k] * w;
+                sum += v[k] * w;
             }
         }
     }
-    const int groups = (count + kJoinSplits - 1) / kJoinSplits;
-    float *scratch = reinterpret_cast<float *>(&acc[0][0][0][0]);
-    if (groups > 1) {
-        const int g = split / kJoinSplits;
-        const int size = min(kJoinSplits, count - g * kJoinSplits);
-        if (!arrive_last(counter + 1 + g, size, &order)) return;
-        float *p = base + (int64_t)g * kJoinSplits * kPart;
-        join<D, R, false>(p, kPart, size, a, b, scratch, lane, wave);
-        if (!arrive_last(counter, groups, &order)) return;
-        join<D, R, true>(base, (int64_t)kJoinSplits * kPart, groups, a, b, scratch, lane, wave);
-    } else {
-        if (!arrive_last(counter, count, &order)) return;
-        join<D, R, true>(base, kPart, count, a, b, scratch, lane, wave);
+#pragma unroll
+    for (int x = 16; x < 64; x *= 2) {
+        ls += __shfl_xor(ls, x);
+        ds += __shfl_xor(ds, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += __shfl_xor(sum[e], x);
     }
+    if (NW > 1) {
+        if (lane < 16) acc[wave][row] = sum, stats[wave][0][row] = top, stats[wave][1][row] = ls, stats[wave][2][row] = ds;
+        __syncthreads();
+        top = kNegInf, ls = ds = 0;
+        sum = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < NW; ++s) top = fmaxf(top, stats[s][0][row]);
+#pragma unroll
+        for (int s = 0; s < NW; ++s) {
+            const float w = RowTile<D>::weight(stats[s][0][row], top);
+            ls += stats[s][1][row] * w;
+            ds += stats[s][2][row] * w;
+            sum += acc[s][row] * w;
+        }
+    }
+    if (wave > 0 || lane >= 16 || !used) return;
+    const int at = b.first + r * 16 + row, i = at / a.group, h = b.head * a.group + at % a.group;
+    const float inv = ds == 0 ? 0.0f : 1.0f / ds;
+    uint16_t *o = const_cast<uint16_t *>(a.out.p) + (int64_t)(b.q0 + i) * a.out.ts + (int64_t)h * a.out.hs + q * (4 * P::W) + j;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e * P::W] = (uint16_t)bf16_rne(sum[e] * inv);
+    if (j == 0 && q == 0) a.lse[(int64_t)(b.q0 + i) * a.heads + h] = log_sum(top, ls);
 }
 
-constexpr int kCounters = 16384;  // counters at the start of the workspace
-constexpr int kSplits = kJoinSplits * kJoinSplits;  // workgroups that share a row block, at most
-constexpr int kFill = 1024;       // workgroups that fill the device: four on each compute unit
-
+constexpr int kCus = 256;
+constexpr int kLong = 8;
+constexpr int kSplits = 256;  // workgroups that share a row block, at most
 // How a call is laid out, by its sizes alone.
 struct Plan {
     bool wide;
     int tiles;  // row tiles of a wave
-    int blocks, splits;
+    int waves;  // of a workgroup
+    int blocks, splits, chunk;
     int64_t units;
 };
 
-Plan plan(int batch, int max_q, int64_t max_kv, int group, int kv_heads, int dim) {
+Plan plan(int batch, int max_q, int64_t max_kv, int64_t window, int group, int kv_heads, int dim) {
     Plan p = {};
     const int64_t rows = (int64_t)max_q * group, tiles = (rows + 15) / 16;
     const int most = dim == 64 ? 3 : dim == 128 ? 2 : 1;
     p.tiles = (int)(tiles < most ? tiles : most);
     p.blocks = (int)((tiles + p.tiles - 1) / p.tiles);
     p.units = (int64_t)batch * kv_heads * p.blocks;
-    p.wide = p.blocks >= kWaves && p.units >= kFill;
-    p.splits = 1;
-    if (p.wide || p.units >= kFill || p.units * (1 + kJoinSplits) > kCounters) return p;
+    p.wide = p.blocks >= kWaves && p.units >= 1024;
+    p.splits = p.chunk = 1;
+    p.waves = kWaves;
+    if (p.wide) return p;
+    if (window && max_kv > window + max_q) max_kv = window + max_q;
     const int64_t steps = (max_kv + kTile - 1) / kTile;
-    int64_t s = (kFill + p.units - 1) / p.units;
-    if (s > steps / (2 * kWaves)) s = steps / (2 * kWaves);
+    const bool few = p.units < 2 * kCus;
+    p.waves = few ? 2 * kWaves : kWaves;
+    const int64_t fill = (few ? 1 : 3) * kCus;  // workgroups that the device runs at once
+    // one round of workgroups while there is a tile for each wave, and up to
+    // four, which even out ragged lengths, while each wave has kLong tiles
+    int64_t s = fill / p.units;
+    if (s > steps / p.waves) s = steps / p.waves;
+    int64_t more = !few ? 1 : (4 * fill + p.units - 1) / p.units;
+    if (more > steps / (p.waves * kLong)) more = steps / (p.waves * kLong);
+    if (s < more) s = more;
     if (s > kSplits) s = kSplits;
     p.splits = s < 1 ? 1 : (int)s;
+    p.chunk = (int)((steps + p.splits - 1) / p.splits);
     return p;
 }
 
-int64_t part_floats(const Plan &p, int dim) { return (int64_t)p.tiles * (dim / 16 * 256 + 32); }
+int64_t part_floats(const Plan &p, int dim) { return (int64_t)p.tiles * (dim / 16 * 256 + 48); }
 
 bool valid_sizes(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, int heads, int kv_heads, int dim) {
     return batch >= 0 && batch <= 1 << 20 && tokens >= 0 && tokens <= 1 << 28 && max_q >= 0 &&
@@ -592,28 +673,33 @@ bool valid_sizes(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, i
            (dim == 64 || dim == 128 || dim == 256);
 }
 
-#define AR_NARROW(D_, R_) \
-    case R_: return reinterpret_cast<const void *>(&k_kv4_attention<D_, R_>);
+// The kernel of a call, and the one that joins its ranges.
+struct Kernels {
+    const void *main, *join;
+    int items;  // workgroups of the second for each row block
+};
 
-const void *pick(const Plan &p, int dim) {
-    if (p.wide) {
-        switch (dim) {
-            case 64: return reinterpret_cast<const void *>(&k_kv4_attention_wide<64, 3>);
-            case 128: return reinterpret_cast<const void *>(&k_kv4_attention_wide<128, 2>);
-            default: return reinterpret_cast<const void *>(&k_kv4_attention_wide<256, 1>);
-        }
+template <int D, int R>
+Kernels pick_rows(const Plan &p) {
+    const int items = p.splits <= 64 ? R * Kv4<D>::W : R * Kv4<D>::W * 4;
+    const void *join = p.splits <= 4    ? reinterpret_cast<const void *>(&k_kv4_join<D, R, 1, 1>)
+                       : p.splits <= 16 ? reinterpret_cast<const void *>(&k_kv4_join<D, R, 4, 1>)
+                       : p.splits <= 64 ? reinterpret_cast<const void *>(&k_kv4_join<D, R, 16, 1>)
+                                        : reinterpret_cast<const void *>(&k_kv4_join<D, R, 16, 4>);
+    if (p.wide) return {reinterpret_cast<const void *>(&k_kv4_attention_wide<D, R>), join, items};
+    if (p.waves == kWaves) return {reinterpret_cast<const void *>(&k_kv4_attention<D, R, kWaves>), join, items};
+    return {reinterpret_cast<const void *>(&k_kv4_attention<D, R, 2 * kWaves>), join, items};
+}
+
+Kernels pick(const Plan &p, int dim) {
+    switch (dim * 4 + p.tiles) {
+        case 64 * 4 + 1: return pick_rows<64, 1>(p);
+        case 64 * 4 + 2: return pick_rows<64, 2>(p);
+        case 64 * 4 + 3: return pick_rows<64, 3>(p);
+        case 128 * 4 + 1: return pick_rows<128, 1>(p);
+        case 128 * 4 + 2: return pick_rows<128, 2>(p);
+        default: return pick_rows<256, 1>(p);
     }
-    switch (dim) {
-        case 64:
-            switch (p.tiles) { AR_NARROW(64, 1) AR_NARROW(64, 2) AR_NARROW(64, 3) }
-            break;
-        case 128:
-            switch (p.tiles) { AR_NARROW(128, 1) AR_NARROW(128, 2) }
-            break;
-        default:
-            switch (p.tiles) { AR_NARROW(256, 1) }
-    }
-    return nullptr;
 }
 
 }  // namespace
@@ -626,9 +712,9 @@ extern "C" {
 int64_t ar_kv4_attention_workspace(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv,
                                    int heads, int kv_heads, int dim) {
     if (!valid_sizes(batch, tokens, max_q, max_kv, heads, kv_heads, dim)) return AR_EINVAL;
-    if (batch == 0 || max_q == 0) return 4 * kCounters;
-    const Plan p = plan((int)batch, (int)max_q, max_kv, heads / kv_heads, kv_heads, dim);
-    return 4 * kCounters + (p.splits > 1 ? p.units * p.splits * part_floats(p, dim) * 4 : 0);
+    if (batch == 0 || max_q == 0) return 16;
+    const Plan p = plan((int)batch, (int)max_q, max_kv, 0, heads / kv_heads, kv_heads, dim);
+    return p.splits > 1 ? p.units * p.splits * part_floats(p, dim) * 4 : 16;
 }
 
 int ar_kv4_attention(ar_rows q, const void *cache, const void *page_table, int64_t table_stride,
@@ -664,26 +750,28 @@ int ar_kv4_attention(ar_rows q, const void *cache, const void *page_table, int64
         for (int j = i + 1; j < 3; ++j)
             if (overlap(writes[i], writes[j])) return AR_EALIAS;
     }
-    const Plan p = plan((int)batch, (int)max_q, max_kv, heads / kv_heads, kv_heads, dim);
+    const Plan p = plan((int)batch, (int)max_q, max_kv, window, heads / kv_heads, kv_heads, dim);
     AttnArgs a = {};
     a.q = rows(rq), a.out = rows(ro);
     a.cache = static_cast<const uint8_t *>(cache);
     a.table = static_cast<const int32_t *>(page_table);
     a.q_start = static_cast<const int32_t *>(q_start), a.kv_len = static_cast<const int32_t *>(kv_len);
     a.lse = static_cast<float *>(lse);
-    a.counters = static_cast<uint32_t *>(workspace);
-    a.part = reinterpret_cast<float *>(a.counters + kCounters);
+    a.part = static_cast<float *>(workspace);
     a.table_stride = table_stride;
     a.tokens = (int)tokens, a.batch = (int)batch, a.heads = heads, a.kv_heads = kv_heads, a.group = heads / kv_heads;
     a.pages = (int)pages, a.per_seq = pages ? (int)pages_per_seq : 0, a.shift = shift - 5;
     a.window = (int)window, a.max_q = (int)max_q;
-    a.blocks = p.blocks, a.splits = p.splits;
+    a.blocks = p.blocks, a.splits = p.splits, a.chunk = p.chunk, a.waves = p.waves;
     a.vec = rq.vec() && ro.vec();
     a.c = scale * kLog2e;
     const int64_t pairs = batch * kv_heads;
     const int64_t grid = p.wide ? pairs * ((p.blocks + kWaves - 1) / kWaves) : pairs * p.blocks * p.splits;
-    if (grid > 0x7FFFFFFF / kThreads) return AR_EINVAL;
-    return launch(pick(p, dim), (unsigned)grid, kThreads, a, stream);
+    if (grid > 0x7FFFFFFF / (64 * p.waves)) return AR_EINVAL;
+    const Kernels k = pick(p, dim);
+    const int rc = launch(k.main, (unsigned)grid, 64 * p.waves, a, stream);
+    if (rc != AR_OK || p.splits == 1) return rc;
+    return launch(k.join, (unsigned)(p.units * k.items), 256, a, stream);
 }
 
 }  // extern "C"

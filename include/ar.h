@@ -388,10 +388,8 @@ int ar_kv4_read(const void *cache, const void *slots, ar_rows k_out, ar_rows v_o
  *               are not seen.  Entries past a sequence's tokens are not read.
  *   q_start     batch + 1 int32, rising; kv_len batch int32.
  *   lse         (tokens, heads) floats.
- *   workspace   ar_kv4_attention_workspace bytes, zeroed once; every call
- *               leaves it fit for the next, of any sizes that it is large
- *               enough for.  Two calls in flight on one workspace are not
- *               allowed.
+ *   workspace   ar_kv4_attention_workspace bytes of any contents.  Two calls
+ *               in flight on one workspace are not allowed.
  *   max_q       at least the largest number of queries of a sequence (those
  *               past it get no output); max_kv the largest kv_len, or any
  *               bound on it: it only says how the work is split.
