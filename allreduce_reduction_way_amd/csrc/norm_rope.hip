@@ -18,16 +18,16 @@
 // token share the wave's cosines and sines, so a wave stays on one token and
 // takes several steps of rows.
 #include "host.h"
-#include "join.h"
 #include "rows.h"
 
 namespace ar {
 namespace {
 
 constexpr int kMaxHeads = 1 << 16;
-constexpr int kSteps = 4;      // steps of rows that a wave has in flight, forward
-constexpr int kGradSteps = 2;  // the same backwards (two loads a row)
-
+// Above this many bytes, rows are read and written past the caches (as the
+// reduce kernels do): 268 MB forward take 53.8 us with it, 57.7 without, and
+// 226 MB backwards 49.9 and 53.9; 0.5 to 12 MB take up to 0.7 us longer.
+constexpr int64_t kStreamBytes = (int64_t)128 << 20;
 struct NormArgs {
     Rows q, k, gq, gk, oq, ok;  // gq, gk: incoming gradients (backwards only)
     const uint16_t *wq, *wk;
@@ -35,11 +35,11 @@ struct NormArgs {
     const int64_t *pos;
     float *dwq, *dwk;  // backwards only
     float *slots;      // backwards: partial sums of dw, 2 D floats for each workgroup
-    uint32_t *counters;
     int64_t tokens, table;
-    int hq, heads;  // query heads, and query + key heads
+    int hq, hk;  // query heads and key heads
     int rotated, interleaved;
-    int steps, parts;  // steps of rows a token takes; waves that share a token (forward)
+    int qsteps, steps, per, parts;  // steps of rows: of a token's queries, of it all, of a wave; waves that share a token
+    int blocks;             // backwards: workgroups, each with a slot
     float eps;
 };
 
@@ -86,7 +86,9 @@ struct Turn {
         within = a.interleaved != 0;
         mate = within || !turns ? lane : li < half ? lane + half : lane - half;
     }
-    __device__ __forceinline__ void load(const NormArgs &a, int lane, const float *row) {
+    __device__ __forceinline__ void load(const NormArgs &a, int lane, int64_t pos) {
+        const bool known = pos >= 0 && pos < a.table;
+        const float *row = a.cs + (known ? pos : 0) * a.rotated;
         constexpr int kLanes = D / 8;
         const int li = lane % kLanes, half = a.rotated / 16;
         if (within) {
@@ -110,161 +112,188 @@ struct Turn {
                 }
             }
         }
+        if (!known) {  // NaN rows
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c[e] = __uint_as_float(0x7FC00000u);
+        }
     }
-    // The words of the mates of a lane's four words.
+    // The words of the mates of a lane's four words; zeros where it does not
+    // turn.
     __device__ __forceinline__ u32x4 mates(u32x4 v) const {
         u32x4 r;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            r[i] = within ? (v[i] >> 16) | (v[i] << 16) : (uint32_t)__shfl((int)v[i], mate);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = within ? (v[i] >> 16) | (v[i] << 16) : (uint32_t)__shfl((int)v[i], mate);
+            r[i] = turns ? w : 0;
+        }
         return r;
     }
 };
 
-template <int D, bool VEC>
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    bf16x2 r;
+    r[0] = (__bf16)lo;
+    r[1] = (__bf16)hi;
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A token's rows of queries, or of keys, and its steps [begin, end) that a
+// wave takes: a step is kRows heads.
+struct Share {
+    const uint16_t *x;
+    uint16_t *out;
+    const uint16_t *w;
+    int64_t in_hs, out_hs;
+    int heads, begin, end;
+};
+
+// VEC and NT: 16-byte accesses, non-temporal ones.
+template <bool VEC, bool NT>
+__device__ __forceinline__ u32x4 load_row(const uint16_t *p) {
+    return NT ? __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p)) : load8<VEC>(p);
+}
+
+template <bool VEC, bool NT>
+__device__ __forceinline__ void store_row(uint16_t *p, u32x4 v) {
+    if (NT) __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
+    else store8<VEC>(p, v);
+}
+
+// U: steps of rows that a wave has in flight.  A step is of queries or of
+// keys, so that all that depends on that is the same in a wave's lanes, and
+// the weights are multiplied into the cosines and sines once.
+template <int D, bool VEC, int U, bool NT>
 __global__ __launch_bounds__(kThreads) void k_norm_rope(NormArgs a) {
     constexpr int kLanes = D / 8, kRows = 64 / kLanes;
     const int lane = threadIdx.x % 64, li = lane % kLanes;
-    const int64_t item = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+    const int item = uniform(blockIdx.x * (kThreads / 64) + threadIdx.x / 64);
     const int64_t token = item / a.parts;
     if (token >= a.tokens) return;
-    const int first = (int)(item % a.parts) * kSteps;
-
-    u32x4 x[kSteps];
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-        const int h = (first + u) * kRows + lane / kLanes;
-        if (h < a.heads) {
-            const bool isq = h < a.hq;
-            const uint16_t *p = isq ? a.q.p + token * a.q.ts + h * a.q.hs
-                                    : a.k.p + token * a.k.ts + (h - a.hq) * a.k.hs;
-            x[u] = load8<VEC>(p + li * 8);
-        } else {
-            x[u] = u32x4{0, 0, 0, 0};
-        }
-    }
-    Turn<D, VEC> turn;
-    turn.place(a, lane);
+    const int begin = item % a.parts * a.per, end = min(begin + a.per, a.steps);
     const int64_t pos = a.pos[token];
-    const bool known = pos >= 0 && pos < a.table;
-    turn.load(a, lane, a.cs + (known ? pos : 0) * a.rotated);
-    u32x4 wq = {0, 0, 0, 0}, wk = {0, 0, 0, 0};
-    if (a.hq > 0) wq = load8<VEC>(a.wq + li * 8);
-    if (a.heads > a.hq) wk = load8<VEC>(a.wk + li * 8);
-    const u32x4 wqm = turn.mates(wq), wkm = turn.mates(wk);
-
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-        const int h = (first + u) * kRows + lane / kLanes;
-        const bool isq = h < a.hq;
-        const u32x4 xm = turn.mates(x[u]);
-        float f[8], m[8], w[8], wm[8];
-        widen(x[u], f);
-        widen(xm, m);
-        widen(isq ? wq : wk, w);
-        widen(isq ? wqm : wkm, wm);
-        float ss = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
-        const float r = rsqrtf(row_sum<kLanes>(ss) * (1.0f / D) + a.eps);
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float z = f[e] * r * w[e];
-            const float t = z * turn.c[e] + m[e] * r * wm[e] * turn.s[e];
-            y[e] = !known ? __uint_as_float(0x7FC00000u) : turn.turns ? t : z;
-        }
-        if (h < a.heads) {
-            uint16_t *p = const_cast<uint16_t *>(isq ? a.oq.p + token * a.oq.ts + h * a.oq.hs
-                                                     : a.ok.p + token * a.ok.ts + (h - a.hq) * a.ok.hs);
-            u32x4 o;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
-            store8<VEC>(p + li * 8, o);
-        }
-    }
-}
-
-// Backwards.  Each lane keeps the sums of g n of its channels over all rows
-// that it meets (binary32; rows, lanes, waves, workgroups and groups of
-// workgroups are joined as a tree in a fixed order, so the sums do not depend
-// on which workgroup ends last).
-template <int D, bool VEC>
-__global__ __launch_bounds__(kThreads) void k_norm_rope_grad(NormArgs a) {
-    constexpr int kLanes = D / 8, kRows = 64 / kLanes, kWaves = kThreads / 64;
-    const int lane = threadIdx.x % 64, li = lane % kLanes, wave = threadIdx.x / 64;
     Turn<D, VEC> turn;
     turn.place(a, lane);
-    u32x4 wq = {0, 0, 0, 0}, wk = {0, 0, 0, 0};
-    if (a.tokens > 0 && a.hq > 0) wq = load8<VEC>(a.wq + li * 8);
-    if (a.tokens > 0 && a.heads > a.hq) wk = load8<VEC>(a.wk + li * 8);
-    float dq[8] = {}, dk[8] = {};
 
-    for (int64_t token = (int64_t)blockIdx.x * kWaves + wave; token < a.tokens;
-         token += (int64_t)gridDim.x * kWaves) {
-        const int64_t pos = a.pos[token];
-        const bool known = pos >= 0 && pos < a.table;
-        turn.load(a, lane, a.cs + (known ? pos : 0) * a.rotated);
-        for (int first = 0; first < a.steps; first += kGradSteps) {
-            u32x4 x[kGradSteps], gy[kGradSteps];
+    const auto go = [&](const Share &sh) {
+        if (sh.begin >= sh.end) return;
+        const auto at = [&](int first, int u) { return (first + u) * kRows + lane / kLanes; };
+        u32x4 x[U];
+        const auto load = [&](int first) {
 #pragma unroll
-            for (int u = 0; u < kGradSteps; ++u) {
-                const int h = (first + u) * kRows + lane / kLanes;
-                x[u] = gy[u] = u32x4{0, 0, 0, 0};
-                if (h < a.heads) {
-                    const bool isq = h < a.hq;
-                    const int hh = isq ? h : h - a.hq;
-                    x[u] = load8<VEC>((isq ? a.q.p + token * a.q.ts + hh * a.q.hs
-                                           : a.k.p + token * a.k.ts + hh * a.k.hs) + li * 8);
-                    gy[u] = load8<VEC>((isq ? a.gq.p + token * a.gq.ts + hh * a.gq.hs
-                                            : a.gk.p + token * a.gk.ts + hh * a.gk.hs) + li * 8);
-                }
+            for (int u = 0; u < U; ++u) {
+                x[u] = u32x4{0, 0, 0, 0};
+                if (at(first, u) < sh.heads) x[u] = load_row<VEC, NT>(sh.x + at(first, u) * sh.in_hs + li * 8);
             }
+        };
+        load(sh.begin);
+        const u32x4 weight = load8<VEC>(sh.w + li * 8);
+        turn.load(a, lane, pos);
+        float own[8], mate[8];  // y_c = r (x_c own_c + x_mate mate_c)
+        widen(weight, own);
+        widen(turn.mates(weight), mate);
 #pragma unroll
-            for (int u = 0; u < kGradSteps; ++u) {
-                const int h = (first + u) * kRows + lane / kLanes;
-                const bool isq = h < a.hq;
-                float f[8], g[8], m[8], w[8];
+        for (int e = 0; e < 8; ++e) own[e] *= turn.c[e], mate[e] *= turn.s[e];
+        for (int first = sh.begin; first < sh.end; first += U) {
+            if (first != sh.begin) load(first);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float f[8], m[8];
                 widen(x[u], f);
-                widen(gy[u], g);
-                widen(turn.mates(gy[u]), m);
-                widen(isq ? wq : wk, w);
+                widen(turn.mates(x[u]), m);
                 float ss = 0;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
                 const float r = rsqrtf(row_sum<kLanes>(ss) * (1.0f / D) + a.eps);
-                float along = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float t = g[e] * turn.c[e] - m[e] * turn.s[e];
-                    g[e] = !known ? __uint_as_float(0x7FC00000u) : turn.turns ? t : g[e];
-                    f[e] *= r;
-                    along += g[e] * w[e] * f[e];
-                }
-                along = row_sum<kLanes>(along) * (1.0f / D);
-                if (h < a.heads) {
-                    u32x4 o;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o[i] = pack_bf16x2(r * (g[2 * i] * w[2 * i] - f[2 * i] * along),
-                                           r * (g[2 * i + 1] * w[2 * i + 1] - f[2 * i + 1] * along));
-                    const int hh = isq ? h : h - a.hq;
-                    store8<VEC>(const_cast<uint16_t *>(isq ? a.oq.p + token * a.oq.ts + hh * a.oq.hs
-                                                           : a.ok.p + token * a.ok.ts + hh * a.ok.hs) + li * 8, o);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float t = g[e] * f[e];
-                        if (isq) dq[e] += t;
-                        else dk[e] += t;
-                    }
+                for (int e = 0; e < 8; ++e) f[e] = (f[e] * own[e] + m[e] * mate[e]) * r;
+                if (at(first, u) < sh.heads && first + u < sh.end) {
+                    const u32x4 o = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
+                    store_row<VEC, NT>(sh.out + at(first, u) * sh.out_hs + li * 8, o);
                 }
             }
         }
+    };
+    go(Share{a.q.p + token * a.q.ts, const_cast<uint16_t *>(a.oq.p) + token * a.oq.ts, a.wq, a.q.hs, a.oq.hs, a.hq, begin,
+             min(end, a.qsteps)});
+    go(Share{a.k.p + token * a.k.ts, const_cast<uint16_t *>(a.ok.p) + token * a.ok.ts, a.wk, a.k.hs, a.ok.hs, a.hk,
+             max(begin - a.qsteps, 0), end - a.qsteps});
+}
+
+// Backwards.  Each lane keeps the sums of g n of its channels over all rows
+// that it meets (binary32; rows, lanes, waves and workgroups are joined as a
+// tree in a fixed order, so the sums are the same each time).  Each workgroup
+// leaves its own in the workspace, and a second launch adds them up: with the
+// last workgroup to arrive doing that, 440 tokens of 6 heads took 10.4 us where
+// the two launches take 8.3.
+template <int D, bool VEC, bool NT>
+__global__ __launch_bounds__(kThreads) void k_norm_rope_grad(NormArgs a) {
+    constexpr int kLanes = D / 8, kRows = 64 / kLanes, kWaves = kThreads / 64;
+    const int lane = threadIdx.x % 64, li = lane % kLanes, wave = uniform(threadIdx.x / 64);
+    Turn<D, VEC> turn;
+    turn.place(a, lane);
+    float dq[8] = {}, dk[8] = {};
+
+    for (int64_t item = (int64_t)blockIdx.x * kWaves + wave; item < a.tokens * a.parts;
+         item += (int64_t)gridDim.x * kWaves) {
+        const int64_t token = item / a.parts;
+        const int begin = (int)(item % a.parts) * a.per, end = min(begin + a.per, a.steps);
+        turn.load(a, lane, a.pos[token]);
+        const auto go = [&](const Share &sh, const uint16_t *gy, int64_t gy_hs, float(&dw)[8]) {
+            if (sh.begin >= sh.end) return;
+            u32x4 x, gx;  // of the step that comes next
+            const auto load = [&](int step) {
+                const int h = step * kRows + lane / kLanes;
+                x = gx = u32x4{0, 0, 0, 0};
+                if (h < sh.heads) {
+                    x = load_row<VEC, NT>(sh.x + h * sh.in_hs + li * 8);
+                    gx = load_row<VEC, NT>(gy + h * gy_hs + li * 8);
+                }
+            };
+            load(sh.begin);
+            float w[8];
+            widen(load8<VEC>(sh.w + li * 8), w);
+            for (int step = sh.begin; step < sh.end; ++step) {
+                const int h = step * kRows + lane / kLanes;
+                float n[8], g[8], m[8];
+                widen(x, n);
+                widen(gx, g);
+                widen(turn.mates(gx), m);
+                if (step + 1 < sh.end) load(step + 1);
+                float ss = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss += n[e] * n[e];
+                const float r = rsqrtf(row_sum<kLanes>(ss) * (1.0f / D) + a.eps);
+                float along = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    n[e] *= r;
+                    g[e] = g[e] * turn.c[e] - m[e] * turn.s[e];
+                    if (h < sh.heads) dw[e] += g[e] * n[e];
+                    g[e] *= w[e];
+                    along += g[e] * n[e];
+                }
+                along = row_sum<kLanes>(along) * (1.0f / D);
+                if (h < sh.heads) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[e] = r * (g[e] - n[e] * along);
+                    const u32x4 o = {bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3]), bf16_pair(g[4], g[5]), bf16_pair(g[6], g[7])};
+                    store_row<VEC, NT>(sh.out + h * sh.out_hs + li * 8, o);
+                }
+            }
+        };
+        go(Share{a.q.p + token * a.q.ts, const_cast<uint16_t *>(a.oq.p) + token * a.oq.ts, a.wq, a.q.hs, a.oq.hs, a.hq, begin,
+                 min(end, a.qsteps)},
+           a.gq.p + token * a.gq.ts, a.gq.hs, dq);
+        go(Share{a.k.p + token * a.k.ts, const_cast<uint16_t *>(a.ok.p) + token * a.ok.ts, a.wk, a.k.hs, a.ok.hs, a.hk,
+                 max(begin - a.qsteps, 0), end - a.qsteps},
+           a.gk.p + token * a.gk.ts, a.gk.hs, dk);
     }
 
     // the rows of a wave, then the waves of the workgroup
     __shared__ float part[kWaves][2 * D];
-    __shared__ uint32_t order;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
 #pragma unroll
@@ -283,57 +312,71 @@ __global__ __launch_bounds__(kThreads) void k_norm_rope_grad(NormArgs a) {
         float t = part[0][c];
 #pragma unroll
         for (int i = 1; i < kWaves; ++i) t += part[i][c];
-        store_shared(slot + c, t);
-    }
-    // groups of kJoin workgroups, then the groups: whoever comes last in a
-    // group adds its slots up into the group's first, whoever comes last of
-    // the groups adds those
-    const int groups = (int)((gridDim.x + kJoin - 1) / kJoin), mine = (int)(blockIdx.x / kJoin);
-    const int size = min(kJoin, (int)gridDim.x - mine * kJoin);
-    if (!arrive_last(a.counters + 1 + mine, size, &order)) return;
-    float *base = a.slots + (int64_t)mine * kJoin * 2 * D;
-    for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
-        float t = 0;
-#pragma unroll 8
-        for (int i = 0; i < size; ++i) t += load_shared(base + (int64_t)i * 2 * D + c);
-        store_shared(base + c, t);
-    }
-    if (!arrive_last(a.counters, groups, &order)) return;
-    for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
-        float t = 0;
-#pragma unroll 8
-        for (int i = 0; i < groups; ++i) t += load_shared(a.slots + (int64_t)i * kJoin * 2 * D + c);
-        if (c < D) {
-            if (a.dwq) a.dwq[c] = t;
-        } else if (a.dwk) {
-            a.dwk[c - D] = t;
-        }
+        slot[c] = t;
     }
 }
 
-template <bool GRAD>
-const void *pick(int dim, bool vec) {
-#define AR_PICK(D_)                                                                        \
-    case D_:                                                                               \
-        if (GRAD)                                                                          \
-            return vec ? reinterpret_cast<const void *>(&k_norm_rope_grad<D_, true>)       \
-                       : reinterpret_cast<const void *>(&k_norm_rope_grad<D_, false>);     \
-        return vec ? reinterpret_cast<const void *>(&k_norm_rope<D_, true>)                \
-                   : reinterpret_cast<const void *>(&k_norm_rope<D_, false>);
-    switch (dim) {
-        AR_PICK(64)
-        AR_PICK(128)
-        AR_PICK(256)
+// Adds the workgroups' sums up: eight columns to a workgroup, 32 slots of each
+// at a time.
+__global__ __launch_bounds__(256) void k_norm_rope_weights(NormArgs a, int dim) {
+    __shared__ float part[32][8];
+    const int c = blockIdx.x * 8 + threadIdx.x % 8, s0 = threadIdx.x / 8;
+    float t = 0;
+    for (int s = s0; s < a.blocks; s += 32 * 16) {
+        float v[16];  // all on their way at once
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = a.slots[(int64_t)min(s + 32 * k, a.blocks - 1) * 2 * dim + c];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) t += s + 32 * k < a.blocks ? v[k] : 0.0f;
     }
-#undef AR_PICK
-    return nullptr;
+    part[s0][threadIdx.x % 8] = t;
+    __syncthreads();
+    if (s0 > 0) return;
+#pragma unroll
+    for (int s = 1; s < 32; ++s) t += part[s][threadIdx.x];
+    if (c < dim) {
+        if (a.dwq) a.dwq[c] = t;
+    } else if (a.dwk) {
+        a.dwk[c - dim] = t;
+    }
 }
 
-// Workgroups of the backward pass: a token to each wave, as long as the slots
-// of the partial sums last.
-int grad_blocks(int64_t tokens) {
-    const int64_t blocks = (tokens + kThreads / 64 - 1) / (kThreads / 64);
-    return (int)(blocks < kJoin * kJoin ? blocks : kJoin * kJoin);
+template <int D>
+const void *pick_dim(bool grad, bool vec, bool few, bool stream) {
+    if (grad)
+        return !vec     ? reinterpret_cast<const void *>(&k_norm_rope_grad<D, false, false>)
+               : stream ? reinterpret_cast<const void *>(&k_norm_rope_grad<D, true, true>)
+                        : reinterpret_cast<const void *>(&k_norm_rope_grad<D, true, false>);
+    return !vec     ? reinterpret_cast<const void *>(&k_norm_rope<D, false, 1, false>)
+           : few    ? reinterpret_cast<const void *>(&k_norm_rope<D, true, 1, false>)
+           : stream ? reinterpret_cast<const void *>(&k_norm_rope<D, true, 4, true>)
+                    : reinterpret_cast<const void *>(&k_norm_rope<D, true, 4, false>);
+}
+
+const void *pick(int dim, bool grad, bool vec, bool few, bool stream) {
+    return dim == 64    ? pick_dim<64>(grad, vec, few, stream)
+           : dim == 128 ? pick_dim<128>(grad, vec, few, stream)
+                        : pick_dim<256>(grad, vec, few, stream);
+}
+
+void count_steps(NormArgs &a, int dim) {
+    const int per = 512 / dim;  // rows that a wave works on at once
+    a.qsteps = (a.hq + per - 1) / per;
+    a.steps = a.qsteps + (a.hk + per - 1) / per;
+}
+
+constexpr int kSlots = 1024;  // workgroups of the backward pass, at most
+
+// Waves that share a token backwards, and workgroups, each with a slot for its
+// sums: a wave for each step of a token while the slots last.
+int grad_parts(int64_t tokens, int steps) {
+    const int64_t parts = tokens ? kSlots * (kThreads / 64) / tokens : 1;
+    return (int)(parts < 1 ? 1 : parts > steps ? steps : parts);
+}
+
+int grad_blocks(int64_t tokens, int parts) {
+    const int64_t blocks = (tokens * parts + kThreads / 64 - 1) / (kThreads / 64);
+    return (int)(blocks < 1 ? 1 : blocks < kSlots ? blocks : kSlots);
 }
 
 bool valid_shape(int64_t tokens, int heads, int kv_heads, int dim) {
@@ -393,21 +436,32 @@ int ar_qk_norm_rope(ar_rows q, ar_rows k, const void *q_weight, const void *k_we
     a.q = rows(rq), a.k = rows(rk), a.oq = rows(oq), a.ok = rows(ok);
     a.wq = static_cast<const uint16_t *>(q_weight), a.wk = static_cast<const uint16_t *>(k_weight);
     a.cs = static_cast<const float *>(cos_sin), a.pos = static_cast<const int64_t *>(positions);
-    a.tokens = tokens, a.table = table, a.hq = heads, a.heads = heads + kv_heads;
+    a.tokens = tokens, a.table = table, a.hq = heads, a.hk = kv_heads;
     a.rotated = rotated, a.interleaved = interleaved != 0, a.eps = eps;
-    const int per = 512 / dim;  // rows a wave works on at once
-    a.steps = (a.heads + per - 1) / per;
-    a.parts = (a.steps + kSteps - 1) / kSteps;
+    count_steps(a, dim);
+    // Few rows: a wave for each step, since what a wave does takes longer than
+    // its share of the memory.  Many: as many steps to a wave as leave sixteen
+    // waves for each SIMD (eight at once: 53.6 us for 268 MB against 57.7 with
+    // eight in all), which read their token's cosines and sines once.
+    const bool few = tokens * a.steps <= 8192;
+    const int64_t parts = few ? a.steps : (16384 + tokens - 1) / tokens;
+    a.per = (int)((a.steps + parts - 1) / parts);
+    if (!few) a.per = (a.per + 3) / 4 * 4;
+    a.parts = (a.steps + a.per - 1) / a.per;
     const bool vec = rq.vec() && rk.vec() && oq.vec() && ok.vec() && aligned_to(q_weight, 16) &&
                      aligned_to(k_weight, 16) && aligned_to(cos_sin, 16);
     const int64_t blocks = (tokens * a.parts + kThreads / 64 - 1) / (kThreads / 64);
     if (blocks > 0x7FFFFFFF / kThreads) return AR_EINVAL;
-    return launch(pick<false>(dim, vec), (unsigned)blocks, kThreads, a, stream);
+    const int64_t bytes = 4 * tokens * (heads + kv_heads) * dim;
+    return launch(pick(dim, false, vec, few, bytes > kStreamBytes), (unsigned)blocks, kThreads, a, stream);
 }
 
 int64_t ar_qk_norm_rope_bwd_workspace(int64_t tokens, int heads, int kv_heads, int dim) {
     if (!valid_shape(tokens, heads, kv_heads, dim)) return AR_EINVAL;
-    return 4 * (int64_t)kJoinCounters + (int64_t)grad_blocks(tokens) * 2 * dim * 4;
+    NormArgs a = {};
+    a.hq = heads, a.hk = kv_heads;
+    count_steps(a, dim);
+    return (int64_t)grad_blocks(tokens, grad_parts(tokens, a.steps)) * 2 * dim * 4;
 }
 
 int ar_qk_norm_rope_bwd(ar_rows q_grad, ar_rows k_grad, ar_rows q, ar_rows k, const void *q_weight,
@@ -447,17 +501,25 @@ int ar_qk_norm_rope_bwd(ar_rows q_grad, ar_rows k_grad, ar_rows q, ar_rows k, co
     a.cs = static_cast<const float *>(cos_sin), a.pos = static_cast<const int64_t *>(positions);
     a.dwq = heads ? static_cast<float *>(dq_weight) : nullptr;
     a.dwk = kv_heads ? static_cast<float *>(dk_weight) : nullptr;
-    a.counters = static_cast<uint32_t *>(workspace);
-    a.slots = reinterpret_cast<float *>(a.counters + kJoinCounters);
-    a.tokens = tokens, a.table = table, a.hq = heads, a.heads = heads + kv_heads;
+    a.slots = static_cast<float *>(workspace);
+    a.tokens = tokens, a.table = table, a.hq = heads, a.hk = kv_heads;
     a.rotated = rotated, a.interleaved = interleaved != 0, a.eps = eps;
-    const int per = 512 / dim;
-    a.steps = (a.heads + per - 1) / per;
+    count_steps(a, dim);
     const bool vec = rq.vec() && rk.vec() && gq.vec() && gk.vec() && oq.vec() && ok.vec() &&
                      aligned_to(q_weight, 16) && aligned_to(k_weight, 16) && aligned_to(cos_sin, 16);
     // no tokens: one workgroup still writes the weights' gradients, zeros
-    const int blocks = tokens ? grad_blocks(tokens) : 1;
-    return launch(pick<true>(dim, vec), (unsigned)blocks, kThreads, a, stream);
+    const int parts = grad_parts(tokens, a.steps);
+    a.per = (a.steps + parts - 1) / parts;
+    a.parts = (a.steps + a.per - 1) / a.per;
+    a.blocks = grad_blocks(tokens, parts);
+    const int64_t bytes = 6 * tokens * (heads + kv_heads) * dim;
+    const int rc2 = launch(pick(dim, true, vec, false, bytes > kStreamBytes), (unsigned)a.blocks, kThreads, a, stream);
+    if (rc2 != AR_OK) return rc2;
+    void *args[] = {&a, &dim};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&k_norm_rope_weights), dim3(2 * dim / 8), dim3(256), args, 0,
+                           static_cast<hipStream_t>(stream)) == hipSuccess
+               ? AR_OK
+               : AR_ELAUNCH;
 }
 
 }  // extern "C"

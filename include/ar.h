@@ -324,10 +324,8 @@ int ar_qk_norm_rope(ar_rows q, ar_rows k, const void *q_weight, const void *k_we
  * q_grad and k_grad, and the weights' gradients (dim floats each, sums over
  * tokens and heads in binary32, in an order that depends on the sizes alone).
  *   dq, dk     may be q_grad or q, and k_grad or k, exactly.
- *   workspace  ar_qk_norm_rope_bwd_workspace bytes, zeroed once; every call
- *              leaves it fit for the next, of any sizes that it is large
- *              enough for.  Two calls in flight on one workspace are not
- *              allowed.
+ *   workspace  ar_qk_norm_rope_bwd_workspace bytes of any contents.  Two calls
+ *              in flight on one workspace are not allowed.
  * tokens == 0 sets the weights' gradients to 0.
  * ------------------------------------------------------------------------- */
 int64_t ar_qk_norm_rope_bwd_workspace(int64_t tokens, int heads, int kv_heads, int dim);

@@ -194,7 +194,7 @@ def test_binding_checks_attention():
                        (dict(lse=torch.zeros(4, 8).double()), "float32"), (dict(table=torch.zeros(4, 3).long()), "int32"),
                        (dict(table=torch.zeros(3, 4, dtype=i32).t()), "page_table"), (dict(qs=torch.zeros(4, dtype=i32)), "q_start"),
                        (dict(kv=torch.zeros(5, dtype=i32)), "kv_len"), (dict(cache=good["cache"][:, :1].contiguous()), "cache"),
-                       (dict(ws=torch.zeros(100, dtype=torch.uint8)), "workspace")):
+                       (dict(ws=torch.zeros(8, dtype=torch.uint8)), "workspace")):
         with pytest.raises(ValueError, match=match):
             ar.ar_kv4_attention(*{**good, **bad}.values(), **kw)
     with pytest.raises(ar.ArError):
