@@ -89,20 +89,32 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p) {
     }
 }
 
+// Where a lane's parts lie in every tile: offsets to the tile's address, which
+// is the same in all lanes.
 template <int D>
-__device__ __forceinline__ void load_tile(Tile<D> &t, const uint8_t *p, int lane) {
+struct Places {
     using L = Kv4<D>;
-    const int r = lane % 16, q = lane / 16;
+    uint32_t k, ks, v, vs;
+    explicit __device__ __forceinline__ Places(int lane) {
+        const int r = lane % 16, q = lane / 16;
+        k = L::k_code(r / 4 * 8 + r % 4, D == 64 ? q * 16 : q * 32);
+        ks = L::kKScale + ((D == 64 ? q / 2 : q) * 16 + r) * 2;
+        v = L::kV + lane * (4 * L::W);
+        vs = L::kVScale + (q * L::G + r * L::W / kGroup) * 8;
+    }
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(Tile<D> &t, const uint8_t *p, const Places<D> &at) {
+    using L = Kv4<D>;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int b = 0; b < Tile<D>::kBlocks; ++b)
-            load_words(t.k[i][b], p + L::k_code(r / 4 * 8 + i * 4 + r % 4, D == 64 ? q * 16 : b * 128 + q * 32));
+        for (int b = 0; b < Tile<D>::kBlocks; ++b) load_words(t.k[i][b], p + (at.k + (uint32_t)L::k_code(i * 4, b * 128)));
 #pragma unroll
-    for (int b = 0; b < Tile<D>::kBlocks; ++b)
-        t.ks[b] = *reinterpret_cast<const uint16_t *>(p + L::kKScale + ((D == 64 ? q / 2 : b * 4 + q) * 16 + r) * 2);
-    load_words(t.v, p + L::kV + lane * (4 * L::W));
-    load_words(t.vs, p + L::kVScale + (q * L::G + r * L::W / kGroup) * 8);
+    for (int b = 0; b < Tile<D>::kBlocks; ++b) t.ks[b] = *reinterpret_cast<const uint16_t *>(p + (at.ks + 128u * b));
+    load_words(t.v, p + at.v);
+    load_words(t.vs, p + at.vs);
 }
 
 // Byte n of the scales as a scale.  The conversions take the exponent's bits
@@ -173,8 +185,82 @@ constexpr float kSlack = 8.0f;
 template <int D, int R>
 constexpr int kRing = D == 64 ? 3 : 2;
 
+// The value, which the compiler takes for another one: what is computed from it
+// stays in the branch where it is needed.  (Comparisons of masks were done for
+// every tile otherwise, a quarter of the instructions of an unmasked one.)
+__device__ __forceinline__ int here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 __device__ __forceinline__ bool sees(int pos, int token, int window) {
     return token <= pos && (window == 0 || pos - token < window);
+}
+
+// Scores to weights: s[r][h][i] is the score of row tile r's row lane % 16
+// against token first + 4 h + i; p[r][n] takes the weights of tokens 2 n and
+// 2 n + 1 of those eight, as bf16.
+template <int D, int R>
+__device__ __forceinline__ void weights(State<D, R> &st, f32x4 (&s)[R][2], uint32_t (&p)[R][4], int first, bool masked, const AttnArgs &a) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        RowTile<D> &o = st.row[r];
+        if (masked) {
+            const int token = here(first);
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+                if (!sees(st.pos[r], token + n, a.window)) s[r][n / 4][n % 4] = kNegInf;
+        }
+        float top = s[r][0][0];
+#pragma unroll
+        for (int n = 1; n < 8; ++n) top = fmaxf(top, s[r][n / 4][n % 4]);
+        if (__any(top * a.c > o.m + kSlack)) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float m = fmaxf(o.m, top * a.c);
+            o.rescale(o.weight(o.m, m));
+            o.m = m;
+        }
+        const float base = o.m == kNegInf ? 0.0f : o.m;
+        float w[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            w[n] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][n / 4][n % 4], a.c, -base));
+            o.l += w[n];
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) p[r][n] = bf16_pair(w[2 * n], w[2 * n + 1]);
+    }
+}
+
+// What else a tile adds to the running results.
+template <int D, int R>
+__device__ __forceinline__ void finish_step(State<D, R> &st, const uint32_t (&p)[R][4], const uint32_t (&flag)[4], bool nan_values, int first, const AttnArgs &a) {
+    constexpr int W = Kv4<D>::W;
+    // The output is divided by the sum of the rounded weights, so that a row
+    // that few tokens dominate keeps no error of their rounding; the matrix
+    // unit adds it up beside the output.  lse has the unrounded sum.
+    const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        st.row[r].d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(ones), as_bf16(p[r]), st.row[r].d, 0, 0, 0);
+    if (nan_values) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint32_t seen[4] = {0, 0, 0, 0};
+            const int token = here(first);
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+                if (sees(st.pos[r], token + n, a.window)) seen[n / 2] |= 0x3F80u << (n % 2 * 16);
+            const f32x4 z = {0, 0, 0, 0};
+            const f32x4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(flag), as_bf16(seen), z, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n[i] > 0) st.row[r].acc[j][i] = __uint_as_float(0x7FC00000u);
+        }
+    }
 }
 
 // One tile.  `masked` (the same in all lanes): some of its tokens are unseen by
@@ -217,34 +303,7 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, boo
     }
     uint32_t p[R][4];
     const int first = index * kTile + lane / 16 * 8;  // this lane's first token
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        RowTile<D> &o = st.row[r];
-        if (masked) {
-#pragma unroll
-            for (int n = 0; n < 8; ++n)
-                if (!sees(st.pos[r], first + n, a.window)) s[r][n / 4][n % 4] = kNegInf;
-        }
-        float top = s[r][0][0];
-#pragma unroll
-        for (int n = 1; n < 8; ++n) top = fmaxf(top, s[r][n / 4][n % 4]);
-        if (__any(top * a.c > o.m + kSlack)) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float m = fmaxf(o.m, top * a.c);
-            o.rescale(o.weight(o.m, m));
-            o.m = m;
-        }
-        const float base = o.m == kNegInf ? 0.0f : o.m;
-        float w[8];
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            w[n] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][n / 4][n % 4], a.c, -base));
-            o.l += w[n];
-        }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) p[r][n] = bf16_pair(w[2 * n], w[2 * n + 1]);
-    }
+    weights<D, R>(st, s, p, first, masked, a);
 #pragma unroll
     for (int j = 0; j < W; j += 2) {
         uint32_t v[2][4];  // channels j and j + 1 of eight tokens
@@ -262,29 +321,7 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, boo
             for (int i = 0; i < 2; ++i)
                 st.row[r].acc[j + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(v[i]), as_bf16(p[r]), st.row[r].acc[j + i], 0, 0, 0);
     }
-    // The output is divided by the sum of the rounded weights, so that a row
-    // that few tokens dominate keeps no error of their rounding; the matrix
-    // unit adds it up beside the output.  lse has the unrounded sum.
-    const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        st.row[r].d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(ones), as_bf16(p[r]), st.row[r].d, 0, 0, 0);
-    if (nan_values) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            uint32_t seen[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int n = 0; n < 8; ++n)
-                if (sees(st.pos[r], first + n, a.window)) seen[n / 2] |= 0x3F80u << (n % 2 * 16);
-            const f32x4 z = {0, 0, 0, 0};
-            const f32x4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(flag), as_bf16(seen), z, 0, 0, 0);
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (n[i] > 0) st.row[r].acc[j][i] = __uint_as_float(0x7FC00000u);
-        }
-    }
+    finish_step<D, R>(st, p, flag, nan_values, first, a);
 }
 
 // The rows of a block, where they lie, and the tiles that they see.
@@ -347,12 +384,13 @@ __device__ __forceinline__ void sweep(State<D, R> &st, const AttnArgs &a, const 
         const int page = pages[(t + min(lane, count - 1) * by) >> a.shift];
         Tile<D> ring[N];
         bool known[N];
+        const Places<D> places(lane);
         const auto load = [&](int i, int to) {
             i = min(i, count - 1);  // past the last tile it is loaded again
             const int pg = __builtin_amdgcn_readlane(page, i);
             known[to] = pg >= 0 && pg < a.pages;
             const int64_t tile = (((int64_t)(known[to] ? pg : 0) * a.kv_heads + b.head) << a.shift) + ((t + i * by) & ((1 << a.shift) - 1));
-            load_tile(ring[to], a.cache + tile * Kv4<D>::kBytes, lane);
+            load_tile(ring[to], a.cache + tile * Kv4<D>::kBytes, places);
         };
 #pragma unroll
         for (int k = 0; k < N - 1; ++k) load(k, k);
@@ -465,20 +503,164 @@ struct Exchange {
     }
 };
 
-// Many rows: every wave has a row block of its own and sweeps all its tiles.
+// Many rows: the four waves of a workgroup have R row tiles each, and share
+// the work of turning codes into bf16: each turns a quarter of the next tile,
+// two of its words of K and two of each lane's eight tokens of V, and leaves it
+// in LDS as the products take it.
+template <int D>
+struct Shared {
+    static constexpr int W = Kv4<D>::W;
+    u32x4 k[2][D / 32][64];
+    uint32_t v[W][64][4];
+    uint32_t flag[64][4];  // of a masked tile: tokens whose V scale stands for NaN
+};
+
+// A wave's quarter of a tile, as it lies in the cache.
+template <int D>
+struct Quarter {
+    static constexpr int kWords = D / 64;
+    uint32_t k[kWords], v[kWords];
+    uint32_t ks, vs;
+
+    // The places of a lane's parts, as in Places.
+    static __device__ __forceinline__ Places<D> places(int lane, int wave) {
+        using L = Kv4<D>;
+        const int r = lane % 16, q = lane / 16, h = wave % 2, part = wave / 2;
+        Places<D> at(lane);
+        at.k = L::k_code(r / 4 * 8 + h * 4 + r % 4, D == 64 ? q * 16 + part * 8 : D == 128 ? q * 32 + part * 16 : part * 128 + q * 32);
+        at.ks += h + (D == 256 ? part * 128 : 0);
+        at.v += wave * L::W;
+        at.vs += wave * 2;
+        return at;
+    }
+    __device__ __forceinline__ void load(const uint8_t *p, const Places<D> &at) {
+        words(k, p + at.k);
+        ks = p[at.ks];
+        words(v, p + at.v);
+        vs = *reinterpret_cast<const uint16_t *>(p + at.vs);
+    }
+    static __device__ __forceinline__ void words(uint32_t (&w)[kWords], const uint8_t *p) {
+        if constexpr (kWords == 1) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            load_words(w, p);
+        }
+    }
+    __device__ __forceinline__ void turn(Shared<D> &to, bool masked, int lane, int wave) {
+        constexpr int W = Kv4<D>::W;
+        const int h = wave % 2, part = wave / 2;
+        const float scale = kv4_scale(ks);
+#pragma unroll
+        for (int n = 0; n < kWords; ++n) {
+            u32x4 t;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = kv4_pair(k[n], scale, e);
+            to.k[h][part * kWords + n][lane] = t;
+        }
+        if (masked) {
+            uint32_t f = 0;
+            if ((vs & 255u) == 255u) f |= 0x3F80u, vs &= 0xFF00u;
+            if (vs >> 8 == 255u) f |= 0x3F800000u, vs &= 0xFFu;
+            to.flag[lane][wave] = f;
+        }
+        const uint32_t one[1] = {vs};
+        const float s0 = scale_at(one, 0), s1 = scale_at(one, 1);
+#pragma unroll
+        for (int j = 0; j < W; j += 2) {
+            const int b0 = j / 2, b1 = b0 + W / 2;
+            const uint32_t x = kv4_pair(v[b0 / 4], s0, b0 % 4), y = kv4_pair(v[b1 / 4], s1, b1 % 4);
+            to.v[j][lane][wave] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+            to.v[j + 1][lane][wave] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+        }
+    }
+};
+
+template <int D, int R>
+__device__ __forceinline__ void step_shared(State<D, R> &st, const Shared<D> &t, int index, bool masked, const AttnArgs &a, int lane) {
+    constexpr int W = Kv4<D>::W;
+    f32x4 s[R][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[r][h] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n) {
+            const bf16x8 k = __builtin_bit_cast(bf16x8, t.k[h][n][lane]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, as_bf16(st.q[r][n]), s[r][h], 0, 0, 0);
+        }
+    }
+    uint32_t p[R][4];
+    const int first = index * kTile + lane / 16 * 8;
+    weights<D, R>(st, s, p, first, masked, a);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        const bf16x8 v = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(t.v[j][lane]));
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            st.row[r].acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, as_bf16(p[r]), st.row[r].acc[j], 0, 0, 0);
+    }
+    uint32_t flag[4] = {0, 0, 0, 0};
+    bool nan_values = false;
+    if (masked) {
+        const u32x4 f = *reinterpret_cast<const u32x4 *>(t.flag[lane]);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) flag[n] = f[n];
+        nan_values = __any((f[0] | f[1] | f[2] | f[3]) != 0);
+    }
+    finish_step<D, R>(st, p, flag, nan_values, first, a);
+}
+
 template <int D, int R>
 __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) {
+    __shared__ __attribute__((aligned(16))) Shared<D> buffer[2];
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
-    const int per = (a.blocks + kWaves - 1) / kWaves;
-    const int id = blockIdx.x;
-    const int unit = id / per, block = id % per * kWaves + wave;
-    Block b;
-    if (block >= a.blocks || !locate(b, a, unit % a.batch, unit / a.batch, block, 16 * R)) return;
+    // Each XCD takes a run of workgroups, so that the row blocks that read one
+    // key head find it in one L2; later rows see more tokens and begin first.
+    const int runs = gridDim.x / 8, id = blockIdx.x % 8 * runs + blockIdx.x / 8;
+    const int unit = id / a.blocks, block = a.blocks - 1 - id % a.blocks;
+    if (unit >= a.batch * a.kv_heads) return;
+    Block b, w;  // of the workgroup, of this wave
+    constexpr int kRows = 16 * R;
+    if (!locate(b, a, unit % a.batch, unit / a.batch, block, kWaves * kRows)) return;
+    const bool works = locate(w, a, b.seq, b.head, block * kWaves + wave, kRows);
     State<D, R> st;
-    begin(st, a, b, lane);
-    sweep<D, R, 2>(st, a, b, b.lo, b.hi, 1, lane);
+    if (works) begin(st, a, w, lane);
+    const int32_t *pages = a.table + (int64_t)b.seq * a.table_stride;
+    const Places<D> places = Quarter<D>::places(lane, wave);
+    for (int t = b.lo; t < b.hi; t += 64) {  // 64 tiles' pages at a time
+        const int count = min(64, b.hi - t);
+        const int page = pages[(t + min(lane, count - 1)) >> a.shift];
+        const auto known = [&](int i) {
+            const int pg = __builtin_amdgcn_readlane(page, i);
+            return pg >= 0 && pg < a.pages;
+        };
+        const auto masked = [&](int i) { return (t + i) * kTile < b.seen_lo || (t + i + 1) * kTile > b.seen_hi; };
+        Quarter<D> next;
+        const auto load = [&](int i) {
+            i = min(i, count - 1);
+            const int pg = known(i) ? __builtin_amdgcn_readlane(page, i) : 0;
+            const int64_t tile = (((int64_t)pg * a.kv_heads + b.head) << a.shift) + ((t + i) & ((1 << a.shift) - 1));
+            next.load(a.cache + tile * Kv4<D>::kBytes, places);
+        };
+        load(0);
+        next.turn(buffer[0], masked(0), lane, wave);
+        load(1);
+        __syncthreads();
+        for (int i = 0; i < count; ++i) {
+            if (i + 1 < count) next.turn(buffer[(i + 1) % 2], masked(i + 1), lane, wave);
+            load(i + 2);
+            if (works && known(i)) step_shared<D, R>(st, buffer[i % 2], t + i, masked(i), a, lane);
+            __syncthreads();
+        }
+    }
+    if (!works) return;
 #pragma unroll
-    for (int r = 0; r < R; ++r) finish(st.row[r], a, b, r, lane);
+    for (int r = 0; r < R; ++r) {
+        st.row[r].l += __shfl_xor(st.row[r].l, 16);
+        st.row[r].l += __shfl_xor(st.row[r].l, 32);
+        finish(st.row[r], a, w, r, lane);
+    }
 }
 
 // How the tiles of a block are shared by workgroups: equal ranges, none shorter
@@ -634,17 +816,23 @@ struct Plan {
     int64_t units;
 };
 
+constexpr int wide_tiles(int dim) { return dim == 64 ? 4 : dim == 128 ? 2 : 1; }
+
 Plan plan(int batch, int max_q, int64_t max_kv, int64_t window, int group, int kv_heads, int dim) {
     Plan p = {};
     const int64_t rows = (int64_t)max_q * group, tiles = (rows + 15) / 16;
     const int most = dim == 64 ? 3 : dim == 128 ? 2 : 1;
     p.tiles = (int)(tiles < most ? tiles : most);
-    p.blocks = (int)((tiles + p.tiles - 1) / p.tiles);
-    p.units = (int64_t)batch * kv_heads * p.blocks;
-    p.wide = p.blocks >= kWaves && p.units >= 1024;
     p.splits = p.chunk = 1;
     p.waves = kWaves;
+    // rows enough for four waves on half of the compute units
+    const int wide = kWaves * wide_tiles(dim);
+    p.blocks = (int)((tiles + wide - 1) / wide);
+    p.units = (int64_t)batch * kv_heads * p.blocks;
+    p.wide = tiles >= wide && p.units >= kCus / 2;
     if (p.wide) return p;
+    p.blocks = (int)((tiles + p.tiles - 1) / p.tiles);
+    p.units = (int64_t)batch * kv_heads * p.blocks;
     if (window && max_kv > window + max_q) max_kv = window + max_q;
     const int64_t steps = (max_kv + kTile - 1) / kTile;
     const bool few = p.units < 2 * kCus;
@@ -686,7 +874,7 @@ Kernels pick_rows(const Plan &p) {
                        : p.splits <= 16 ? reinterpret_cast<const void *>(&k_kv4_join<D, R, 4, 1>)
                        : p.splits <= 64 ? reinterpret_cast<const void *>(&k_kv4_join<D, R, 16, 1>)
                                         : reinterpret_cast<const void *>(&k_kv4_join<D, R, 16, 4>);
-    if (p.wide) return {reinterpret_cast<const void *>(&k_kv4_attention_wide<D, R>), join, items};
+    if (p.wide) return {reinterpret_cast<const void *>(&k_kv4_attention_wide<D, wide_tiles(D)>), join, items};
     if (p.waves == kWaves) return {reinterpret_cast<const void *>(&k_kv4_attention<D, R, kWaves>), join, items};
     return {reinterpret_cast<const void *>(&k_kv4_attention<D, R, 2 * kWaves>), join, items};
 }
@@ -766,7 +954,7 @@ int ar_kv4_attention(ar_rows q, const void *cache, const void *page_table, int64
     a.vec = rq.vec() && ro.vec();
     a.c = scale * kLog2e;
     const int64_t pairs = batch * kv_heads;
-    const int64_t grid = p.wide ? pairs * ((p.blocks + kWaves - 1) / kWaves) : pairs * p.blocks * p.splits;
+    const int64_t grid = p.wide ? (pairs * p.blocks + 7) / 8 * 8 : pairs * p.blocks * p.splits;
     if (grid > 0x7FFFFFFF / (64 * p.waves)) return AR_EINVAL;
     const Kernels k = pick(p, dim);
     const int rc = launch(k.main, (unsigned)grid, 64 * p.waves, a, stream);

@@ -347,3 +347,22 @@ def test_a_cache_past_4_gib():
                         torch.tensor([n], dtype=torch.int32, device=DEV), out, lse, ws, page_size=page, kv_heads=hk, max_q=2, max_kv=n)
     c.check(out.cpu(), lse.cpu())
     assert np.array_equal(c.kc.shape, (c.pages, hk, page // 32, 32, D))
+
+
+@pytest.mark.parametrize("D,heads,hk,m,n", [(64, 16, 8, 520, 700), (128, 32, 8, 300, 300), (256, 16, 8, 260, 333)])
+def test_prompts_with_nan_and_lost_pages(D, heads, hk, m, n):
+    """Many rows: NaN values that some rows of a tile see, NaN past the tokens,
+    pages outside the cache."""
+    c = Case([m, m - 3, 2], [n, n - 5, 1], heads, hk, D, 32)
+    first = n - m  # what the second query sees last
+    for t, g in ((first + 1, 0), (first + 40, 1), (n - 1, 0)):
+        c.vb[c.table[0, t // 32], 1, 0, t % 32, g] = 255
+    c.kb[c.table[1, 1], 0, 0, 5, 0] = 255
+    for b in range(2):
+        p = c.table[b, (c.kvlens[b] - 1) // 32]
+        c.vb[p, :, 0, (c.kvlens[b] - 1) % 32 + 1:] = 255
+        c.kb[p, :, 0, (c.kvlens[b] - 1) % 32 + 1:] = 255
+    c.table[0, 2], c.table[1, 0] = c.pages + 3, -1
+    out, lse = c.run()
+    c.check(out, lse)
+    assert torch.isnan(out).any() and not torch.isnan(out).all()
