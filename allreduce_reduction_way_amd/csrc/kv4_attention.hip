@@ -148,11 +148,12 @@ template <int D>
 struct RowTile {
     static constexpr int W = Kv4<D>::W;
     float m, l;
+    float base, limit;  // m, 0 before there is one; the score from which m has to move
     f32x4 d;  // four times the same: the sum of the weights as they were rounded
     f32x4 acc[W];
 
     __device__ __forceinline__ void clear() {
-        m = kNegInf, l = 0;
+        m = limit = kNegInf, l = base = 0;
         d = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < W; ++j) acc[j] = f32x4{0, 0, 0, 0};
@@ -197,45 +198,64 @@ __device__ __forceinline__ bool sees(int pos, int token, int window) {
     return token <= pos && (window == 0 || pos - token < window);
 }
 
-// Scores to weights: s[r][h][i] is the score of row tile r's row lane % 16
-// against token first + 4 h + i; p[r][n] takes the weights of tokens 2 n and
-// 2 n + 1 of those eight, as bf16.
-template <int D, int R>
-__device__ __forceinline__ void weights(State<D, R> &st, f32x4 (&s)[R][2], uint32_t (&p)[R][4], int first, bool masked, const AttnArgs &a) {
+// Scores of N tiles to weights: s[r][2 k + h][i] is the score of row tile r's
+// row lane % 16 against token first[k] + 4 h + i; p[r][k][n] takes the weights
+// of tokens 2 n and 2 n + 1 of those eight, as bf16.
+template <int D, int R, int N>
+__device__ __forceinline__ void weights(State<D, R> &st, f32x4 (&s)[R][2 * N], uint32_t (&p)[R][N][4], const int (&first)[N], bool masked, const AttnArgs &a) {
+    if (masked) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int token = here(first[k]);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+                    if (!sees(st.pos[r], token + n, a.window)) s[r][2 * k + n / 4][n % 4] = kNegInf;
+        }
+    }
+    float top[R];
+    bool more = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        top[r] = s[r][0][0];
+#pragma unroll
+        for (int n = 1; n < 8 * N; ++n) top[r] = fmaxf(top[r], s[r][n / 4][n % 4]);
+        more |= top[r] > st.row[r].limit;
+    }
+    if (__any(more)) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            RowTile<D> &o = st.row[r];
+            float t = fmaxf(top[r], __shfl_xor(top[r], 16));
+            t = fmaxf(t, __shfl_xor(t, 32));
+            const float m = fmaxf(o.m, t * a.c);
+            o.rescale(o.weight(o.m, m));
+            o.m = m;
+            o.base = m == kNegInf ? 0.0f : m;
+            o.limit = (m + kSlack) / a.c;
+        }
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         RowTile<D> &o = st.row[r];
-        if (masked) {
-            const int token = here(first);
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
-                if (!sees(st.pos[r], token + n, a.window)) s[r][n / 4][n % 4] = kNegInf;
+        for (int k = 0; k < N; ++k) {
+            float w[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                w[n] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][2 * k + n / 4][n % 4], a.c, -o.base));
+                o.l += w[n];
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) p[r][k][n] = bf16_pair(w[2 * n], w[2 * n + 1]);
         }
-        float top = s[r][0][0];
-#pragma unroll
-        for (int n = 1; n < 8; ++n) top = fmaxf(top, s[r][n / 4][n % 4]);
-        if (__any(top * a.c > o.m + kSlack)) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float m = fmaxf(o.m, top * a.c);
-            o.rescale(o.weight(o.m, m));
-            o.m = m;
-        }
-        const float base = o.m == kNegInf ? 0.0f : o.m;
-        float w[8];
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            w[n] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][n / 4][n % 4], a.c, -base));
-            o.l += w[n];
-        }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) p[r][n] = bf16_pair(w[2 * n], w[2 * n + 1]);
     }
 }
 
 // What else a tile adds to the running results.
 template <int D, int R>
-__device__ __forceinline__ void finish_step(State<D, R> &st, const uint32_t (&p)[R][4], const uint32_t (&flag)[4], bool nan_values, int first, const AttnArgs &a) {
+__device__ __forceinline__ void finish_step(State<D, R> &st, const bf16x8 (&p)[R], const uint32_t (&flag)[4], bool nan_values, int first, const AttnArgs &a) {
     constexpr int W = Kv4<D>::W;
     // The output is divided by the sum of the rounded weights, so that a row
     // that few tokens dominate keeps no error of their rounding; the matrix
@@ -243,7 +263,7 @@ __device__ __forceinline__ void finish_step(State<D, R> &st, const uint32_t (&p)
     const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
     for (int r = 0; r < R; ++r)
-        st.row[r].d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(ones), as_bf16(p[r]), st.row[r].d, 0, 0, 0);
+        st.row[r].d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(ones), p[r], st.row[r].d, 0, 0, 0);
     if (nan_values) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -301,9 +321,12 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, boo
                 s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(k), as_bf16(st.q[r][n]), s[r][h], 0, 0, 0);
         }
     }
-    uint32_t p[R][4];
-    const int first = index * kTile + lane / 16 * 8;  // this lane's first token
-    weights<D, R>(st, s, p, first, masked, a);
+    uint32_t pw[R][1][4];
+    const int first[1] = {index * kTile + lane / 16 * 8};  // this lane's first token
+    weights<D, R, 1>(st, s, pw, first, masked, a);
+    bf16x8 p[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) p[r] = as_bf16(pw[r][0]);
 #pragma unroll
     for (int j = 0; j < W; j += 2) {
         uint32_t v[2][4];  // channels j and j + 1 of eight tokens
@@ -319,9 +342,9 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, boo
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                st.row[r].acc[j + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(v[i]), as_bf16(p[r]), st.row[r].acc[j + i], 0, 0, 0);
+                st.row[r].acc[j + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(v[i]), p[r], st.row[r].acc[j + i], 0, 0, 0);
     }
-    finish_step<D, R>(st, p, flag, nan_values, first, a);
+    finish_step<D, R>(st, p, flag, nan_values, first[0], a);
 }
 
 // The rows of a block, where they lie, and the tiles that they see.
@@ -575,45 +598,58 @@ struct Quarter {
     }
 };
 
-template <int D, int R>
-__device__ __forceinline__ void step_shared(State<D, R> &st, const Shared<D> &t, int index, bool masked, const AttnArgs &a, int lane) {
+// N tiles; first[k] is this lane's first token of tile k.
+template <int D, int R, int N>
+__device__ __forceinline__ void step_shared(State<D, R> &st, const Shared<D> (&t)[N], const int (&first)[N], bool masked, const AttnArgs &a, int lane) {
     constexpr int W = Kv4<D>::W;
-    f32x4 s[R][2];
+    f32x4 s[R][2 * N];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int r = 0; r < R; ++r) s[r][h] = f32x4{0, 0, 0, 0};
+        for (int h = 0; h < 2 * N; ++h) s[r][h] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
 #pragma unroll
         for (int n = 0; n < D / 32; ++n) {
-            const bf16x8 k = __builtin_bit_cast(bf16x8, t.k[h][n][lane]);
 #pragma unroll
-            for (int r = 0; r < R; ++r) s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, as_bf16(st.q[r][n]), s[r][h], 0, 0, 0);
+            for (int h = 0; h < 2; ++h) {
+                const bf16x8 c = __builtin_bit_cast(bf16x8, t[k].k[h][n][lane]);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    s[r][2 * k + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c, as_bf16(st.q[r][n]), s[r][2 * k + h], 0, 0, 0);
+            }
         }
     }
-    uint32_t p[R][4];
-    const int first = index * kTile + lane / 16 * 8;
-    weights<D, R>(st, s, p, first, masked, a);
+    uint32_t pw[R][N][4];
+    weights<D, R, N>(st, s, pw, first, masked, a);
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        const bf16x8 v = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(t.v[j][lane]));
+    for (int k = 0; k < N; ++k) {
+        bf16x8 p[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            st.row[r].acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, as_bf16(p[r]), st.row[r].acc[j], 0, 0, 0);
+        for (int r = 0; r < R; ++r) p[r] = as_bf16(pw[r][k]);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const bf16x8 v = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(t[k].v[j][lane]));
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                st.row[r].acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[r], st.row[r].acc[j], 0, 0, 0);
+        }
+        uint32_t flag[4] = {0, 0, 0, 0};
+        bool nan_values = false;
+        if (masked) {
+            const u32x4 f = *reinterpret_cast<const u32x4 *>(t[k].flag[lane]);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) flag[n] = f[n];
+            nan_values = __any((f[0] | f[1] | f[2] | f[3]) != 0);
+        }
+        finish_step<D, R>(st, p, flag, nan_values, first[k], a);
     }
-    uint32_t flag[4] = {0, 0, 0, 0};
-    bool nan_values = false;
-    if (masked) {
-        const u32x4 f = *reinterpret_cast<const u32x4 *>(t.flag[lane]);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) flag[n] = f[n];
-        nan_values = __any((f[0] | f[1] | f[2] | f[3]) != 0);
-    }
-    finish_step<D, R>(st, p, flag, nan_values, first, a);
 }
 
-template <int D, int R>
+// N: tiles between two barriers.
+template <int D, int R, int N>
 __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) {
-    __shared__ __attribute__((aligned(16))) Shared<D> buffer[2];
+    __shared__ __attribute__((aligned(16))) Shared<D> buffer[2][N];
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     // Each XCD takes a run of workgroups, so that the row blocks that read one
     // key head find it in one L2; later rows see more tokens and begin first.
@@ -635,22 +671,41 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
             const int pg = __builtin_amdgcn_readlane(page, i);
             return pg >= 0 && pg < a.pages;
         };
-        const auto masked = [&](int i) { return (t + i) * kTile < b.seen_lo || (t + i + 1) * kTile > b.seen_hi; };
-        Quarter<D> next;
-        const auto load = [&](int i) {
-            i = min(i, count - 1);
-            const int pg = known(i) ? __builtin_amdgcn_readlane(page, i) : 0;
-            const int64_t tile = (((int64_t)pg * a.kv_heads + b.head) << a.shift) + ((t + i) & ((1 << a.shift) - 1));
-            next.load(a.cache + tile * Kv4<D>::kBytes, places);
+        // of the N tiles from i on, those past the last among them
+        const auto masked = [&](int i) {
+            bool lost = i + N > count || (t + i) * kTile < b.seen_lo || (t + i + N) * kTile > b.seen_hi;
+#pragma unroll
+            for (int k = 0; k < N; ++k) lost |= !known(min(i + k, count - 1));
+            return lost;
+        };
+        Quarter<D> next[N];
+        const auto load = [&](int first) {  // past the last tile it is loaded again
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int i = min(first + k, count - 1);
+                const int pg = known(i) ? __builtin_amdgcn_readlane(page, i) : 0;
+                const int64_t tile = (((int64_t)pg * a.kv_heads + b.head) << a.shift) + ((t + i) & ((1 << a.shift) - 1));
+                next[k].load(a.cache + tile * Kv4<D>::kBytes, places);
+            }
+        };
+        const auto turn = [&](int first, int to) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) next[k].turn(buffer[to][k], masked(first), lane, wave);
         };
         load(0);
-        next.turn(buffer[0], masked(0), lane, wave);
-        load(1);
+        turn(0, 0);
+        load(N);
         __syncthreads();
-        for (int i = 0; i < count; ++i) {
-            if (i + 1 < count) next.turn(buffer[(i + 1) % 2], masked(i + 1), lane, wave);
-            load(i + 2);
-            if (works && known(i)) step_shared<D, R>(st, buffer[i % 2], t + i, masked(i), a, lane);
+        for (int i = 0, at = 0; i < count; i += N, at ^= 1) {
+            if (i + N < count) turn(i + N, at ^ 1);
+            load(i + 2 * N);
+            if (works) {
+                int first[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k)  // tokens that are not there are past every row's position
+                    first[k] = i + k < count && known(min(i + k, count - 1)) ? (t + i + k) * kTile + lane / 16 * 8 : 0x7FFFFF00;
+                step_shared<D, R, N>(st, buffer[at], first, masked(i), a, lane);
+            }
             __syncthreads();
         }
     }
@@ -874,7 +929,7 @@ Kernels pick_rows(const Plan &p) {
                        : p.splits <= 16 ? reinterpret_cast<const void *>(&k_kv4_join<D, R, 4, 1>)
                        : p.splits <= 64 ? reinterpret_cast<const void *>(&k_kv4_join<D, R, 16, 1>)
                                         : reinterpret_cast<const void *>(&k_kv4_join<D, R, 16, 4>);
-    if (p.wide) return {reinterpret_cast<const void *>(&k_kv4_attention_wide<D, wide_tiles(D)>), join, items};
+    if (p.wide) return {reinterpret_cast<const void *>(&k_kv4_attention_wide<D, wide_tiles(D), D == 256 ? 1 : 2>), join, items};
     if (p.waves == kWaves) return {reinterpret_cast<const void *>(&k_kv4_attention<D, R, kWaves>), join, items};
     return {reinterpret_cast<const void *>(&k_kv4_attention<D, R, 2 * kWaves>), join, items};
 }
