@@ -74,18 +74,30 @@ struct Tile {
     uint32_t vs[2];
 };
 
+// A tile is addressed by a buffer resource, the same in all lanes, and an
+// offset of 32 bits: no addresses of 64 bits are added up in the lanes.
+typedef __amdgpu_buffer_rsrc_t TileAddr;
+
+template <int D>
+__device__ __forceinline__ TileAddr tile_addr(const uint8_t *p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), (short)0, Kv4<D>::kBytes, 0x00020000);
+}
+
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p) {
-    if (N == 2) {
-        const uint2 t = *reinterpret_cast<const uint2 *>(p);
-        w[0] = t.x, w[1] = t.y;
-        return;
-    }
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], TileAddr p, uint32_t at) {
+    if constexpr (N == 1) {
+        w[0] = __builtin_amdgcn_raw_buffer_load_b32(p, at, 0, 0);
+    } else if constexpr (N == 2) {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(p, at, 0, 0);
+        w[0] = t[0], w[1] = t[1];
+    } else {
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-        const u32x4 t = reinterpret_cast<const u32x4 *>(p)[i];
+        for (int i = 0; i < N / 4; ++i) {
+            const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(p, at + 16 * i, 0, 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[i * 4 + j] = t[j];
+            for (int j = 0; j < 4; ++j) w[i * 4 + j] = t[j];
+        }
     }
 }
 
@@ -105,16 +117,17 @@ struct Places {
 };
 
 template <int D>
-__device__ __forceinline__ void load_tile(Tile<D> &t, const uint8_t *p, const Places<D> &at) {
+__device__ __forceinline__ void load_tile(Tile<D> &t, const uint8_t *tile, const Places<D> &at) {
     using L = Kv4<D>;
+    const TileAddr p = tile_addr<D>(tile);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int b = 0; b < Tile<D>::kBlocks; ++b) load_words(t.k[i][b], p + (at.k + (uint32_t)L::k_code(i * 4, b * 128)));
+        for (int b = 0; b < Tile<D>::kBlocks; ++b) load_words(t.k[i][b], p, at.k + (uint32_t)L::k_code(i * 4, b * 128));
 #pragma unroll
-    for (int b = 0; b < Tile<D>::kBlocks; ++b) t.ks[b] = *reinterpret_cast<const uint16_t *>(p + (at.ks + 128u * b));
-    load_words(t.v, p + at.v);
-    load_words(t.vs, p + at.vs);
+    for (int b = 0; b < Tile<D>::kBlocks; ++b) t.ks[b] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(p, at.ks + 128u * b, 0, 0);
+    load_words(t.v, p, at.v);
+    load_words(t.vs, p, at.vs);
 }
 
 // Byte n of the scales as a scale.  The conversions take the exponent's bits
@@ -198,21 +211,18 @@ __device__ __forceinline__ bool sees(int pos, int token, int window) {
     return token <= pos && (window == 0 || pos - token < window);
 }
 
-// Scores of N tiles to weights: s[r][2 k + h][i] is the score of row tile r's
-// row lane % 16 against token first[k] + 4 h + i; p[r][k][n] takes the weights
-// of tokens 2 n and 2 n + 1 of those eight, as bf16.
-template <int D, int R, int N>
-__device__ __forceinline__ void weights(State<D, R> &st, f32x4 (&s)[R][2 * N], uint32_t (&p)[R][N][4], const int (&first)[N], bool masked, const AttnArgs &a) {
+// Scores of a tile, s[r][h][i] of row tile r's row lane % 16 against token
+// first + 4 h + i, made ready for weights(): tokens that a row does not see are
+// taken out, and its maximum moves if they outgrow it.
+template <int D, int R>
+__device__ __forceinline__ void settle(State<D, R> &st, f32x4 (&s)[R][2], int first, bool masked, const AttnArgs &a) {
     if (masked) {
+        const int token = here(first);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int token = here(first[k]);
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int n = 0; n < 8; ++n)
-                    if (!sees(st.pos[r], token + n, a.window)) s[r][2 * k + n / 4][n % 4] = kNegInf;
-        }
+            for (int n = 0; n < 8; ++n)
+                if (!sees(st.pos[r], token + n, a.window)) s[r][n / 4][n % 4] = kNegInf;
     }
     float top[R];
     bool more = false;
@@ -220,7 +230,7 @@ __device__ __forceinline__ void weights(State<D, R> &st, f32x4 (&s)[R][2 * N], u
     for (int r = 0; r < R; ++r) {
         top[r] = s[r][0][0];
 #pragma unroll
-        for (int n = 1; n < 8 * N; ++n) top[r] = fmaxf(top[r], s[r][n / 4][n % 4]);
+        for (int n = 1; n < 8; ++n) top[r] = fmaxf(top[r], s[r][n / 4][n % 4]);
         more |= top[r] > st.row[r].limit;
     }
     if (__any(more)) {
@@ -236,20 +246,23 @@ __device__ __forceinline__ void weights(State<D, R> &st, f32x4 (&s)[R][2 * N], u
             o.limit = (m + kSlack) / a.c;
         }
     }
+}
+
+// The weights of the lane's eight tokens, two in a word, as bf16.
+template <int D, int R>
+__device__ __forceinline__ void weights(State<D, R> &st, const f32x4 (&s)[R][2], bf16x8 (&p)[R], const AttnArgs &a) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         RowTile<D> &o = st.row[r];
+        float w[8];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            float w[8];
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                w[n] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][2 * k + n / 4][n % 4], a.c, -o.base));
-                o.l += w[n];
-            }
-#pragma unroll
-            for (int n = 0; n < 4; ++n) p[r][k][n] = bf16_pair(w[2 * n], w[2 * n + 1]);
+        for (int n = 0; n < 8; ++n) {
+            w[n] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][n / 4][n % 4], a.c, -o.base));
+            o.l += w[n];
         }
+        asm volatile("" : "+v"(o.l));  // here, and not where the compiler would put it: after the products
+        const uint32_t v[4] = {bf16_pair(w[0], w[1]), bf16_pair(w[2], w[3]), bf16_pair(w[4], w[5]), bf16_pair(w[6], w[7])};
+        p[r] = as_bf16(v);
     }
 }
 
@@ -321,12 +334,10 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, boo
                 s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(k), as_bf16(st.q[r][n]), s[r][h], 0, 0, 0);
         }
     }
-    uint32_t pw[R][1][4];
-    const int first[1] = {index * kTile + lane / 16 * 8};  // this lane's first token
-    weights<D, R, 1>(st, s, pw, first, masked, a);
+    const int first = index * kTile + lane / 16 * 8;  // this lane's first token
+    settle<D, R>(st, s, first, masked, a);
     bf16x8 p[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) p[r] = as_bf16(pw[r][0]);
+    weights<D, R>(st, s, p, a);
 #pragma unroll
     for (int j = 0; j < W; j += 2) {
         uint32_t v[2][4];  // channels j and j + 1 of eight tokens
@@ -344,7 +355,7 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, boo
             for (int i = 0; i < 2; ++i)
                 st.row[r].acc[j + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(v[i]), p[r], st.row[r].acc[j + i], 0, 0, 0);
     }
-    finish_step<D, R>(st, p, flag, nan_values, first[0], a);
+    finish_step<D, R>(st, p, flag, nan_values, first, a);
 }
 
 // The rows of a block, where they lie, and the tiles that they see.
@@ -396,33 +407,46 @@ __device__ __forceinline__ void begin(State<D, R> &st, const AttnArgs &a, const 
     }
 }
 
+// The pages of up to 64 tiles of a sequence, t, t + by, ..., one in each lane.
+struct Pages {
+    int page;        // of this lane's tile; the first where it is lost
+    uint64_t known;  // tiles whose page is one of the cache's
+    int t, by, count;
+
+    __device__ __forceinline__ Pages(const AttnArgs &a, const int32_t *row, int t_, int by_, int hi, int lane)
+        : t(t_), by(by_), count(min(64, (hi - t_ + by_ - 1) / by_)) {
+        page = row[(t + min(lane, count - 1) * by) >> a.shift];
+        known = __ballot((uint32_t)page < (uint32_t)a.pages);
+        if ((uint32_t)page >= (uint32_t)a.pages) page = 0;
+    }
+    // Tile i, or the last one past it.
+    __device__ __forceinline__ bool has(int i) const { return known >> min(i, count - 1) & 1; }
+    template <int D>
+    __device__ __forceinline__ const uint8_t *tile(const AttnArgs &a, int head, int i) const {
+        i = min(i, count - 1);
+        const int64_t at = (((int64_t)__builtin_amdgcn_readlane(page, i) * a.kv_heads + head) << a.shift) + ((t + i * by) & ((1 << a.shift) - 1));
+        return a.cache + at * Kv4<D>::kBytes;
+    }
+};
+
 // Tiles lo, lo + by, ... below hi.  While a tile is worked on, the next N - 1
 // are on their way; the pages of 64 tiles are looked up at once, one in each
 // lane.
 template <int D, int R, int N>
 __device__ __forceinline__ void sweep(State<D, R> &st, const AttnArgs &a, const Block &b, int lo, int hi, int by, int lane) {
-    const int32_t *pages = a.table + (int64_t)b.seq * a.table_stride;
+    const int32_t *row = a.table + (int64_t)b.seq * a.table_stride;
+    const Places<D> places(lane);
     for (int t = lo; t < hi; t += 64 * by) {
-        const int count = min(64, (hi - t + by - 1) / by);
-        const int page = pages[(t + min(lane, count - 1) * by) >> a.shift];
+        const Pages pages(a, row, t, by, hi, lane);
         Tile<D> ring[N];
-        bool known[N];
-        const Places<D> places(lane);
-        const auto load = [&](int i, int to) {
-            i = min(i, count - 1);  // past the last tile it is loaded again
-            const int pg = __builtin_amdgcn_readlane(page, i);
-            known[to] = pg >= 0 && pg < a.pages;
-            const int64_t tile = (((int64_t)(known[to] ? pg : 0) * a.kv_heads + b.head) << a.shift) + ((t + i * by) & ((1 << a.shift) - 1));
-            load_tile(ring[to], a.cache + tile * Kv4<D>::kBytes, places);
-        };
 #pragma unroll
-        for (int k = 0; k < N - 1; ++k) load(k, k);
-        for (int i = 0; i < count; i += N) {
+        for (int k = 0; k < N - 1; ++k) load_tile(ring[k], pages.tile<D>(a, b.head, k), places);
+        for (int i = 0; i < pages.count; i += N) {
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                if (i + k >= count) break;
-                load(i + k + N - 1, (k + N - 1) % N);
-                if (!known[k]) continue;
+                if (i + k >= pages.count) break;
+                load_tile(ring[(k + N - 1) % N], pages.tile<D>(a, b.head, i + k + N - 1), places);
+                if (!pages.has(i + k)) continue;
                 const int index = t + (i + k) * by;
                 const bool masked = index * kTile < b.seen_lo || (index + 1) * kTile > b.seen_hi;
                 step<D, R>(st, ring[k], index, masked, a, lane);
@@ -527,23 +551,32 @@ struct Exchange {
 };
 
 // Many rows: the four waves of a workgroup have R row tiles each, and share
-// the work of turning codes into bf16: each turns a quarter of the next tile,
-// two of its words of K and two of each lane's eight tokens of V, and leaves it
-// in LDS as the products take it.
+// the work of turning codes into bf16: each turns a quarter of a tile, two words
+// of K and two of each lane's eight tokens of V at D = 128, and leaves it in LDS
+// as the products take it.
+//
+// While a tile's scores become weights, the products of the next tile's scores
+// run, and the next tiles are turned beside the products of the output: in one
+// stream of instructions, because one wave alone issues to its vector unit only
+// every eighth cycle, and two waves to a SIMD are what the registers allow.
 template <int D>
-struct Shared {
-    static constexpr int W = Kv4<D>::W;
+struct SharedK {
     u32x4 k[2][D / 32][64];
+};
+
+template <int D>
+struct SharedV {
+    static constexpr int W = Kv4<D>::W;
     uint32_t v[W][64][4];
     uint32_t flag[64][4];  // of a masked tile: tokens whose V scale stands for NaN
 };
 
-// A wave's quarter of a tile, as it lies in the cache.
+// A wave's quarter of a tile's keys, or values, as it lies in the cache.
 template <int D>
 struct Quarter {
     static constexpr int kWords = D / 64;
-    uint32_t k[kWords], v[kWords];
-    uint32_t ks, vs;
+    uint32_t w[kWords];
+    uint32_t scale;
 
     // The places of a lane's parts, as in Places.
     static __device__ __forceinline__ Places<D> places(int lane, int wave) {
@@ -556,100 +589,68 @@ struct Quarter {
         at.vs += wave * 2;
         return at;
     }
-    __device__ __forceinline__ void load(const uint8_t *p, const Places<D> &at) {
-        words(k, p + at.k);
-        ks = p[at.ks];
-        words(v, p + at.v);
-        vs = *reinterpret_cast<const uint16_t *>(p + at.vs);
+    __device__ __forceinline__ void load_k(const uint8_t *tile, const Places<D> &at) {
+        const TileAddr p = tile_addr<D>(tile);
+        load_words(w, p, at.k);
+        scale = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(p, at.ks, 0, 0);
     }
-    static __device__ __forceinline__ void words(uint32_t (&w)[kWords], const uint8_t *p) {
-        if constexpr (kWords == 1) {
-            w[0] = *reinterpret_cast<const uint32_t *>(p);
-        } else {
-            load_words(w, p);
-        }
+    __device__ __forceinline__ void load_v(const uint8_t *tile, const Places<D> &at) {
+        const TileAddr p = tile_addr<D>(tile);
+        load_words(w, p, at.v);
+        scale = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(p, at.vs, 0, 0);
     }
-    __device__ __forceinline__ void turn(Shared<D> &to, bool masked, int lane, int wave) {
-        constexpr int W = Kv4<D>::W;
-        const int h = wave % 2, part = wave / 2;
-        const float scale = kv4_scale(ks);
+    __device__ __forceinline__ void turn_k(SharedK<D> &to, int lane, int wave) const {
+        const float by = kv4_scale(scale);
 #pragma unroll
         for (int n = 0; n < kWords; ++n) {
             u32x4 t;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = kv4_pair(k[n], scale, e);
-            to.k[h][part * kWords + n][lane] = t;
+            for (int e = 0; e < 4; ++e) t[e] = kv4_pair(w[n], by, e);
+            to.k[wave % 2][wave / 2 * kWords + n][lane] = t;
         }
-        if (masked) {
-            uint32_t f = 0;
-            if ((vs & 255u) == 255u) f |= 0x3F80u, vs &= 0xFF00u;
-            if (vs >> 8 == 255u) f |= 0x3F800000u, vs &= 0xFFu;
-            to.flag[lane][wave] = f;
-        }
-        const uint32_t one[1] = {vs};
+    }
+    // Values that are NaN are taken out of a masked tile, and flagged.
+    __device__ __forceinline__ void hide(SharedV<D> &to, int lane, int wave) {
+        uint32_t f = 0;
+        if ((scale & 255u) == 255u) f |= 0x3F80u, scale &= 0xFF00u;
+        if (scale >> 8 == 255u) f |= 0x3F800000u, scale &= 0xFFu;
+        to.flag[lane][wave] = f;
+    }
+    __device__ __forceinline__ void turn_v(SharedV<D> &to, int lane, int wave) const {
+        constexpr int W = Kv4<D>::W;
+        const uint32_t one[1] = {scale};
         const float s0 = scale_at(one, 0), s1 = scale_at(one, 1);
 #pragma unroll
         for (int j = 0; j < W; j += 2) {
             const int b0 = j / 2, b1 = b0 + W / 2;
-            const uint32_t x = kv4_pair(v[b0 / 4], s0, b0 % 4), y = kv4_pair(v[b1 / 4], s1, b1 % 4);
+            const uint32_t x = kv4_pair(w[b0 / 4], s0, b0 % 4), y = kv4_pair(w[b1 / 4], s1, b1 % 4);
             to.v[j][lane][wave] = __builtin_amdgcn_perm(y, x, 0x05040100u);
             to.v[j + 1][lane][wave] = __builtin_amdgcn_perm(y, x, 0x07060302u);
         }
     }
 };
 
-// N tiles; first[k] is this lane's first token of tile k.
-template <int D, int R, int N>
-__device__ __forceinline__ void step_shared(State<D, R> &st, const Shared<D> (&t)[N], const int (&first)[N], bool masked, const AttnArgs &a, int lane) {
-    constexpr int W = Kv4<D>::W;
-    f32x4 s[R][2 * N];
+template <int D, int R>
+__device__ __forceinline__ void scores(f32x4 (&s)[R][2], const State<D, R> &st, const SharedK<D> &t, int lane) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int n = 0; n < D / 32; ++n) {
 #pragma unroll
-        for (int h = 0; h < 2 * N; ++h) s[r][h] = f32x4{0, 0, 0, 0};
+        for (int h = 0; h < 2; ++h) {
+            const bf16x8 k = __builtin_bit_cast(bf16x8, t.k[h][n][lane]);
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-#pragma unroll
-        for (int n = 0; n < D / 32; ++n) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bf16x8 c = __builtin_bit_cast(bf16x8, t[k].k[h][n][lane]);
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    s[r][2 * k + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c, as_bf16(st.q[r][n]), s[r][2 * k + h], 0, 0, 0);
+            for (int r = 0; r < R; ++r) {
+                const f32x4 z = {0, 0, 0, 0};
+                s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, as_bf16(st.q[r][n]), n ? s[r][h] : z, 0, 0, 0);
             }
         }
     }
-    uint32_t pw[R][N][4];
-    weights<D, R, N>(st, s, pw, first, masked, a);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        bf16x8 p[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) p[r] = as_bf16(pw[r][k]);
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-            const bf16x8 v = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(t[k].v[j][lane]));
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                st.row[r].acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[r], st.row[r].acc[j], 0, 0, 0);
-        }
-        uint32_t flag[4] = {0, 0, 0, 0};
-        bool nan_values = false;
-        if (masked) {
-            const u32x4 f = *reinterpret_cast<const u32x4 *>(t[k].flag[lane]);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) flag[n] = f[n];
-            nan_values = __any((f[0] | f[1] | f[2] | f[3]) != 0);
-        }
-        finish_step<D, R>(st, p, flag, nan_values, first[k], a);
-    }
 }
 
-// N: tiles between two barriers.
-template <int D, int R, int N>
+template <int D, int R>
 __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) {
-    __shared__ __attribute__((aligned(16))) Shared<D> buffer[2][N];
+    constexpr int W = Kv4<D>::W;
+    __shared__ __attribute__((aligned(16))) SharedK<D> ks[2];
+    __shared__ __attribute__((aligned(16))) SharedV<D> vs[2];
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     // Each XCD takes a run of workgroups, so that the row blocks that read one
     // key head find it in one L2; later rows see more tokens and begin first.
@@ -659,53 +660,65 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
     Block b, w;  // of the workgroup, of this wave
     constexpr int kRows = 16 * R;
     if (!locate(b, a, unit % a.batch, unit / a.batch, block, kWaves * kRows)) return;
+    // a wave past the last row repeats that one, and writes nothing
     const bool works = locate(w, a, b.seq, b.head, block * kWaves + wave, kRows);
     State<D, R> st;
-    if (works) begin(st, a, w, lane);
-    const int32_t *pages = a.table + (int64_t)b.seq * a.table_stride;
+    begin(st, a, w, lane);
+    const int32_t *row = a.table + (int64_t)b.seq * a.table_stride;
     const Places<D> places = Quarter<D>::places(lane, wave);
-    for (int t = b.lo; t < b.hi; t += 64) {  // 64 tiles' pages at a time
-        const int count = min(64, b.hi - t);
-        const int page = pages[(t + min(lane, count - 1)) >> a.shift];
-        const auto known = [&](int i) {
-            const int pg = __builtin_amdgcn_readlane(page, i);
-            return pg >= 0 && pg < a.pages;
-        };
-        // of the N tiles from i on, those past the last among them
+    for (int t = b.lo; t < b.hi; t += 64) {
+        const Pages pages(a, row, t, 1, b.hi, lane);
+        const auto tile = [&](int i) { return pages.tile<D>(a, b.head, i); };
         const auto masked = [&](int i) {
-            bool lost = i + N > count || (t + i) * kTile < b.seen_lo || (t + i + N) * kTile > b.seen_hi;
-#pragma unroll
-            for (int k = 0; k < N; ++k) lost |= !known(min(i + k, count - 1));
-            return lost;
+            return !pages.has(i) | ((t + i) * kTile < b.seen_lo) | ((t + i + 1) * kTile > b.seen_hi);
         };
-        Quarter<D> next[N];
-        const auto load = [&](int first) {  // past the last tile it is loaded again
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const int i = min(first + k, count - 1);
-                const int pg = known(i) ? __builtin_amdgcn_readlane(page, i) : 0;
-                const int64_t tile = (((int64_t)pg * a.kv_heads + b.head) << a.shift) + ((t + i) & ((1 << a.shift) - 1));
-                next[k].load(a.cache + tile * Kv4<D>::kBytes, places);
-            }
-        };
-        const auto turn = [&](int first, int to) {
-#pragma unroll
-            for (int k = 0; k < N; ++k) next[k].turn(buffer[to][k], masked(first), lane, wave);
-        };
-        load(0);
-        turn(0, 0);
-        load(N);
+        Quarter<D> k, v;
+        f32x4 s[R][2];
+        k.load_k(tile(0), places);
+        v.load_v(tile(0), places);
+        k.turn_k(ks[0], lane, wave);
+        if (masked(0)) v.hide(vs[0], lane, wave);
+        v.turn_v(vs[0], lane, wave);
+        k.load_k(tile(1), places);
+        v.load_v(tile(1), places);
+        k.turn_k(ks[1], lane, wave);
+        k.load_k(tile(2), places);
         __syncthreads();
-        for (int i = 0, at = 0; i < count; i += N, at ^= 1) {
-            if (i + N < count) turn(i + N, at ^ 1);
-            load(i + 2 * N);
-            if (works) {
-                int first[N];
+        scores<D, R>(s, st, ks[0], lane);
+        __syncthreads();
+        for (int i = 0; i < pages.count; ++i) {
+            const int now = i % 2;
+            const bool hidden = masked(i);
+            // tokens on a lost page are past every row's position
+            const int first = pages.has(i) ? (t + i) * kTile + lane / 16 * 8 : 0x7FFFFF00;
+            if (masked(i + 1)) v.hide(vs[1 - now], lane, wave);
+            settle<D, R>(st, s, first, hidden, a);
+            bf16x8 p[R];
+            f32x4 ahead[R][2];
+            weights<D, R>(st, s, p, a);
+            scores<D, R>(ahead, st, ks[1 - now], lane);
+            k.turn_k(ks[now], lane, wave);
+            v.turn_v(vs[1 - now], lane, wave);
+            k.load_k(tile(i + 3), places);
+            v.load_v(tile(i + 2), places);
 #pragma unroll
-                for (int k = 0; k < N; ++k)  // tokens that are not there are past every row's position
-                    first[k] = i + k < count && known(min(i + k, count - 1)) ? (t + i + k) * kTile + lane / 16 * 8 : 0x7FFFFF00;
-                step_shared<D, R, N>(st, buffer[at], first, masked(i), a, lane);
+            for (int j = 0; j < W; ++j) {
+                const bf16x8 c = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(vs[now].v[j][lane]));
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    st.row[r].acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c, p[r], st.row[r].acc[j], 0, 0, 0);
             }
+            uint32_t flag[4] = {0, 0, 0, 0};
+            bool nan_values = false;
+            if (hidden) {
+                const u32x4 f = *reinterpret_cast<const u32x4 *>(vs[now].flag[lane]);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) flag[n] = f[n];
+                nan_values = __any((f[0] | f[1] | f[2] | f[3]) != 0);
+            }
+            finish_step<D, R>(st, p, flag, nan_values, first, a);
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[r][0] = ahead[r][0], s[r][1] = ahead[r][1];
             __syncthreads();
         }
     }
@@ -871,7 +884,7 @@ struct Plan {
     int64_t units;
 };
 
-constexpr int wide_tiles(int dim) { return dim == 64 ? 4 : dim == 128 ? 2 : 1; }
+constexpr int wide_tiles(int dim) { return dim == 64 ? 3 : dim == 128 ? 2 : 1; }
 
 Plan plan(int batch, int max_q, int64_t max_kv, int64_t window, int group, int kv_heads, int dim) {
     Plan p = {};
@@ -929,7 +942,7 @@ Kernels pick_rows(const Plan &p) {
                        : p.splits <= 16 ? reinterpret_cast<const void *>(&k_kv4_join<D, R, 4, 1>)
                        : p.splits <= 64 ? reinterpret_cast<const void *>(&k_kv4_join<D, R, 16, 1>)
                                         : reinterpret_cast<const void *>(&k_kv4_join<D, R, 16, 4>);
-    if (p.wide) return {reinterpret_cast<const void *>(&k_kv4_attention_wide<D, wide_tiles(D), D == 256 ? 1 : 2>), join, items};
+    if (p.wide) return {reinterpret_cast<const void *>(&k_kv4_attention_wide<D, wide_tiles(D)>), join, items};
     if (p.waves == kWaves) return {reinterpret_cast<const void *>(&k_kv4_attention<D, R, kWaves>), join, items};
     return {reinterpret_cast<const void *>(&k_kv4_attention<D, R, 2 * kWaves>), join, items};
 }
