@@ -631,20 +631,32 @@ struct Quarter {
 };
 
 template <int D, int R>
-__device__ __forceinline__ void scores(f32x4 (&s)[R][2], const State<D, R> &st, const SharedK<D> &t, int lane) {
+__device__ __forceinline__ void scores(f32x4 (&s)[R][2], const State<D, R> &st, const bf16x8 (&k)[2][D / 32]) {
 #pragma unroll
     for (int n = 0; n < D / 32; ++n) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const bf16x8 k = __builtin_bit_cast(bf16x8, t.k[h][n][lane]);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const f32x4 z = {0, 0, 0, 0};
-                s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, as_bf16(st.q[r][n]), n ? s[r][h] : z, 0, 0, 0);
+                s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[h][n], as_bf16(st.q[r][n]), n ? s[r][h] : z, 0, 0, 0);
             }
         }
     }
 }
+
+// The order of the instructions before: after each of `products` products,
+// `others` of the vector unit, and reads of LDS beside the last ones.
+template <int products, int others, int reads>
+__device__ __forceinline__ void mix() {
+#pragma unroll
+    for (int x = 0; x < products; ++x) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, others, 0);
+        if (x >= products - reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+}
+constexpr int kWeightsMix = 5, kTurnMix = 2;
 
 template <int D, int R>
 __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) {
@@ -684,7 +696,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
         k.turn_k(ks[1], lane, wave);
         k.load_k(tile(2), places);
         __syncthreads();
-        scores<D, R>(s, st, ks[0], lane);
+        {
+            bf16x8 kf[2][D / 32];
+#pragma unroll
+            for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) kf[h][n] = __builtin_bit_cast(bf16x8, ks[0].k[h][n][lane]);
+            scores<D, R>(s, st, kf);
+        }
         __syncthreads();
         for (int i = 0; i < pages.count; ++i) {
             const int now = i % 2;
@@ -693,21 +712,33 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
             const int first = pages.has(i) ? (t + i) * kTile + lane / 16 * 8 : 0x7FFFFF00;
             if (masked(i + 1)) v.hide(vs[1 - now], lane, wave);
             settle<D, R>(st, s, first, hidden, a);
-            bf16x8 p[R];
+            // weights beside the products of the next scores, whose operands
+            // are on their way from LDS already
+            bf16x8 p[R], kf[2][D / 32], vf[W];
             f32x4 ahead[R][2];
+#pragma unroll
+            for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) kf[h][n] = __builtin_bit_cast(bf16x8, ks[1 - now].k[h][n][lane]);
+            __builtin_amdgcn_sched_barrier(0);
             weights<D, R>(st, s, p, a);
-            scores<D, R>(ahead, st, ks[1 - now], lane);
+            scores<D, R>(ahead, st, kf);
+#pragma unroll
+            for (int j = 0; j < W; ++j) vf[j] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(vs[now].v[j][lane]));
+            mix<2 * (D / 32) * R, kWeightsMix, W>();
+            __builtin_amdgcn_sched_barrier(0);
+            // the tiles after beside the output's products
             k.turn_k(ks[now], lane, wave);
             v.turn_v(vs[1 - now], lane, wave);
-            k.load_k(tile(i + 3), places);
-            v.load_v(tile(i + 2), places);
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const bf16x8 c = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(vs[now].v[j][lane]));
+            for (int j = 0; j < W; ++j)
 #pragma unroll
                 for (int r = 0; r < R; ++r)
-                    st.row[r].acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c, p[r], st.row[r].acc[j], 0, 0, 0);
-            }
+                    st.row[r].acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[j], p[r], st.row[r].acc[j], 0, 0, 0);
+            mix<W * R, kTurnMix, 0>();
+            __builtin_amdgcn_sched_barrier(0);
+            k.load_k(tile(i + 3), places);
+            v.load_v(tile(i + 2), places);
             uint32_t flag[4] = {0, 0, 0, 0};
             bool nan_values = false;
             if (hidden) {
