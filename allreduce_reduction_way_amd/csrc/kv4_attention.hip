@@ -676,25 +676,35 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
     const bool works = locate(w, a, b.seq, b.head, block * kWaves + wave, kRows);
     State<D, R> st;
     begin(st, a, w, lane);
-    const int32_t *row = a.table + (int64_t)b.seq * a.table_stride;
     const Places<D> places = Quarter<D>::places(lane, wave);
-    for (int t = b.lo; t < b.hi; t += 64) {
-        const Pages pages(a, row, t, 1, b.hi, lane);
-        const auto tile = [&](int i) { return pages.tile<D>(a, b.head, i); };
-        const auto masked = [&](int i) {
-            return !pages.has(i) | ((t + i) * kTile < b.seen_lo) | ((t + i + 1) * kTile > b.seen_hi);
-        };
-        Quarter<D> k, v;
+    // A tile's page is looked up an iteration before its address is needed, by
+    // a scalar load.  Tiles past the last are that one again, and not used.
+    typedef const __attribute__((address_space(4))) int32_t *Table;
+    const Table row = (Table)(uintptr_t)(a.table + (int64_t)b.seq * a.table_stride);
+    const auto page = [&](int t) { return row[min(t, b.hi - 1) >> a.shift]; };
+    const auto lost = [&](int pg) { return (uint32_t)pg >= (uint32_t)a.pages; };
+    const auto tile = [&](int t, int pg) {
+        const int64_t at = (((int64_t)(lost(pg) ? 0 : pg) * a.kv_heads + b.head) << a.shift) + (min(t, b.hi - 1) & ((1 << a.shift) - 1));
+        return a.cache + at * Kv4<D>::kBytes;
+    };
+    // whether tile t, on that page, has tokens that a row does not see
+    const auto masked = [&](int t, int pg) { return lost(pg) | (t * kTile < b.seen_lo) | ((t + 1) * kTile > b.seen_hi); };
+    if (b.lo < b.hi) {
+        int pg[5];  // of tiles t .. t + 4
+#pragma unroll
+        for (int i = 0; i < 5; ++i) pg[i] = page(b.lo + i);
+        Quarter<D> k, v, ahead_k;
         f32x4 s[R][2];
-        k.load_k(tile(0), places);
-        v.load_v(tile(0), places);
+        const uint8_t *next = tile(b.lo + 2, pg[2]);  // of the values that are loaded next
+        k.load_k(tile(b.lo, pg[0]), places);
+        v.load_v(tile(b.lo, pg[0]), places);
+        ahead_k.load_k(tile(b.lo + 1, pg[1]), places);
         k.turn_k(ks[0], lane, wave);
-        if (masked(0)) v.hide(vs[0], lane, wave);
+        if (masked(b.lo, pg[0])) v.hide(vs[0], lane, wave);
         v.turn_v(vs[0], lane, wave);
-        k.load_k(tile(1), places);
-        v.load_v(tile(1), places);
-        k.turn_k(ks[1], lane, wave);
-        k.load_k(tile(2), places);
+        v.load_v(tile(b.lo + 1, pg[1]), places);
+        k.load_k(next, places);
+        ahead_k.turn_k(ks[1], lane, wave);
         __syncthreads();
         {
             bf16x8 kf[2][D / 32];
@@ -705,12 +715,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
             scores<D, R>(s, st, kf);
         }
         __syncthreads();
-        for (int i = 0; i < pages.count; ++i) {
-            const int now = i % 2;
-            const bool hidden = masked(i);
+        for (int t = b.lo, now = 0; t < b.hi; ++t, now ^= 1) {
+            const bool hidden = masked(t, pg[0]);
             // tokens on a lost page are past every row's position
-            const int first = pages.has(i) ? (t + i) * kTile + lane / 16 * 8 : 0x7FFFFF00;
-            if (masked(i + 1)) v.hide(vs[1 - now], lane, wave);
+            const int first = lost(pg[0]) ? 0x7FFFFF00 : t * kTile + lane / 16 * 8;
+            if (masked(t + 1, pg[1])) v.hide(vs[1 - now], lane, wave);
             settle<D, R>(st, s, first, hidden, a);
             // weights beside the products of the next scores, whose operands
             // are on their way from LDS already
@@ -737,8 +746,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
                     st.row[r].acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[j], p[r], st.row[r].acc[j], 0, 0, 0);
             mix<W * R, kTurnMix, 0>();
             __builtin_amdgcn_sched_barrier(0);
-            k.load_k(tile(i + 3), places);
-            v.load_v(tile(i + 2), places);
+            v.load_v(next, places);
+            next = tile(t + 3, pg[3]);
+            k.load_k(next, places);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pg[i] = pg[i + 1];
+            pg[4] = page(t + 5);
             uint32_t flag[4] = {0, 0, 0, 0};
             bool nan_values = false;
             if (hidden) {
