@@ -645,19 +645,6 @@ __device__ __forceinline__ void scores(f32x4 (&s)[R][2], const State<D, R> &st, 
     }
 }
 
-// The order of the instructions before: after each of `products` products,
-// `others` of the vector unit, and reads of LDS beside the last ones.
-template <int products, int others, int reads>
-__device__ __forceinline__ void mix() {
-#pragma unroll
-    for (int x = 0; x < products; ++x) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, others, 0);
-        if (x >= products - reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    }
-}
-constexpr int kWeightsMix = 5, kTurnMix = 2;
-
 template <int D, int R>
 __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) {
     constexpr int W = Kv4<D>::W;
@@ -730,12 +717,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
 #pragma unroll
                 for (int h = 0; h < 2; ++h) kf[h][n] = __builtin_bit_cast(bf16x8, ks[1 - now].k[h][n][lane]);
             __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(1);  // before the wave that waits or looks pages up
             weights<D, R>(st, s, p, a);
             scores<D, R>(ahead, st, kf);
 #pragma unroll
             for (int j = 0; j < W; ++j) vf[j] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(vs[now].v[j][lane]));
-            mix<2 * (D / 32) * R, kWeightsMix, W>();
-            __builtin_amdgcn_sched_barrier(0);
             // the tiles after beside the output's products
             k.turn_k(ks[now], lane, wave);
             v.turn_v(vs[1 - now], lane, wave);
@@ -744,8 +730,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
 #pragma unroll
                 for (int r = 0; r < R; ++r)
                     st.row[r].acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[j], p[r], st.row[r].acc[j], 0, 0, 0);
-            mix<W * R, kTurnMix, 0>();
-            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(0);
             v.load_v(next, places);
             next = tile(t + 3, pg[3]);
             k.load_k(next, places);
