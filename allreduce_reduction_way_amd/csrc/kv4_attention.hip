@@ -51,7 +51,7 @@ struct AttnArgs {
     int64_t table_stride;
     int tokens, batch, heads, kv_heads, group;
     int pages, per_seq, shift;  // pages of the cache, entries of a table row, log2 of tiles a page
-    int window, max_q;
+    int window, max_q;  // window: 2^31 - 1 where there is none
     int blocks;  // row blocks of a sequence's key head
     int splits;  // workgroups that share a row block, at most
     int chunk;   // tiles of such a workgroup, at least
@@ -59,6 +59,17 @@ struct AttnArgs {
     int vec;
     float c;  // scale log2(e)
 };
+
+// The kernel's arguments, read again: what is needed after a sweep is not kept
+// in scalar registers during it.  (They did not all fit: those of the drafted
+// tokens' kernel were moved to and from vector registers some thirty times a
+// tile.)
+__device__ __forceinline__ const AttnArgs &again() {
+    typedef const __attribute__((address_space(4))) AttnArgs *Args;
+    Args p = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const AttnArgs *)p;
+}
 
 // The codes and scales that a lane takes of one tile.  With r = lane % 16 and
 // a = lane / 16, of K: D/4 channels of tokens r / 4 * 8 + r % 4 and four on,
@@ -208,7 +219,7 @@ __device__ __forceinline__ int here(int v) {
 }
 
 __device__ __forceinline__ bool sees(int pos, int token, int window) {
-    return token <= pos && (window == 0 || pos - token < window);
+    return (uint32_t)(pos - token) < (uint32_t)window;  // a token past pos: 2^31 or more
 }
 
 // Scores of a tile, s[r][h][i] of row tile r's row lane % 16 against token
@@ -372,17 +383,17 @@ __device__ __forceinline__ bool locate(Block &b, const AttnArgs &a, int seq, int
     const int q0 = min(max(a.q_start[seq], 0), a.tokens), q1 = min(max(a.q_start[seq + 1], q0), a.tokens);
     b.seq = seq, b.head = head;
     b.q0 = q0, b.len = q1 - q0;
-    // 31 bits hold the tokens of a table row: checked on the host
+    // 30 bits hold the tokens of a table row: checked on the host
     b.n = min(max(a.kv_len[seq], 0), a.per_seq << (a.shift + 5));
     b.rows = min(b.len, a.max_q) * a.group;
     b.first = block * size;
     if (b.first >= b.rows) return false;
     const int lowest = b.n - b.len + b.first / a.group;
     const int highest = b.n - b.len + (min(b.rows, b.first + size) - 1) / a.group;
-    const int from = a.window ? (int)max((int64_t)0, (int64_t)lowest - a.window + 1) : 0;
+    const int from = (int)max((int64_t)0, (int64_t)lowest - a.window + 1);
     b.lo = from / kTile;
     b.hi = highest >= from ? highest / kTile + 1 : b.lo;
-    b.seen_lo = a.window ? (int)max((int64_t)0, (int64_t)highest - a.window + 1) : 0;
+    b.seen_lo = (int)max((int64_t)0, (int64_t)highest - a.window + 1);
     b.seen_hi = lowest + 1;
     return true;
 }
@@ -402,7 +413,7 @@ __device__ __forceinline__ void begin(State<D, R> &st, const AttnArgs &a, const 
 #pragma unroll
             for (int e = 0; e < 4; ++e) st.q[r][n][e] = w[e];
         }
-        st.pos[r] = b.n - b.len + i;
+        st.pos[r] = max(b.n - b.len + i, -1);  // before all tokens
         st.row[r].clear();
     }
 }
@@ -756,7 +767,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
     for (int r = 0; r < R; ++r) {
         st.row[r].l += __shfl_xor(st.row[r].l, 16);
         st.row[r].l += __shfl_xor(st.row[r].l, 32);
-        finish(st.row[r], a, w, r, lane);
+        finish(st.row[r], again(), w, r, lane);
     }
 }
 
@@ -796,14 +807,15 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv4_attention(AttnArgs a) {
         sweep<D, R, kRing<D, R>>(st, a, b, lo + wave, min(b.hi, lo + chunk), NW, lane);
         ex.leave(st.row, lane, wave);
     }
+    const AttnArgs &z = again();
     const int rows = min(b.rows - b.first, 16 * R);
     if (count == 1) {
         ex.join(rows, lane, wave, [&](int r, int j, const f32x4(&sum)[2], float m, float l, float d) {
-            put_pair<D>(a, b, r, j, sum, m, l, d, lane);
+            put_pair<D>(z, b, r, j, sum, m, l, d, lane);
         });
         return;
     }
-    float *to = a.part + ((int64_t)unit * a.splits + split) * P::kFloats;
+    float *to = z.part + ((int64_t)unit * z.splits + split) * P::kFloats;
     ex.join(rows, lane, wave, [&](int r, int j, const f32x4(&sum)[2], float m, float l, float d) {
         f32x4 *v = reinterpret_cast<f32x4 *>(to) + (r * P::W + j) * 64 + lane;
         v[0] = sum[0];
@@ -1010,7 +1022,7 @@ int ar_kv4_attention(ar_rows q, const void *cache, const void *page_table, int64
     int shift = 0;
     if (!valid_sizes(batch, tokens, max_q, max_kv, heads, kv_heads, dim) ||
         !kv4_shape(kv_heads, dim, pages, page_size, &shift) || pages_per_seq < 0 ||
-        pages_per_seq > 0x7FFFFFFF / page_size || table_stride < 0 || window < 0 ||
+        pages_per_seq > 0x3FFFFFFF / page_size || table_stride < 0 || window < 0 ||
         window > 0x7FFFFFFF || !(scale > 0) || !(scale <= 3.0e38f) ||
         table_stride > ((int64_t)1 << 40) / (batch + 1))
         return AR_EINVAL;
@@ -1046,7 +1058,7 @@ int ar_kv4_attention(ar_rows q, const void *cache, const void *page_table, int64
     a.table_stride = table_stride;
     a.tokens = (int)tokens, a.batch = (int)batch, a.heads = heads, a.kv_heads = kv_heads, a.group = heads / kv_heads;
     a.pages = (int)pages, a.per_seq = pages ? (int)pages_per_seq : 0, a.shift = shift - 5;
-    a.window = (int)window, a.max_q = (int)max_q;
+    a.window = window ? (int)window : 0x7FFFFFFF, a.max_q = (int)max_q;
     a.blocks = p.blocks, a.splits = p.splits, a.chunk = p.chunk, a.waves = p.waves;
     a.vec = rq.vec() && ro.vec();
     a.c = scale * kLog2e;

@@ -384,6 +384,7 @@ int ar_kv4_read(const void *cache, const void *slots, ar_rows k_out, ar_rows v_o
  *               token j of a sequence is on the page of entry j / page_size.
  *               Tokens past the last entry, or on a page outside the cache,
  *               are not seen.  Entries past a sequence's tokens are not read.
+ *               pages_per_seq * page_size is below 2^30.
  *   q_start     batch + 1 int32, rising; kv_len batch int32.
  *   lse         (tokens, heads) floats.
  *   workspace   ar_kv4_attention_workspace bytes of any contents.  Two calls
