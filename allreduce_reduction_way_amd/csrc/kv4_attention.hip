@@ -934,11 +934,15 @@ Plan plan(int batch, int max_q, int64_t max_kv, int64_t window, int group, int k
     p.tiles = (int)(tiles < most ? tiles : most);
     p.splits = p.chunk = 1;
     p.waves = kWaves;
-    // rows enough for four waves on half of the compute units
+    // Rows enough for two workgroups on each compute unit.  Where there are
+    // fewer, a wave of this kernel waits for each tile's conversion, and the
+    // split kernel is faster: one sequence of 4096 tokens, 8 key heads of 128,
+    // four queries to each: 1024 queries take 122 us here and 96 there, 2048
+    // 148 and 161.
     const int wide = kWaves * wide_tiles(dim);
     p.blocks = (int)((tiles + wide - 1) / wide);
     p.units = (int64_t)batch * kv_heads * p.blocks;
-    p.wide = tiles >= wide && p.units >= kCus / 2;
+    p.wide = tiles >= wide && p.units >= 2 * kCus;
     if (p.wide) return p;
     p.blocks = (int)((tiles + p.tiles - 1) / p.tiles);
     p.units = (int64_t)batch * kv_heads * p.blocks;
@@ -947,11 +951,12 @@ Plan plan(int batch, int max_q, int64_t max_kv, int64_t window, int group, int k
     const bool few = p.units < 2 * kCus;
     p.waves = few ? 2 * kWaves : kWaves;
     const int64_t fill = (few ? 1 : 3) * kCus;  // workgroups that the device runs at once
-    // one round of workgroups while there is a tile for each wave, and up to
-    // four, which even out ragged lengths, while each wave has kLong tiles
+    // One round of workgroups while there is a tile for each wave, and up to
+    // four, which even out ragged lengths, while each wave has kLong tiles and
+    // a sequence's rows are one block (with more, its results outweigh that).
     int64_t s = fill / p.units;
     if (s > steps / p.waves) s = steps / p.waves;
-    int64_t more = !few ? 1 : (4 * fill + p.units - 1) / p.units;
+    int64_t more = !few || p.blocks > 1 ? 1 : (4 * fill + p.units - 1) / p.units;
     if (more > steps / (p.waves * kLong)) more = steps / (p.waves * kLong);
     if (s < more) s = more;
     if (s > kSplits) s = kSplits;

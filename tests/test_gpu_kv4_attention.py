@@ -136,7 +136,9 @@ def test_parity(shape, odd):
 
 
 @pytest.mark.parametrize("D,heads,hk,m,n,window", [(64, 16, 8, 700, 720, 0), (128, 32, 8, 600, 800, 0), (128, 8, 8, 1100, 1111, 90),
-                                                  (256, 16, 8, 300, 333, 0)])
+                                                  (256, 16, 8, 300, 333, 0), (64, 16, 16, 2100, 2111, 0),
+                                                  (128, 32, 8, 1100, 1300, 0), (128, 32, 8, 1100, 1111, 90),
+                                                  (256, 16, 8, 1100, 1133, 0)])
 def test_prompts(D, heads, hk, m, n, window):
     """Enough rows that every wave has its own."""
     announce(f"kv4_attention prompt {D} {heads} {hk} {m} {n} {window}")
@@ -349,7 +351,8 @@ def test_a_cache_past_4_gib():
     assert np.array_equal(c.kc.shape, (c.pages, hk, page // 32, 32, D))
 
 
-@pytest.mark.parametrize("D,heads,hk,m,n", [(64, 16, 8, 520, 700), (128, 32, 8, 300, 300), (256, 16, 8, 260, 333)])
+@pytest.mark.parametrize("D,heads,hk,m,n", [(64, 16, 8, 520, 700), (128, 32, 8, 300, 300), (256, 16, 8, 260, 333),
+                                               (64, 48, 16, 1100, 1200), (128, 32, 8, 1100, 1100), (256, 16, 8, 1100, 1133)])
 def test_prompts_with_nan_and_lost_pages(D, heads, hk, m, n):
     """Many rows: NaN values that some rows of a tile see, NaN past the tokens,
     pages outside the cache."""
