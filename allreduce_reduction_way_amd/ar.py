@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of libar.so.  The functions carry the C names.  Buffer arguments may
 be torch CUDA tensors (bf16 / int16 / uint16 elements, uint8 for scratch and
-control blocks) or raw device addresses as ints; ``stream`` may be None (the
+control blocks) or raw device addresses as ints (the attention operators take
+tensors alone); ``stream`` may be None (the
 current torch stream), a ``torch.cuda.Stream`` or a raw hipStream_t int.
 A non-zero status raises :class:`ArError`.  The library is loaded on first
 use; if it is not built, that first call raises: there is no fallback.

@@ -24,10 +24,21 @@
 // sixteen to tokens 8 a + i and 8 a + 4 + i: P never moves between lanes.  The
 // statistics of a row are in the lanes that hold its output, too.
 //
-// A step of one sequence reads its cache once for few rows: bound by memory.
-// The waves of a workgroup then take the tiles of a range of tokens in turn
-// and join their results through LDS, several workgroups share a sequence, and
-// the last of them to arrive joins theirs.
+// Three kernels, by the number of rows alone (plan() below):
+//
+// k_kv4_attention, few rows: bound by the cache's bytes, or by latency where
+// there are few of those.  The waves of a workgroup take the tiles of a range of
+// tokens in turn and join their results through LDS, and several workgroups
+// share a sequence.  128 sequences of 2048 to 8192 tokens, 8 key heads of 128:
+// 731 MB in 146 us, 5.0 TB/s (a copy of 1 GiB runs at 5.1); one sequence of
+// 200003 tokens, one key head: 27 MB in 14 us with the join.
+//
+// k_kv4_join joins the ranges of a row block.
+//
+// k_kv4_attention_wide, many rows: bound by the issue of vector and matrix
+// instructions.  Two chunks of 2048 queries over 8192 and fewer tokens, 32
+// heads: 468 GFLOP in 470 us, 0.99 PFLOP/s (a library product of 8192^3 reaches
+// 1.16); the matrix unit is busy for 42% of the time.
 #include "host.h"
 #include "kv4.h"
 #include "rows.h"
@@ -206,9 +217,10 @@ struct State {
 // maximum by less, so that rescaling the output is rare.
 constexpr float kSlack = 8.0f;
 
-// Tiles that a wave of the split kernel has in its registers.
-template <int D, int R>
-constexpr int kRing = D == 64 ? 3 : 2;
+// Tiles that a wave of the split kernel has in its registers: the one that it
+// works on and the next.  A third gained nothing: drafted tokens took 19.0 us
+// with it and 18.5 without, the long sequence 10.3 and 9.4.
+constexpr int kRing = 2;
 
 // The value, which the compiler takes for another one: what is computed from it
 // stays in the branch where it is needed.  (Comparisons of masks were done for
@@ -804,7 +816,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_kv4_attention(AttnArgs a) {
         State<D, R> st;
         begin(st, a, b, lane);
         const int lo = b.lo + split * chunk;
-        sweep<D, R, kRing<D, R>>(st, a, b, lo + wave, min(b.hi, lo + chunk), NW, lane);
+        sweep<D, R, kRing>(st, a, b, lo + wave, min(b.hi, lo + chunk), NW, lane);
         ex.leave(st.row, lane, wave);
     }
     const AttnArgs &z = again();
@@ -946,17 +958,20 @@ Plan plan(int batch, int max_q, int64_t max_kv, int64_t window, int group, int k
     if (p.wide) return p;
     p.blocks = (int)((tiles + p.tiles - 1) / p.tiles);
     p.units = (int64_t)batch * kv_heads * p.blocks;
+    // Row blocks enough that two of their workgroups are on each compute unit:
+    // none is split, and a third fits beside them.
+    if (p.units >= 2 * kCus) return p;
+    p.waves = 2 * kWaves;
     if (window && max_kv > window + max_q) max_kv = window + max_q;
     const int64_t steps = (max_kv + kTile - 1) / kTile;
-    const bool few = p.units < 2 * kCus;
-    p.waves = few ? 2 * kWaves : kWaves;
-    const int64_t fill = (few ? 1 : 3) * kCus;  // workgroups that the device runs at once
     // One round of workgroups while there is a tile for each wave, and up to
     // four, which even out ragged lengths, while each wave has kLong tiles and
     // a sequence's rows are one block (with more, its results outweigh that).
-    int64_t s = fill / p.units;
+    // Fifteen sequences of up to 108125 tokens, four key heads: 61 us in four
+    // rounds, 93 in one.
+    int64_t s = kCus / p.units;
     if (s > steps / p.waves) s = steps / p.waves;
-    int64_t more = !few || p.blocks > 1 ? 1 : (4 * fill + p.units - 1) / p.units;
+    int64_t more = p.blocks > 1 ? 1 : (4 * kCus + p.units - 1) / p.units;
     if (more > steps / (p.waves * kLong)) more = steps / (p.waves * kLong);
     if (s < more) s = more;
     if (s > kSplits) s = kSplits;
