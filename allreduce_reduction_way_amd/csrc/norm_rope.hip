@@ -16,7 +16,7 @@
 // (pairs side by side) or in two lanes of the row, which exchange the packed
 // bf16 words (half the exchanges of the widened values).  The heads of one
 // token share the wave's cosines and sines, so a wave stays on one token and
-// takes several steps of rows.  Measured: 8192 tokens of 64 heads of 128 in 49.5
+// takes several steps of rows.  Measured: 8192 tokens of 64 heads of 128 in 49
 // us, 5.5 TB/s; the gradient of 4096 tokens of 72 heads in 49.6 us, 4.6 TB/s,
 // 4.6 us of them the sums of the weights' gradients.
 #include "host.h"
@@ -203,6 +203,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_rope(NormArgs a) {
             if (first != sh.begin) load(first);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                if (first + u >= sh.end) break;
                 float f[8], m[8];
                 widen(x[u], f);
                 widen(turn.mates(x[u]), m);
@@ -212,7 +213,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_rope(NormArgs a) {
                 const float r = rsqrtf(row_sum<kLanes>(ss) * (1.0f / D) + a.eps);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] = (f[e] * own[e] + m[e] * mate[e]) * r;
-                if (at(first, u) < sh.heads && first + u < sh.end) {
+                if (at(first, u) < sh.heads) {
                     const u32x4 o = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
                     store_row<VEC, NT>(sh.out + at(first, u) * sh.out_hs + li * 8, o);
                 }
@@ -442,11 +443,13 @@ int ar_qk_norm_rope(ar_rows q, ar_rows k, const void *q_weight, const void *k_we
     a.tokens = tokens, a.table = table, a.hq = heads, a.hk = kv_heads;
     a.rotated = rotated, a.interleaved = interleaved != 0, a.eps = eps;
     count_steps(a, dim);
-    // Few rows: a wave for each step, since what a wave does takes longer than
-    // its share of the memory.  Many: as many steps to a wave as leave sixteen
-    // waves for each SIMD (eight at once: 53.6 us for 268 MB against 57.7 with
-    // eight in all), which read their token's cosines and sines once.
-    const bool few = tokens * a.steps <= 8192;
+    // Few rows, or few to a token: a wave for each step, since what a wave does
+    // takes longer than its share of the memory (8000 tokens of 16 heads of 64:
+    // 9.7 us, and 11.2 with both steps to a wave).  Many: as many steps to a
+    // wave as leave sixteen waves for each SIMD (eight at once: 53.6 us for 268
+    // MB against 57.7 with eight in all), which read their token's cosines and
+    // sines once.
+    const bool few = tokens * a.steps <= 8192 || a.steps <= 2;
     const int64_t parts = few ? a.steps : (16384 + tokens - 1) / tokens;
     a.per = (int)((a.steps + parts - 1) / parts);
     if (!few) a.per = (a.per + 3) / 4 * 4;
