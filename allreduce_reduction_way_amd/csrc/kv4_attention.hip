@@ -37,8 +37,8 @@
 //
 // k_kv4_attention_wide, many rows: bound by the issue of vector and matrix
 // instructions.  Two chunks of 2048 queries over 8192 and fewer tokens, 32
-// heads: 468 GFLOP in 470 us, 0.99 PFLOP/s (a library product of 8192^3 reaches
-// 1.16); the matrix unit is busy for 42% of the time.
+// heads: 468 GFLOP in 467 us, 1.00 PFLOP/s (a library product of 8192^3 reaches
+// 1.16); the matrix unit is busy for 43% of the time.
 #include "host.h"
 #include "kv4.h"
 #include "rows.h"
@@ -234,18 +234,23 @@ __device__ __forceinline__ bool sees(int pos, int token, int window) {
     return (uint32_t)(pos - token) < (uint32_t)window;  // a token past pos: 2^31 or more
 }
 
+// The token that a lane's score n = 4 h + i belongs to, of its eight from
+// `first` on: pairs of them begin at pair -turn, which is 0 for the split
+// kernel and lane / 16 for the one of many rows (see Quarter).
+__device__ __forceinline__ int place(int first, int n, int turn) { return first + ((n / 2 - turn) & 3) * 2 + n % 2; }
+
 // Scores of a tile, s[r][h][i] of row tile r's row lane % 16 against token
-// first + 4 h + i, made ready for weights(): tokens that a row does not see are
+// place(first, 4 h + i, turn), made ready for weights(): tokens that a row does not see are
 // taken out, and its maximum moves if they outgrow it.
 template <int D, int R>
-__device__ __forceinline__ void settle(State<D, R> &st, f32x4 (&s)[R][2], int first, bool masked, const AttnArgs &a) {
+__device__ __forceinline__ void settle(State<D, R> &st, f32x4 (&s)[R][2], int first, int turn, bool masked, const AttnArgs &a) {
     if (masked) {
         const int token = here(first);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int n = 0; n < 8; ++n)
-                if (!sees(st.pos[r], token + n, a.window)) s[r][n / 4][n % 4] = kNegInf;
+                if (!sees(st.pos[r], place(token, n, turn), a.window)) s[r][n / 4][n % 4] = kNegInf;
     }
     float top[R];
     bool more = false;
@@ -291,7 +296,7 @@ __device__ __forceinline__ void weights(State<D, R> &st, const f32x4 (&s)[R][2],
 
 // What else a tile adds to the running results.
 template <int D, int R>
-__device__ __forceinline__ void finish_step(State<D, R> &st, const bf16x8 (&p)[R], const uint32_t (&flag)[4], bool nan_values, int first, const AttnArgs &a) {
+__device__ __forceinline__ void finish_step(State<D, R> &st, const bf16x8 (&p)[R], const uint32_t (&flag)[4], bool nan_values, int first, int turn, const AttnArgs &a) {
     constexpr int W = Kv4<D>::W;
     // The output is divided by the sum of the rounded weights, so that a row
     // that few tokens dominate keeps no error of their rounding; the matrix
@@ -307,7 +312,7 @@ __device__ __forceinline__ void finish_step(State<D, R> &st, const bf16x8 (&p)[R
             const int token = here(first);
 #pragma unroll
             for (int n = 0; n < 8; ++n)
-                if (sees(st.pos[r], token + n, a.window)) seen[n / 2] |= 0x3F80u << (n % 2 * 16);
+                if (sees(st.pos[r], place(token, n, turn), a.window)) seen[n / 2] |= 0x3F80u << (n % 2 * 16);
             const f32x4 z = {0, 0, 0, 0};
             const f32x4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(flag), as_bf16(seen), z, 0, 0, 0);
 #pragma unroll
@@ -358,7 +363,7 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, boo
         }
     }
     const int first = index * kTile + lane / 16 * 8;  // this lane's first token
-    settle<D, R>(st, s, first, masked, a);
+    settle<D, R>(st, s, first, 0, masked, a);
     bf16x8 p[R];
     weights<D, R>(st, s, p, a);
 #pragma unroll
@@ -378,7 +383,7 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, boo
             for (int i = 0; i < 2; ++i)
                 st.row[r].acc[j + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(v[i]), p[r], st.row[r].acc[j + i], 0, 0, 0);
     }
-    finish_step<D, R>(st, p, flag, nan_values, first, a);
+    finish_step<D, R>(st, p, flag, nan_values, first, 0, a);
 }
 
 // The rows of a block, where they lie, and the tiles that they see.
@@ -595,6 +600,12 @@ struct SharedV {
 };
 
 // A wave's quarter of a tile's keys, or values, as it lies in the cache.
+//
+// The lanes' pairs of tokens are turned by lane / 16 places in LDS, so that the
+// sixty-four words that a wave writes of a pair fall on as many banks (they
+// fell on sixteen, and conflicts were a third of LDS's time: the chunked prompts
+// took 567 us traced, and 547 without them).  K's tokens are taken in that
+// order, too, which leaves the weights in it.
 template <int D>
 struct Quarter {
     static constexpr int kWords = D / 64;
@@ -606,8 +617,9 @@ struct Quarter {
         using L = Kv4<D>;
         const int r = lane % 16, q = lane / 16, h = wave % 2, part = wave / 2;
         Places<D> at(lane);
-        at.k = L::k_code(r / 4 * 8 + h * 4 + r % 4, D == 64 ? q * 16 + part * 8 : D == 128 ? q * 32 + part * 16 : part * 128 + q * 32);
-        at.ks += h + (D == 256 ? part * 128 : 0);
+        const int token = place(r / 4 * 8, h * 4 + r % 4, r / 4);
+        at.k = L::k_code(token, D == 64 ? q * 16 + part * 8 : D == 128 ? q * 32 + part * 16 : part * 128 + q * 32);
+        at.ks = L::k_scale(token, D == 64 ? q / 2 : D == 128 ? q : part * 4 + q);
         at.v += wave * L::W;
         at.vs += wave * 2;
         return at;
@@ -637,7 +649,7 @@ struct Quarter {
         uint32_t f = 0;
         if ((scale & 255u) == 255u) f |= 0x3F80u, scale &= 0xFF00u;
         if (scale >> 8 == 255u) f |= 0x3F800000u, scale &= 0xFFu;
-        to.flag[lane][wave] = f;
+        to.flag[lane][(wave + lane / 16) % 4] = f;
     }
     __device__ __forceinline__ void turn_v(SharedV<D> &to, int lane, int wave) const {
         constexpr int W = Kv4<D>::W;
@@ -647,8 +659,8 @@ struct Quarter {
         for (int j = 0; j < W; j += 2) {
             const int b0 = j / 2, b1 = b0 + W / 2;
             const uint32_t x = kv4_pair(w[b0 / 4], s0, b0 % 4), y = kv4_pair(w[b1 / 4], s1, b1 % 4);
-            to.v[j][lane][wave] = __builtin_amdgcn_perm(y, x, 0x05040100u);
-            to.v[j + 1][lane][wave] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+            to.v[j][lane][(wave + lane / 16) % 4] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+            to.v[j + 1][lane][(wave + lane / 16) % 4] = __builtin_amdgcn_perm(y, x, 0x07060302u);
         }
     }
 };
@@ -730,7 +742,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
             // tokens on a lost page are past every row's position
             const int first = lost(pg[0]) ? 0x7FFFFF00 : t * kTile + lane / 16 * 8;
             if (masked(t + 1, pg[1])) v.hide(vs[1 - now], lane, wave);
-            settle<D, R>(st, s, first, hidden, a);
+            settle<D, R>(st, s, first, lane / 16, hidden, a);
             // weights beside the products of the next scores, whose operands
             // are on their way from LDS already
             bf16x8 p[R], kf[2][D / 32], vf[W];
@@ -768,7 +780,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
                 for (int n = 0; n < 4; ++n) flag[n] = f[n];
                 nan_values = __any((f[0] | f[1] | f[2] | f[3]) != 0);
             }
-            finish_step<D, R>(st, p, flag, nan_values, first, a);
+            finish_step<D, R>(st, p, flag, nan_values, first, lane / 16, a);
 #pragma unroll
             for (int r = 0; r < R; ++r) s[r][0] = ahead[r][0], s[r][1] = ahead[r][1];
             __syncthreads();
