@@ -12,6 +12,9 @@ namespace ar {
 constexpr int kTile = 32;    // tokens of a tile
 constexpr int kGroup = 32;   // channels that share a scale
 constexpr int kNanScale = 255;
+// From this scale on, 2^126, a group's values may be infinities or NaN: codes of
+// 4 and more go beyond bf16.  Those that are written end at 252.
+constexpr uint32_t kWildScale = 253;
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 

@@ -170,10 +170,10 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, r);
 }
 
-// A byte of 255 among four.
-__device__ __forceinline__ bool any_nan_scale(uint32_t w) {
-    const uint32_t z = ~w;
-    return ((z - 0x01010101u) & ~z & 0x80808080u) != 0;
+// A byte from kWildScale on among four: one of their complements below 3.
+__device__ __forceinline__ bool any_wild_scale(uint32_t w) {
+    static_assert(kWildScale == 253, "the complement's bound");
+    return ((~w - 0x03030303u) & w & 0x80808080u) != 0;
 }
 
 // A row tile's running result: the maximum (in units of log2) and the sum of
@@ -331,15 +331,16 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, boo
     constexpr int W = Kv4<D>::W;
     using T = Tile<D>;
     bool nan_values = false;
-    uint32_t flag[4] = {0, 0, 0, 0};  // 1 for each token whose V scale stands for NaN
+    uint32_t flag[4] = {0, 0, 0, 0};  // 1 for each token whose V scale is wild
     if (masked) {
         // a token that a row does not see adds nothing to it, whatever V holds:
-        // NaNs are taken out here and given to the rows that see them
-        nan_values = __any(any_nan_scale(t.vs[0]) || any_nan_scale(t.vs[1]));
+        // what could be infinite or NaN (0 times it is NaN) is taken out here,
+        // and the rows that see it get NaN
+        nan_values = __any(any_wild_scale(t.vs[0]) || any_wild_scale(t.vs[1]));
         if (nan_values) {
 #pragma unroll
             for (int n = 0; n < 8; ++n)
-                if (((t.vs[n / 4] >> (n % 4 * 8)) & 255u) == 255u) {
+                if (((t.vs[n / 4] >> (n % 4 * 8)) & 255u) >= kWildScale) {
                     flag[n / 2] |= 0x3F80u << (n % 2 * 16);
                     t.vs[n / 4] &= ~(255u << (n % 4 * 8));
                 }
@@ -596,7 +597,7 @@ template <int D>
 struct SharedV {
     static constexpr int W = Kv4<D>::W;
     uint32_t v[W][64][4];
-    uint32_t flag[64][4];  // of a masked tile: tokens whose V scale stands for NaN
+    uint32_t flag[64][4];  // of a masked tile: tokens whose V scale is wild
 };
 
 // A wave's quarter of a tile's keys, or values, as it lies in the cache.
@@ -644,11 +645,12 @@ struct Quarter {
             to.k[wave % 2][wave / 2 * kWords + n][lane] = t;
         }
     }
-    // Values that are NaN are taken out of a masked tile, and flagged.
+    // Values that could be infinite or NaN are taken out of a masked tile, and
+    // flagged.
     __device__ __forceinline__ void hide(SharedV<D> &to, int lane, int wave) {
         uint32_t f = 0;
-        if ((scale & 255u) == 255u) f |= 0x3F80u, scale &= 0xFF00u;
-        if (scale >> 8 == 255u) f |= 0x3F800000u, scale &= 0xFFu;
+        if ((scale & 255u) >= kWildScale) f |= 0x3F80u, scale &= 0xFF00u;
+        if (scale >> 8 >= kWildScale) f |= 0x3F800000u, scale &= 0xFFu;
         to.flag[lane][(wave + lane / 16) % 4] = f;
     }
     __device__ __forceinline__ void turn_v(SharedV<D> &to, int lane, int wave) const {

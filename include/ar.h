@@ -344,8 +344,11 @@ int ar_qk_norm_rope_bwd(ar_rows q_grad, ar_rows k_grad, ar_rows q, ar_rows k, co
  * Codes are E2M1 (values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), two in a
  * byte, the even channel in the low half.  32 channels of a token share the
  * scale 2^(byte - 127); 255 stands for a group that held an infinity or a NaN:
- * all its values are NaN (and ar_kv4_write leaves zeros for its codes).  Places in a tile, for token t, channel c, group
- * g = c / 32, W = dim / 16 and G = dim / 32:
+ * all its values are NaN (and ar_kv4_write leaves zeros for its codes).  No
+ * other byte below 2 or above 252 is written.  Where memory that was never
+ * written holds one, what a read or a query that sees it gets in the group's
+ * channels (in all of them, for a key) is not specified.  Places in a tile, for
+ * token t, channel c, group g = c / 32, W = dim / 16 and G = dim / 32:
  *     K code byte   t dim/2 + c/2
  *     V code byte   16 dim + ((t/8 16 + c/W) 8 + t%8) W/2 + c%W/2
  *     K scale byte  32 dim + (g 16 + t/8 4 + t%4) 2 + t%8/4
@@ -377,7 +380,7 @@ int ar_kv4_read(const void *cache, const void *slots, ar_rows k_out, ar_rows v_o
  * those of j > p - window.
  *     out = sum_j softmax_j(scale q . k_j) v_j,  lse = log sum_j exp(scale q . k_j)
  * A query that sees nothing gets zeros and -infinity.  A token that a query
- * does not see adds nothing to it, whatever the cache holds there.
+ * does not see adds nothing to it, whatever bytes the cache holds there.
  *   q, out      (tokens, heads, dim); query head h reads key head
  *               h / (heads / kv_heads).
  *   page_table  (batch, pages_per_seq) int32 with rows table_stride apart:
