@@ -231,7 +231,7 @@ __device__ __forceinline__ int here(int v) {
 }
 
 __device__ __forceinline__ bool sees(int pos, int token, int window) {
-    return (uint32_t)(pos - token) < (uint32_t)window;  // a token past pos: 2^31 or more
+    return (uint32_t)(pos - token) < (uint32_t)window;  // a token past pos: 2^31 or more; window 0: none
 }
 
 // The token that a lane's score n = 4 h + i belongs to, of its eight from
@@ -243,14 +243,14 @@ __device__ __forceinline__ int place(int first, int n, int turn) { return first 
 // place(first, 4 h + i, turn), made ready for weights(): tokens that a row does not see are
 // taken out, and its maximum moves if they outgrow it.
 template <int D, int R>
-__device__ __forceinline__ void settle(State<D, R> &st, f32x4 (&s)[R][2], int first, int turn, bool masked, const AttnArgs &a) {
+__device__ __forceinline__ void settle(State<D, R> &st, f32x4 (&s)[R][2], int first, int turn, bool masked, int window, const AttnArgs &a) {
     if (masked) {
         const int token = here(first);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int n = 0; n < 8; ++n)
-                if (!sees(st.pos[r], place(token, n, turn), a.window)) s[r][n / 4][n % 4] = kNegInf;
+                if (!sees(st.pos[r], place(token, n, turn), window)) s[r][n / 4][n % 4] = kNegInf;
     }
     float top[R];
     bool more = false;
@@ -296,7 +296,7 @@ __device__ __forceinline__ void weights(State<D, R> &st, const f32x4 (&s)[R][2],
 
 // What else a tile adds to the running results.
 template <int D, int R>
-__device__ __forceinline__ void finish_step(State<D, R> &st, const bf16x8 (&p)[R], const uint32_t (&flag)[4], bool nan_values, int first, int turn, const AttnArgs &a) {
+__device__ __forceinline__ void finish_step(State<D, R> &st, const bf16x8 (&p)[R], const uint32_t (&flag)[4], bool nan_values, int first, int turn, int window) {
     constexpr int W = Kv4<D>::W;
     // The output is divided by the sum of the rounded weights, so that a row
     // that few tokens dominate keeps no error of their rounding; the matrix
@@ -312,7 +312,7 @@ __device__ __forceinline__ void finish_step(State<D, R> &st, const bf16x8 (&p)[R
             const int token = here(first);
 #pragma unroll
             for (int n = 0; n < 8; ++n)
-                if (sees(st.pos[r], place(token, n, turn), a.window)) seen[n / 2] |= 0x3F80u << (n % 2 * 16);
+                if (sees(st.pos[r], place(token, n, turn), window)) seen[n / 2] |= 0x3F80u << (n % 2 * 16);
             const f32x4 z = {0, 0, 0, 0};
             const f32x4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(flag), as_bf16(seen), z, 0, 0, 0);
 #pragma unroll
@@ -364,7 +364,7 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, boo
         }
     }
     const int first = index * kTile + lane / 16 * 8;  // this lane's first token
-    settle<D, R>(st, s, first, 0, masked, a);
+    settle<D, R>(st, s, first, 0, masked, a.window, a);
     bf16x8 p[R];
     weights<D, R>(st, s, p, a);
 #pragma unroll
@@ -384,13 +384,13 @@ __device__ __forceinline__ void step(State<D, R> &st, Tile<D> &t, int index, boo
             for (int i = 0; i < 2; ++i)
                 st.row[r].acc[j + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(v[i]), p[r], st.row[r].acc[j + i], 0, 0, 0);
     }
-    finish_step<D, R>(st, p, flag, nan_values, first, 0, a);
+    finish_step<D, R>(st, p, flag, nan_values, first, 0, a.window);
 }
 
 // The rows of a block, where they lie, and the tiles that they see.
 struct Block {
     int seq, head, first, rows;  // rows: of the sequence's key head, first: of this block
-    int q0, n, len;              // first query token; cached tokens; queries
+    int q0, n, len;              // first query token; cached tokens, the table's or more; queries
     int lo, hi;                  // tiles [lo, hi)
     int seen_lo, seen_hi;        // tokens that every row sees: [seen_lo, seen_hi)
 };
@@ -401,16 +401,16 @@ __device__ __forceinline__ bool locate(Block &b, const AttnArgs &a, int seq, int
     const int q0 = min(max(a.q_start[seq], 0), a.tokens), q1 = min(max(a.q_start[seq + 1], q0), a.tokens);
     b.seq = seq, b.head = head;
     b.q0 = q0, b.len = q1 - q0;
-    // 30 bits hold the tokens of a table row: checked on the host
-    b.n = min(max(a.kv_len[seq], 0), a.per_seq << (a.shift + 5));
+    b.n = max(a.kv_len[seq], 0);
     b.rows = min(b.len, a.max_q) * a.group;
     b.first = block * size;
     if (b.first >= b.rows) return false;
     const int lowest = b.n - b.len + b.first / a.group;
     const int highest = b.n - b.len + (min(b.rows, b.first + size) - 1) / a.group;
     const int from = (int)max((int64_t)0, (int64_t)lowest - a.window + 1);
-    b.lo = from / kTile;
-    b.hi = highest >= from ? highest / kTile + 1 : b.lo;
+    const int tiles = a.per_seq << a.shift;  // that the table has: 25 bits, checked on the host
+    b.lo = min(from / kTile, tiles);
+    b.hi = highest >= from ? min(highest / kTile + 1, tiles) : b.lo;
     b.seen_lo = (int)max((int64_t)0, (int64_t)highest - a.window + 1);
     b.seen_hi = lowest + 1;
     return true;
@@ -741,10 +741,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
         __syncthreads();
         for (int t = b.lo, now = 0; t < b.hi; ++t, now ^= 1) {
             const bool hidden = masked(t, pg[0]);
-            // tokens on a lost page are past every row's position
-            const int first = lost(pg[0]) ? 0x7FFFFF00 : t * kTile + lane / 16 * 8;
+            const int window = lost(pg[0]) ? 0 : a.window;
+            const int first = t * kTile + lane / 16 * 8;
             if (masked(t + 1, pg[1])) v.hide(vs[1 - now], lane, wave);
-            settle<D, R>(st, s, first, lane / 16, hidden, a);
+            settle<D, R>(st, s, first, lane / 16, hidden, window, a);
             // weights beside the products of the next scores, whose operands
             // are on their way from LDS already
             bf16x8 p[R], kf[2][D / 32], vf[W];
@@ -782,7 +782,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv4_attention_wide(AttnArgs a) 
                 for (int n = 0; n < 4; ++n) flag[n] = f[n];
                 nan_values = __any((f[0] | f[1] | f[2] | f[3]) != 0);
             }
-            finish_step<D, R>(st, p, flag, nan_values, first, lane / 16, a);
+            finish_step<D, R>(st, p, flag, nan_values, first, lane / 16, window);
 #pragma unroll
             for (int r = 0; r < R; ++r) s[r][0] = ahead[r][0], s[r][1] = ahead[r][1];
             __syncthreads();

@@ -388,7 +388,8 @@ int ar_kv4_read(const void *cache, const void *slots, ar_rows k_out, ar_rows v_o
  *               Tokens past the last entry, or on a page outside the cache,
  *               are not seen.  Entries past a sequence's tokens are not read.
  *               pages_per_seq * page_size is below 2^30.
- *   q_start     batch + 1 int32, rising; kv_len batch int32.
+ *   q_start     batch + 1 int32, rising; kv_len batch int32, also where it is
+ *               more than the row's entries hold (below 0: 0).
  *   lse         (tokens, heads) floats.
  *   workspace   ar_kv4_attention_workspace bytes of any contents.  Two calls
  *               in flight on one workspace are not allowed.
