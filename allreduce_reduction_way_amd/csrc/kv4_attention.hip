@@ -956,7 +956,7 @@ constexpr int wide_tiles(int dim) { return dim == 64 ? 3 : dim == 128 ? 2 : 1; }
 Plan plan(int batch, int max_q, int64_t max_kv, int64_t window, int group, int kv_heads, int dim) {
     Plan p = {};
     const int64_t rows = (int64_t)max_q * group, tiles = (rows + 15) / 16;
-    const int most = dim == 64 ? 3 : dim == 128 ? 2 : 1;
+    const int most = wide_tiles(dim);  // the registers' limit in both kernels
     p.tiles = (int)(tiles < most ? tiles : most);
     p.splits = p.chunk = 1;
     p.waves = kWaves;
@@ -994,7 +994,23 @@ Plan plan(int batch, int max_q, int64_t max_kv, int64_t window, int group, int k
     return p;
 }
 
-int64_t part_floats(const Plan &p, int dim) { return (int64_t)p.tiles * (dim / 16 * 256 + 48); }
+// Floats of the ranges' results, at most, of all calls whose batch, max_q and
+// max_kv are these or smaller.  plan() itself takes fewer ranges where there are
+// more row blocks, so the sizes of single calls rise and fall with the batch.
+// By its rule, with u < 2 kCus units that are split: u kCus / u is at most kCus,
+// u ceil(4 kCus / u) at most 4 kCus + u - 1, neither above u times the steps' limit
+// or u kSplits, and one range leaves nothing.
+int64_t most_floats(int64_t batch, int64_t max_q, int64_t max_kv, int group, int kv_heads, int dim) {
+    const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+    const int64_t steps = (max_kv + kTile - 1) / kTile, few = steps / (2 * kWaves), more = steps / (2 * kWaves * kLong);
+    if (few < 2) return 0;
+    const int64_t tiles = (max_q * group + 15) / 16, most = wide_tiles(dim);
+    const int64_t pairs = least(batch * kv_heads, 2 * kCus - 1);
+    const int64_t units = least(batch * kv_heads * ((tiles + most - 1) / most), 2 * kCus - 1);
+    const int64_t one_round = least(kCus, units * few);
+    const int64_t rounds = least(4 * kCus + pairs - 1, pairs * least(kSplits, more));
+    return (one_round > rounds ? one_round : rounds) * least(tiles, most) * (dim / 16 * 256 + 48);
+}
 
 bool valid_sizes(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, int heads, int kv_heads, int dim) {
     return batch >= 0 && batch <= 1 << 20 && tokens >= 0 && tokens <= 1 << 28 && max_q >= 0 &&
@@ -1043,9 +1059,8 @@ extern "C" {
 int64_t ar_kv4_attention_workspace(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv,
                                    int heads, int kv_heads, int dim) {
     if (!valid_sizes(batch, tokens, max_q, max_kv, heads, kv_heads, dim)) return AR_EINVAL;
-    if (batch == 0 || max_q == 0) return 16;
-    const Plan p = plan((int)batch, (int)max_q, max_kv, 0, heads / kv_heads, kv_heads, dim);
-    return p.splits > 1 ? p.units * p.splits * part_floats(p, dim) * 4 : 16;
+    const int64_t floats = most_floats(batch, max_q, max_kv, heads / kv_heads, kv_heads, dim);
+    return floats > 4 ? 4 * floats : 16;
 }
 
 int ar_kv4_attention(ar_rows q, const void *cache, const void *page_table, int64_t table_stride,

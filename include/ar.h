@@ -392,7 +392,10 @@ int ar_kv4_read(const void *cache, const void *slots, ar_rows k_out, ar_rows v_o
  *               more than the row's entries hold (below 0: 0).
  *   lse         (tokens, heads) floats.
  *   workspace   ar_kv4_attention_workspace bytes of any contents.  Two calls
- *               in flight on one workspace are not allowed.
+ *               in flight on one workspace are not allowed.  The size never
+ *               falls as batch, max_q or max_kv grow: the workspace of the
+ *               largest call serves every smaller one of the same heads,
+ *               kv_heads and dim.
  *   max_q       at least the largest number of queries of a sequence (those
  *               past it get no output); max_kv the largest kv_len, or any
  *               bound on it: it only says how the work is split.
