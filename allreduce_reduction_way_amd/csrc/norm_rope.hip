@@ -378,7 +378,7 @@ int grad_parts(int64_t tokens, int steps) {
     return (int)(parts < 1 ? 1 : parts > steps ? steps : parts);
 }
 
-int grad_blocks(int64_t tokens, int parts) {
+int grad_blocks(int64_t tokens, int64_t parts) {
     const int64_t blocks = (tokens * parts + kThreads / 64 - 1) / (kThreads / 64);
     return (int)(blocks < 1 ? 1 : blocks < kSlots ? blocks : kSlots);
 }
@@ -467,7 +467,10 @@ int64_t ar_qk_norm_rope_bwd_workspace(int64_t tokens, int heads, int kv_heads, i
     NormArgs a = {};
     a.hq = heads, a.hk = kv_heads;
     count_steps(a, dim);
-    return (int64_t)grad_blocks(tokens, grad_parts(tokens, a.steps)) * 2 * dim * 4;
+    // The workgroups of no call of fewer tokens or heads are more than with a
+    // wave for every step (those of single calls rise and fall with the tokens,
+    // as the waves that share one get fewer).
+    return (int64_t)grad_blocks(tokens, a.steps) * 2 * dim * 4;
 }
 
 int ar_qk_norm_rope_bwd(ar_rows q_grad, ar_rows k_grad, ar_rows q, ar_rows k, const void *q_weight,

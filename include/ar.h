@@ -325,7 +325,9 @@ int ar_qk_norm_rope(ar_rows q, ar_rows k, const void *q_weight, const void *k_we
  * tokens and heads in binary32, in an order that depends on the sizes alone).
  *   dq, dk     may be q_grad or q, and k_grad or k, exactly.
  *   workspace  ar_qk_norm_rope_bwd_workspace bytes of any contents.  Two calls
- *              in flight on one workspace are not allowed.
+ *              in flight on one workspace are not allowed.  The size never falls
+ *              as tokens, heads or kv_heads grow: the workspace of the largest
+ *              call serves every smaller one of the same dim.
  * tokens == 0 sets the weights' gradients to 0.
  * ------------------------------------------------------------------------- */
 int64_t ar_qk_norm_rope_bwd_workspace(int64_t tokens, int heads, int kv_heads, int dim);

@@ -28,3 +28,21 @@ def test_attention_workspace_never_falls(heads, kv_heads, dim):
                     n = size(sizes[id(batches)], sizes[id(queries)], sizes[id(tokens)])
                     assert n >= max(16, last), (x, y, z)
                     last = n
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_gradient_workspace_never_falls(dim):
+    tokens = [0, 1, 2, 3, 7, 100, 511, 512, 513, 1023, 1024, 1025, 1366, 2047, 2048, 2049, 4095, 4096, 4097, 100000]
+    heads = [0, 1, 2, 7, 8, 9, 16, 40, 64, 100]
+
+    def size(t, hq, hk):
+        return ar.ar_qk_norm_rope_bwd_workspace(t, hq, hk, dim)
+
+    for a in heads:
+        for b in heads:
+            for lo, hi in zip(tokens, tokens[1:]):
+                assert 8 * dim <= size(lo, a, b) <= size(hi, a, b), (lo, hi, a, b)
+    for t in tokens:
+        for a in heads:
+            for lo, hi in zip(heads, heads[1:]):
+                assert size(t, a, lo) <= size(t, a, hi) and size(t, lo, a) <= size(t, hi, a), (t, a, lo, hi)
