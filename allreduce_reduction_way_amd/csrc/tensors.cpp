@@ -10,6 +10,7 @@
 // current stream of the tensors' device), and returns the C call's status.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -107,10 +108,12 @@ class Args {
 
     double number_or(double otherwise) { return args_[at_] == Py_None ? (++at_, otherwise) : number(); }
 
-    // The stream, the last argument, and the check that all tensors are on
-    // one GPU.
+    // The stream, the last argument, and the check that it and all tensors are
+    // on one GPU, which is the current one until this object goes: kernels are
+    // launched on the current device, whatever their stream.
     void *stream() {
         if (!device_.is_cuda()) fail(PyExc_TypeError, "expected CUDA tensors, got tensors on %s", device_.str().c_str());
+        guard_.reset_device(device_);
         PyObject *s = args_[last_], *owned = nullptr;
         if (s == Py_None) {
             static PyObject *const current = [] {
@@ -124,6 +127,11 @@ class Args {
             s = owned = index ? PyObject_CallOneArg(current, index) : nullptr;
             Py_XDECREF(index);
         } else if (!PyLong_Check(s)) {
+            PyObject *index = PyObject_GetAttrString(s, "device_index");
+            const long at = index ? PyLong_AsLong(index) : -1;
+            Py_XDECREF(index);
+            if (at == -1 && PyErr_Occurred()) throw PythonError();
+            if (at != device_.index()) fail(PyExc_ValueError, "stream: on cuda:%ld, tensors on %s", at, device_.str().c_str());
             s = owned = PyObject_GetAttrString(s, "cuda_stream");
         }
         if (!s) throw PythonError();
@@ -155,6 +163,7 @@ class Args {
     int at_ = 0;
     bool seen_ = false;
     at::Device device_{at::kCPU};
+    c10::OptionalDeviceGuard guard_;
 };
 
 ar_rows as_rows(const at::Tensor &t) {
