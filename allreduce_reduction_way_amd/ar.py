@@ -356,7 +356,10 @@ def ar_packet_recv(scratch: Sequence, outputs: Sequence, flag: int, ctrl, rank_l
 #
 # The attention operators take torch tensors: ar_tensors.so reads their sizes,
 # strides, types and devices, checks them against each other (ValueError, or
-# TypeError for what is no tensor on a GPU) and calls the C library.
+# TypeError for what is no tensor on a GPU) and calls the C library on the
+# tensors' device.  Nothing is recorded for autograd: a tensor that requires a
+# gradient is a ValueError where gradients are recorded (inside a
+# torch.autograd.Function, or under torch.no_grad(), they are not).
 
 _tensors = None
 

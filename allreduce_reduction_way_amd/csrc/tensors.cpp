@@ -11,6 +11,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -149,6 +150,9 @@ class Args {
         if (!seen_) device_ = t.device(), seen_ = true;
         else if (t.device() != device_)
             fail(PyExc_ValueError, "%s: on %s, others on %s", what, t.device().str().c_str(), device_.str().c_str());
+        // nothing is recorded for autograd, and nothing is lost without a word
+        if (t.requires_grad() && c10::GradMode::is_enabled())
+            fail(PyExc_ValueError, "%s: requires a gradient, which this call does not record: call it under torch.no_grad()", what);
         return t;
     }
 
