@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <numeric>
+
 #include "ar.h"
 
 namespace ar {
@@ -82,19 +84,32 @@ struct RowsArg {
                (tokens <= 1 || r.token_stride == o.r.token_stride) &&
                (heads <= 1 || r.head_stride == o.r.head_stride);
     }
-    // Whether the two share an element.  Arrays of one token stride that lie
-    // beside each other in every token (the queries and the keys of one
-    // projection's output) do not; any other crossing of their spans is taken
+    int64_t head_elems() const { return (tokens - 1) * r.token_stride + dim; }  // of one head
+    // The distance that every row's start is a multiple of from the first (0:
+    // there is one row).
+    int64_t step() const {
+        return std::gcd(tokens > 1 ? r.token_stride : 0, heads > 1 ? r.head_stride : 0);
+    }
+    // Whether pieces of `mine` elements of this array and of `theirs` of the
+    // other, each array's at multiples of `period` from its start, lie apart.
+    bool beside(const RowsArg &o, int64_t period, int64_t mine, int64_t theirs) const {
+        if (period < mine + theirs) return false;
+        const int64_t bytes = (int64_t)(addr(o.r.p) - addr(r.p)) % (2 * period);
+        const int64_t at = bytes < 0 ? bytes + 2 * period : bytes;
+        return at >= 2 * mine && at + 2 * theirs <= 2 * period;
+    }
+    // Whether the two share an element.  Arrays that lie beside each other in
+    // every token (the queries and the keys of one projection's output), in
+    // every head, or in a period of all their strides (each head's query, key
+    // and value side by side) do not; any other crossing of their spans is taken
     // as sharing.
     bool overlaps(const RowsArg &o) const {
         if (!overlap(span(), o.span())) return false;
-        const int64_t ts = r.token_stride;
-        if (ts == o.r.token_stride && ts >= row_elems() && ts >= o.row_elems()) {
-            const int64_t bytes = (int64_t)(addr(o.r.p) - addr(r.p)) % (2 * ts);
-            const int64_t at = bytes < 0 ? bytes + 2 * ts : bytes;
-            return at < 2 * row_elems() || at + 2 * o.row_elems() > 2 * ts;
-        }
-        return true;
+        if (r.token_stride == o.r.token_stride && beside(o, r.token_stride, row_elems(), o.row_elems()))
+            return false;
+        if (r.head_stride == o.r.head_stride && beside(o, r.head_stride, head_elems(), o.head_elems()))
+            return false;
+        return !beside(o, std::gcd(step(), o.step()), dim, o.dim);
     }
 };
 
