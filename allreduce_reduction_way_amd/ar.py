@@ -424,7 +424,8 @@ def ar_kv4_cache_bytes(pages: int, kv_heads: int, dim: int, page_size: int) -> i
 
 def ar_kv4_write(k, v, slots, cache, page_size: int, stream=None) -> None:
     """Quantises the tokens of k and v (tokens, kv_heads, dim) into the slots
-    of a 4-bit cache (pages, kv_heads, page_size / 32, 34 dim)."""
+    of a 4-bit cache (pages, kv_heads, page_size / 32, 34 dim).  No slot may be
+    named twice: what it holds then is neither token."""
     rc = (_tensors or tensors()).kv4_write(k, v, slots, cache, page_size, stream)
     if rc:
         raise ArError(rc, "ar_kv4_write")

@@ -364,8 +364,10 @@ int ar_qk_norm_rope_bwd(ar_rows q_grad, ar_rows k_grad, ar_rows q, ar_rows k, co
  * exact in bf16.
  *   k, v    (tokens, kv_heads, dim).
  *   slots   tokens int64: page * page_size + place in the page.  A write to a
- *           slot outside the cache is left out, a read of one gives zeros.  A
- *           slot that is named twice in one write gets either token's bytes.
+ *           slot outside the cache is left out, a read of one gives zeros.
+ *           Name no slot twice in one write: each of its bytes is then one of
+ *           those tokens', in no order, and codes of one may stand under scales
+ *           of another.  Other slots are as they should be.
  *   cache   16-byte aligned.
  * ------------------------------------------------------------------------- */
 int64_t ar_kv4_cache_bytes(int64_t pages, int kv_heads, int dim, int page_size);
