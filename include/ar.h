@@ -288,6 +288,12 @@ int ar_packet_recv(ar_ptrs scratch, ar_ptrs out, int P, int rank_lo, int rank_hi
  * Alignment: weights 2 bytes, float and int32 arrays 4, int64 arrays 8, the
  * cache and workspaces 16.  Buffers that are written must not overlap any
  * other (AR_EALIAS) except where a call says so.
+ *
+ * Sizes (AR_EINVAL beyond): strides times their counts up to 2^40 elements; up
+ * to 2^28 tokens, and 65536 heads of either kind in the norms and the cache.
+ * What a launch cannot hold is refused, too: the norms take every call below
+ * 2^24 tokens, the cache every one whose tokens * kv_heads is below 2^27, and
+ * for the attention see there.
  * ------------------------------------------------------------------------- */
 typedef struct ar_rows {
     void *p;
@@ -383,6 +389,9 @@ int ar_kv4_read(const void *cache, const void *slots, ar_rows k_out, ar_rows v_o
  * at position p = kv_len[b] - m + i and sees tokens j <= p, with a window only
  * those of j > p - window.
  *     out = sum_j softmax_j(scale q . k_j) v_j,  lse = log sum_j exp(scale q . k_j)
+ * Scores, their maxima and sums and the accumulated output are binary32.  The
+ * weights of the output are rounded to bf16 (each by 2^-8 of itself at most),
+ * and it is divided by the sum of the rounded ones; lse has the unrounded sum.
  * A query that sees nothing gets zeros and -infinity.  A token that a query
  * does not see adds nothing to it, whatever bytes the cache holds there.
  *   q, out      (tokens, heads, dim); query head h reads key head
@@ -405,6 +414,8 @@ int ar_kv4_read(const void *cache, const void *slots, ar_rows k_out, ar_rows v_o
  *               bound on it: it only says how the work is split.
  *   window      0: none.
  *   scale       > 0.
+ * At most 2^20 sequences, 4096 kv_heads, 16384 heads, max_q 2^24 and max_q * heads
+ * 2^30; batch * kv_heads * (max_q * heads / kv_heads / 16 + 1) below 2^23.
  * ------------------------------------------------------------------------- */
 int64_t ar_kv4_attention_workspace(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv,
                                    int heads, int kv_heads, int dim);
