@@ -291,8 +291,8 @@ int ar_packet_recv(ar_ptrs scratch, ar_ptrs out, int P, int rank_lo, int rank_hi
  *
  * Sizes (AR_EINVAL beyond): strides times their counts up to 2^40 elements; up
  * to 2^28 tokens, and 65536 heads of either kind in the norms and the cache.
- * What a launch cannot hold is refused, too: the norms take every call below
- * 2^24 tokens, the cache every one whose tokens * kv_heads is below 2^27, and
+ * What a launch cannot hold is refused, too: the norms take every call up to
+ * 2^23 tokens, the cache every one whose tokens * kv_heads is below 2^27, and
  * for the attention see there.
  * ------------------------------------------------------------------------- */
 typedef struct ar_rows {
@@ -415,7 +415,7 @@ int ar_kv4_read(const void *cache, const void *slots, ar_rows k_out, ar_rows v_o
  *   window      0: none.
  *   scale       > 0.
  * At most 2^20 sequences, 4096 kv_heads, 16384 heads, max_q 2^24 and max_q * heads
- * 2^30; batch * kv_heads * (max_q * heads / kv_heads / 16 + 1) below 2^23.
+ * 2^30; batch * kv_heads * (max_q * heads / kv_heads / 16 + 1) up to 2^22.
  * ------------------------------------------------------------------------- */
 int64_t ar_kv4_attention_workspace(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv,
                                    int heads, int kv_heads, int dim);
