@@ -26,6 +26,11 @@ namespace {
 
 struct PythonError {};  // the Python error is set
 
+// torch's function of that name, looked up when the module is loaded: a static
+// that is set at its first use waits for another thread's setting of it with the
+// interpreter's lock held, which that thread may need.
+PyObject *current_stream;
+
 [[noreturn]] void fail(PyObject *type, const char *format, ...) {
     va_list args;
     va_start(args, format);
@@ -117,15 +122,8 @@ class Args {
         guard_.reset_device(device_);
         PyObject *s = args_[last_], *owned = nullptr;
         if (s == Py_None) {
-            static PyObject *const current = [] {
-                PyObject *m = PyImport_ImportModule("torch._C");
-                PyObject *f = m ? PyObject_GetAttrString(m, "_cuda_getCurrentRawStream") : nullptr;
-                Py_XDECREF(m);
-                return f;
-            }();
-            if (!current) throw PythonError();
             PyObject *index = PyLong_FromLong(device_.index());
-            s = owned = index ? PyObject_CallOneArg(current, index) : nullptr;
+            s = owned = index ? PyObject_CallOneArg(current_stream, index) : nullptr;
             Py_XDECREF(index);
         } else if (!PyLong_Check(s)) {
             PyObject *index = PyObject_GetAttrString(s, "device_index");
@@ -302,4 +300,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "ar_tensors", nullptr, -1, methods,
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject *PyInit_ar_tensors(void) { return PyModule_Create(&module); }
+extern "C" __attribute__((visibility("default"))) PyObject *PyInit_ar_tensors(void) {
+    PyObject *torch = PyImport_ImportModule("torch._C");
+    current_stream = torch ? PyObject_GetAttrString(torch, "_cuda_getCurrentRawStream") : nullptr;
+    Py_XDECREF(torch);
+    return current_stream ? PyModule_Create(&module) : nullptr;
+}
