@@ -43,6 +43,7 @@ class Layer:
         self.cos_sin = torch.cat([angle.cos(), angle.sin()], 1).float()
         per = -(-tokens // PAGE)  # pages of a sequence
         self.max_kv = per * PAGE
+        self.room, self.used = tokens, 0  # tokens of a sequence: that fit, that are cached
         order = torch.randperm(batch * per, generator=g, device="cuda")
         self.table = order.reshape(batch, per).int()
         self.cache = [torch.zeros(batch * per, kv_heads, PAGE // 32, 34 * dim, dtype=torch.uint8, device="cuda")
@@ -58,19 +59,28 @@ class Layer:
     def fill(self, keys, values) -> None:
         """Caches a prompt: keys and values (tokens, kv_heads, dim) of each rank
         and sequence, keys normed and turned already."""
+        self._take(keys[0][0].shape[0] - self.used)
         for r in range(self.P):
             for b in range(self.B):
                 k, v = keys[r][b], values[r][b]
                 at = torch.arange(k.shape[0], device="cuda")
                 slots = self.table[b].long()[at // PAGE] * PAGE + at % PAGE
                 ar.ar_kv4_write(k, v, slots, self.cache[r], PAGE)
-        self.length.fill_(keys[0][0].shape[0])
+        self.length.fill_(self.used)
+
+    def _take(self, tokens: int) -> None:
+        """Room for so many more tokens of each sequence: pages past the table's
+        would be looked up otherwise."""
+        if self.used + tokens > self.room:
+            raise ValueError(f"{self.used + tokens} tokens, there is room for {self.room}")
+        self.used += tokens
 
     def step(self, qkv) -> list:
         """One new token of every sequence: qkv[r] (batch, heads + 2 kv_heads,
         dim) is what rank r's projection gave, normed and turned in place.
         Returns every rank's copy of the summed output (batch, hidden)."""
         hq, hk = self.hq, self.hk
+        self._take(1)
         positions = self.length.long()
         slots = self.table.long().gather(1, (positions // PAGE)[:, None])[:, 0] * PAGE + positions % PAGE
         self.length += 1
