@@ -12,7 +12,7 @@
 // scales for each channel, and a few operations.  A row lies in D/8 lanes, 16
 // bytes each; a group's largest is an exchange between four lanes.  16384 tokens
 // of eight heads of 128, 170 MB, are written and read back in 32.7 us, 5.2 TB/s;
-// 440 of one head in 6.6, which is what two launches cost their caller.
+// 440 of one head in 7.0, which is what two launches cost their caller.
 #include "host.h"
 #include "kv4.h"
 #include "rows.h"

@@ -37,7 +37,7 @@
 //
 // k_kv4_attention_wide, many rows: bound by the issue of vector and matrix
 // instructions.  Two chunks of 2048 queries over 8192 and fewer tokens, 32
-// heads: 468 GFLOP in 467 us, 1.00 PFLOP/s (a library product of 8192^3 reaches
+// heads: 468 GFLOP in 460 us, 1.02 PFLOP/s (a library product of 8192^3 reaches
 // 1.16); the matrix unit is busy for 43% of the time.
 #include "host.h"
 #include "kv4.h"
@@ -982,8 +982,8 @@ Plan plan(int batch, int max_q, int64_t max_kv, int64_t window, int group, int k
     // Rows enough for two workgroups on each compute unit.  Where there are
     // fewer, a wave of this kernel waits for each tile's conversion, and the
     // split kernel is faster: one sequence of 4096 tokens, 8 key heads of 128,
-    // four queries to each: 1024 queries take 122 us here and 96 there, 2048
-    // 148 and 161.
+    // four queries to each: 1024 queries take 115 us here and 91 there, 2048
+    // 130 and 152.
     const int wide = kWaves * wide_tiles(dim);
     p.blocks = (int)((tiles + wide - 1) / wide);
     p.units = (int64_t)batch * kv_heads * p.blocks;
@@ -992,7 +992,11 @@ Plan plan(int batch, int max_q, int64_t max_kv, int64_t window, int group, int k
     p.blocks = (int)((tiles + p.tiles - 1) / p.tiles);
     p.units = (int64_t)batch * kv_heads * p.blocks;
     // Row blocks enough that two of their workgroups are on each compute unit:
-    // none is split, and a third fits beside them.
+    // none is split, and a third fits beside them.  64 sequences of 4096 tokens,
+    // 8 key heads of 128, take 46 us, and 64 as two ranges of eight waves.  The
+    // batch that loses is one of a long sequence among short ones: 131072
+    // tokens and 63 times 1024 take 561 us, 220 as two ranges (42 for their
+    // bytes).
     if (p.units >= 2 * kCus) return p;
     p.waves = 2 * kWaves;
     if (window && max_kv > window + max_q) max_kv = window + max_q;
@@ -1000,8 +1004,8 @@ Plan plan(int batch, int max_q, int64_t max_kv, int64_t window, int group, int k
     // One round of workgroups while there is a tile for each wave, and up to
     // four, which even out ragged lengths, while each wave has kLong tiles and
     // a sequence's rows are one block (with more, its results outweigh that).
-    // Fifteen sequences of up to 108125 tokens, four key heads: 61 us in four
-    // rounds, 93 in one.
+    // Fifteen sequences of up to 108125 tokens, four key heads of 64: 42 us in four
+    // rounds, 77 in one; other ragged batches take 10% longer to 30% less.
     int64_t s = kCus / p.units;
     if (s > steps / p.waves) s = steps / p.waves;
     int64_t more = p.blocks > 1 ? 1 : (4 * kCus + p.units - 1) / p.units;
