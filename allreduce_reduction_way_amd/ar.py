@@ -83,6 +83,11 @@ def lib() -> ctypes.CDLL:
             "ar_kv4_attention_workspace": (i64, [i64, i64, i64, i64, i32, i32, i32]),
             "ar_kv4_attention": (i32, [rows, vp, vp, i64, vp, vp, rows, vp, vp, i64, i64, i32, i32,
                                        i32, i64, i32, i64, i64, i64, i64, f32, vp]),
+            "ar_block_norm": (i32, [ar_ptrs, i64, i32, rows, vp, rows, vp, rows, rows, i64, i32,
+                                    f32, f32, vp]),
+            "ar_block_norm_bwd_workspace": (i64, [i64, i32]),
+            "ar_block_norm_bwd": (i32, [rows, rows, rows, rows, vp, rows, vp, rows, rows, rows, vp,
+                                        vp, vp, i64, i32, f32, f32, vp]),
             "ar_slice_range": (i32, [i32, i32, i64, ctypes.POINTER(i64), ctypes.POINTER(i64)]),
             "ar_packet_slot_packets": (i64, [i32, i64]),
             "ar_packet_scratch_bytes": (i64, [i32, i64]),
@@ -456,6 +461,42 @@ def ar_kv4_attention(q, cache, page_table, q_start, kv_len, out, lse, workspace,
                                                window, scale, stream)
     if rc:
         raise ArError(rc, "ar_kv4_attention")
+
+
+# ------------------------------------------------------------- around a block
+#
+# Tensors as for the attention operators, and the same checks.
+
+
+def ar_block_norm(parts, x, h, z=None, *, post_weight=None, gate=None, pre_weight=None,
+                  residual_scale: float = 1.0, eps: float = 1e-6, stream=None) -> None:
+    """h = residual_scale x + gate norm(sum of parts), and z, the norm of h with
+    pre_weight.  `parts`: a tensor (tokens, dim) or up to 8 of them; `gate`:
+    (dim) or (tokens, dim); without post_weight the sum is not normed, and
+    without pre_weight there is no z.  h may be x."""
+    rc = (_tensors or tensors()).block_norm(parts, x, h, z, post_weight, gate, pre_weight,
+                                            residual_scale, eps, stream)
+    if rc:
+        raise ArError(rc, "ar_block_norm")
+
+
+def ar_block_norm_bwd_workspace(tokens: int, dim: int) -> int:
+    v = int(lib().ar_block_norm_bwd_workspace(tokens, dim))
+    _check(min(v, 0), "ar_block_norm_bwd_workspace")
+    return v
+
+
+def ar_block_norm_bwd(h_grad, z_grad, y, x, dx, dy, workspace, *, post_weight=None, gate=None,
+                      pre_weight=None, gate_grad=None, post_grad=None, pre_grad=None,
+                      residual_scale: float = 1.0, eps: float = 1e-6, stream=None) -> None:
+    """The gradient of ar_block_norm: dx, and dy for every part, whose sum is y.
+    h_grad is None where nothing else reads h; gate_grad is (dim) of float32 for
+    a gate (dim), bf16 rows for one (tokens, dim)."""
+    rc = (_tensors or tensors()).block_norm_bwd(h_grad, z_grad, y, x, dx, dy, workspace,
+                                                post_weight, gate, pre_weight, gate_grad,
+                                                post_grad, pre_grad, residual_scale, eps, stream)
+    if rc:
+        raise ArError(rc, "ar_block_norm_bwd")
 
 
 def ar_slice_range(P: int, rank: int, n: int) -> tuple:

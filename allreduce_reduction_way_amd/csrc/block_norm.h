@@ -1,0 +1,45 @@
+// block_norm.h -- sums over the lanes of a wave, and bf16 pairs, for the
+// operators around a block.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device.h"
+
+namespace ar {
+
+// v of the lane that the data-parallel primitive `CTRL` names; lanes without
+// one add 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+    const int moved = __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false);
+    return v + __int_as_float(moved);
+}
+
+// Sum of sixteen lanes side by side; every lane of them gets it.  Each step adds
+// the lane that turning the sixteen by 8, 4, 2 and 1 brings: the same pairs in
+// every lane, so that all have the same bits.
+__device__ __forceinline__ float row16_sum(float v) {
+    v = dpp_add<0x128, 0xf>(v);
+    v = dpp_add<0x124, 0xf>(v);
+    v = dpp_add<0x122, 0xf>(v);
+    return dpp_add<0x121, 0xf>(v);
+}
+
+// Sum over the wave; every lane gets it.
+__device__ __forceinline__ float wave_sum(float v) {
+    v = row16_sum(v);
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    bf16x2_t r;
+    r[0] = (__bf16)lo;
+    r[1] = (__bf16)hi;
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+}  // namespace ar

@@ -1,6 +1,6 @@
-// tensors.cpp -- the attention operators' calls with torch tensors: sizes,
-// types, strides and devices are checked here and addresses handed to the C
-// calls of ar.h.  Argument marshalling only.
+// tensors.cpp -- the calls of the attention operators, and of those around a
+// block, with torch tensors: sizes, types, strides and devices are checked here
+// and addresses handed to the C calls of ar.h.  Argument marshalling only.
 //
 // Read from Python, the attributes of a call's eight or more tensors took
 // 12-20 us, several times what the kernels of a decode step run; here a call
@@ -61,7 +61,10 @@ class Args {
 
     // A tensor of that type and shape (kAny: any size).
     const at::Tensor &tensor(const char *what, ScalarType type, std::initializer_list<int64_t> shape, bool contiguous = true) {
-        const at::Tensor &t = next(what);
+        return fitting(next(what), what, type, shape, contiguous);
+    }
+
+    const at::Tensor &fitting(const at::Tensor &t, const char *what, ScalarType type, std::initializer_list<int64_t> shape, bool contiguous) {
         const ScalarType have = t.scalar_type();
         const bool bf16 = type == ScalarType::BFloat16 && (have == ScalarType::Short || have == ScalarType::UInt16);
         if (have != type && !bf16) fail(PyExc_ValueError, "%s: %s expected, got %s", what, name_of(type), at::toString(have));
@@ -83,6 +86,45 @@ class Args {
         return t;
     }
 
+    // Whether the next argument is None, which is taken then.
+    bool none() { return args_[at_] == Py_None ? (++at_, true) : false; }
+
+    // (tokens, channels) of bf16 with contiguous channels.
+    ar_rows plane(const char *what, int64_t tokens, int64_t dim) { return as_plane(fitting(next(what), what, ScalarType::BFloat16, {tokens, dim}, false), what); }
+
+    // (dim) for all tokens, or (tokens, dim).
+    ar_rows gate(const char *what, int64_t tokens, int64_t dim) {
+        const at::Tensor &t = next(what);
+        if (t.dim() == 1) return ar_rows{fitting(t, what, ScalarType::BFloat16, {dim}, true).data_ptr(), 0, 0};
+        ar_rows r = as_plane(fitting(t, what, ScalarType::BFloat16, {tokens, dim}, false), what);
+        if (tokens == 1) r.token_stride = dim;
+        else if (tokens > 1 && r.token_stride == 0)
+            fail(PyExc_ValueError, "%s: one gate for all tokens is a tensor of shape (%lld)", what, (long long)dim);
+        return r;
+    }
+
+    // One tensor (tokens, dim), or a sequence of up to AR_MAX_P of them with one stride.
+    int planes(const char *what, int64_t tokens, int64_t dim, ar_ptrs *to, int64_t *stride) {
+        PyObject *o = args_[at_];
+        if (THPVariable_Check(o)) {
+            const ar_rows r = plane(what, tokens, dim);
+            to->p[0] = r.p, *stride = r.token_stride;
+            return 1;
+        }
+        ++at_;
+        if (!PyList_Check(o) && !PyTuple_Check(o))
+            fail(PyExc_TypeError, "%s: expected CUDA tensors, got %s", what, Py_TYPE(o)->tp_name);
+        const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
+        if (n < 1 || n > AR_MAX_P) fail(PyExc_ValueError, "%s: 1 to %d tensors expected, got %zd", what, AR_MAX_P, n);
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            const ar_rows r = as_plane(fitting(take(PySequence_Fast_GET_ITEM(o, i), what), what, ScalarType::BFloat16, {tokens, dim}, false), what);
+            if (i == 0) *stride = r.token_stride;
+            else if (tokens > 1 && r.token_stride != *stride) fail(PyExc_ValueError, "%s: tensors of one stride expected", what);
+            to->p[i] = r.p;
+        }
+        return (int)n;
+    }
+
     // At least so many bytes, of any type.
     const at::Tensor &bytes(const char *what, int64_t least) {
         const at::Tensor &t = next(what);
@@ -90,6 +132,13 @@ class Args {
         if (!t.is_contiguous()) fail(PyExc_ValueError, "%s: the tensor must be contiguous", what);
         if (have < least)
             fail(PyExc_ValueError, "%s: %lld bytes, the call touches %lld", what, (long long)have, (long long)least);
+        return t;
+    }
+
+    // The argument so many places on, a tensor of that many dimensions; it is not taken.
+    const at::Tensor &peek(int on, const char *what, int64_t dims) {
+        const at::Tensor &t = take(args_[at_ + on], what);
+        if (t.dim() != dims) fail(PyExc_ValueError, "%s: %lld dimensions expected, got %lld", what, (long long)dims, (long long)t.dim());
         return t;
     }
 
@@ -141,8 +190,14 @@ class Args {
     }
 
   private:
-    const at::Tensor &next(const char *what) {
-        PyObject *o = args_[at_++];
+    static ar_rows as_plane(const at::Tensor &t, const char *what) {
+        if (t.size(1) > 1 && t.stride(1) != 1) fail(PyExc_ValueError, "%s: channels must be contiguous", what);
+        return ar_rows{t.numel() ? t.data_ptr() : nullptr, t.stride(0), 0};
+    }
+
+    const at::Tensor &next(const char *what) { return take(args_[at_++], what); }
+
+    const at::Tensor &take(PyObject *o, const char *what) {
         if (!THPVariable_Check(o)) fail(PyExc_TypeError, "%s: expected a CUDA tensor, got %s", what, Py_TYPE(o)->tp_name);
         const at::Tensor &t = THPVariable_Unpack(o);
         if (!seen_) device_ = t.device(), seen_ = true;
@@ -268,6 +323,55 @@ int kv4_attention(Args &a) {
                             batch, as_int(heads), kv_heads, as_int(dim), cache.size(0), page, per, max_q, max_kv, window, scale, a.stream());
 }
 
+// parts, x, h, z, post_weight, gate, pre_weight, residual_scale, eps.
+int block_norm(Args &a) {
+    const at::Tensor &like = a.peek(1, "x", 2);
+    const int64_t tokens = like.size(0), dim = like.size(1);
+    ar_ptrs parts = {};
+    int64_t stride = 0;
+    const int count = a.planes("parts", tokens, dim, &parts, &stride);
+    const ar_rows x = a.plane("x", tokens, dim), h = a.plane("h", tokens, dim);
+    const bool has_z = !a.none();
+    const ar_rows z = has_z ? a.plane("z", tokens, dim) : ar_rows{};
+    void *post = a.none() ? nullptr : a.tensor("post_weight", ScalarType::BFloat16, {dim}).data_ptr();
+    const ar_rows gate = a.none() ? ar_rows{} : a.gate("gate", tokens, dim);
+    void *pre = a.none() ? nullptr : a.tensor("pre_weight", ScalarType::BFloat16, {dim}).data_ptr();
+    if (has_z != (pre != nullptr)) fail(PyExc_ValueError, "z and pre_weight are given together or not at all");
+    const float scale = (float)a.number(), eps = (float)a.number();
+    return ar_block_norm(parts, stride, count, x, post, gate, pre, h, z, tokens, as_int(dim), scale, eps, a.stream());
+}
+
+// h_grad, z_grad, y, x, dx, dy, workspace, post_weight, gate, pre_weight,
+// gate_grad, post_grad, pre_grad, residual_scale, eps.
+int block_norm_bwd(Args &a) {
+    const at::Tensor &like = a.peek(3, "x", 2);
+    const int64_t tokens = like.size(0), dim = like.size(1);
+    const ar_rows dh = a.none() ? ar_rows{} : a.plane("h_grad", tokens, dim);
+    const bool has_dz = !a.none();
+    const ar_rows dz = has_dz ? a.plane("z_grad", tokens, dim) : ar_rows{};
+    const ar_rows y = a.plane("y", tokens, dim), x = a.plane("x", tokens, dim);
+    const ar_rows dx = a.plane("dx", tokens, dim), dy = a.plane("dy", tokens, dim);
+    const int64_t least = ar_block_norm_bwd_workspace(tokens, as_int(dim));
+    if (least < 0) return (int)least;
+    void *ws = a.bytes("workspace", least).data_ptr();
+    void *post = a.none() ? nullptr : a.tensor("post_weight", ScalarType::BFloat16, {dim}).data_ptr();
+    const ar_rows gate = a.none() ? ar_rows{} : a.gate("gate", tokens, dim);
+    void *pre = a.none() ? nullptr : a.tensor("pre_weight", ScalarType::BFloat16, {dim}).data_ptr();
+    if (has_dz != (pre != nullptr)) fail(PyExc_ValueError, "z_grad and pre_weight are given together or not at all");
+    ar_rows dgate = {};
+    if (!a.none()) {
+        if (!gate.p) fail(PyExc_ValueError, "gate_grad: there is no gate");
+        if (gate.token_stride) dgate = a.plane("gate_grad", tokens, dim);
+        else dgate.p = a.tensor("gate_grad", ScalarType::Float, {dim}).data_ptr();
+    }
+    void *dpost = a.none() ? nullptr : a.tensor("post_grad", ScalarType::Float, {dim}).data_ptr();
+    void *dpre = a.none() ? nullptr : a.tensor("pre_grad", ScalarType::Float, {dim}).data_ptr();
+    if (dpost && !post) fail(PyExc_ValueError, "post_grad: there is no post_weight");
+    if (dpre && !pre) fail(PyExc_ValueError, "pre_grad: there is no pre_weight");
+    const float scale = (float)a.number(), eps = (float)a.number();
+    return ar_block_norm_bwd(dh, dz, y, x, post, gate, pre, dx, dy, dgate, dpost, dpre, ws, tokens, as_int(dim), scale, eps, a.stream());
+}
+
 template <int (*CALL)(Args &), int COUNT>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t given) {
     try {
@@ -293,6 +397,8 @@ PyMethodDef methods[] = {
     method<kv4<false>, 6>("kv4_write"),
     method<kv4<true>, 6>("kv4_read"),
     method<kv4_attention, 15>("kv4_attention"),
+    method<block_norm, 10>("block_norm"),
+    method<block_norm_bwd, 16>("block_norm_bwd"),
     {nullptr, nullptr, 0, nullptr},
 };
 

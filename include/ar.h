@@ -426,6 +426,62 @@ int ar_kv4_attention(ar_rows q, const void *cache, const void *page_table, int64
                      int64_t window, float scale, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * Around a block: what a rank runs between the partial sums of one block and the
+ * products of the next.
+ *
+ * Rows here are arrays (tokens, dim) of bf16: an ar_rows whose head_stride is
+ * not looked at.  They start on any even address, and any token stride of at
+ * least 0 will do (of at least dim where the rows are written).  Checks,
+ * alignment and sizes are otherwise those of the attention operators.
+ * ------------------------------------------------------------------------- */
+
+/* ---------------------------------------------------------------------------
+ * ar_block_norm -- the parts of a block's output added up, the norm after the
+ * block, its gate, the scaled residual stream, and the norm before the next
+ * block.  For a token, in binary32 with one rounding of each result:
+ *     y = part_0 + ... + part_{P-1} (in this order)
+ *     u = y / sqrt(mean(y^2) + eps) * post_weight    (y without a post_weight)
+ *     h = residual_scale * x + gate * u              (u without a gate)
+ *     z = h / sqrt(mean(h^2) + eps) * pre_weight
+ * y, u and the h that z is made of are not rounded.
+ *   parts        P = 1..8 arrays (tokens, dim) with one token stride.
+ *   x            (tokens, dim).
+ *   post_weight  dim bf16, or NULL: no norm after the block.
+ *   gate         p NULL: none; token_stride 0: dim bf16 for all tokens;
+ *                otherwise (tokens, dim).
+ *   pre_weight   dim bf16, or NULL: no z (its rows are not looked at).
+ *   h            may be x exactly (in place).
+ *   z            overlaps nothing.
+ *   eps          >= 0.
+ * dim from 1 to 16384, fewer than 2^21 tokens.
+ * ------------------------------------------------------------------------- */
+int ar_block_norm(ar_ptrs parts, int64_t part_stride, int P, ar_rows x, const void *post_weight,
+                  ar_rows gate, const void *pre_weight, ar_rows h, ar_rows z, int64_t tokens, int dim,
+                  float residual_scale, float eps, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * ar_block_norm_bwd -- the gradient of ar_block_norm for h_grad and z_grad: dx,
+ * and dy, which is every part's.  y is the sum of the parts (ar_oneshot_sum
+ * gives it).
+ *   h_grad       p NULL: zeros (nothing else reads the stream).
+ *   z_grad       not looked at without a pre_weight.
+ *   dx, dy       may each be exactly h_grad, z_grad, x or y.
+ *   gate_grad    of a gate for all tokens dim floats, otherwise bf16 rows
+ *                (tokens, dim); p NULL: not wanted.
+ *   post_grad, pre_grad   dim floats, or NULL: not wanted.  Sums over tokens
+ *                are in binary32, in an order that depends on the sizes alone.
+ *   workspace    ar_block_norm_bwd_workspace bytes of any contents, 16-byte
+ *                aligned.  Two calls in flight on one workspace are not allowed.
+ *                The size never falls as tokens or dim grow.
+ * tokens == 0 sets the gradients of what all tokens share to 0.
+ * ------------------------------------------------------------------------- */
+int64_t ar_block_norm_bwd_workspace(int64_t tokens, int dim);
+int ar_block_norm_bwd(ar_rows h_grad, ar_rows z_grad, ar_rows y, ar_rows x, const void *post_weight,
+                      ar_rows gate, const void *pre_weight, ar_rows dx, ar_rows dy, ar_rows gate_grad,
+                      void *post_grad, void *pre_grad, void *workspace, int64_t tokens, int dim,
+                      float residual_scale, float eps, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Host-only helpers: no GPU needed, no HIP call made.
  * ------------------------------------------------------------------------- */
 
