@@ -88,6 +88,13 @@ def lib() -> ctypes.CDLL:
             "ar_block_norm_bwd_workspace": (i64, [i64, i32]),
             "ar_block_norm_bwd": (i32, [rows, rows, rows, rows, vp, rows, vp, rows, rows, rows, vp,
                                         vp, vp, i64, i32, f32, f32, vp]),
+            "ar_w4_bytes": (i64, [i64, i64]),
+            "ar_w4_pack": (i32, [vp, i64, vp, i64, i64, vp]),
+            "ar_w4_unpack": (i32, [vp, vp, i64, i64, i64, vp]),
+            "ar_w4_linear": (i32, [rows, vp, rows, i64, i64, i64, vp]),
+            "ar_w4_experts_workspace": (i64, [i64, i64, i64, i32, i32]),
+            "ar_w4_experts": (i32, [rows, vp, vp, vp, rows, vp, vp, vp, i64, i64, i64, i32, i32,
+                                    f32, vp]),
             "ar_slice_range": (i32, [i32, i32, i64, ctypes.POINTER(i64), ctypes.POINTER(i64)]),
             "ar_packet_slot_packets": (i64, [i32, i64]),
             "ar_packet_scratch_bytes": (i64, [i32, i64]),
@@ -497,6 +504,54 @@ def ar_block_norm_bwd(h_grad, z_grad, y, x, dx, dy, workspace, *, post_weight=No
                                                 post_grad, pre_grad, residual_scale, eps, stream)
     if rc:
         raise ArError(rc, "ar_block_norm_bwd")
+
+
+def ar_w4_bytes(n_out: int, n_in: int) -> int:
+    v = int(lib().ar_w4_bytes(n_out, n_in))
+    _check(min(v, 0), "ar_w4_bytes")
+    return v
+
+
+def ar_w4_pack(w, packed, stream=None) -> None:
+    """Quantises weights w (n_out, n_in) to 4 bits: packed, uint8 of shape
+    (ceil(n_out / 16), ar_w4_bytes(16, n_in))."""
+    rc = (_tensors or tensors()).w4_pack(w, packed, stream)
+    if rc:
+        raise ArError(rc, "ar_w4_pack")
+
+
+def ar_w4_unpack(packed, w, stream=None) -> None:
+    """The values of packed weights."""
+    rc = (_tensors or tensors()).w4_unpack(w, packed, stream)
+    if rc:
+        raise ArError(rc, "ar_w4_unpack")
+
+
+def ar_w4_linear(x, packed, out, stream=None) -> None:
+    """out (tokens, n_out) = x (tokens, n_in) times the transpose of packed
+    weights (n_out, n_in)."""
+    rc = (_tensors or tensors()).w4_linear(x, packed, out, stream)
+    if rc:
+        raise ArError(rc, "ar_w4_linear")
+
+
+def ar_w4_experts_workspace(tokens: int, hidden: int, inner: int, experts: int, top_k: int) -> int:
+    v = int(lib().ar_w4_experts_workspace(tokens, hidden, inner, experts, top_k))
+    _check(min(v, 0), "ar_w4_experts_workspace")
+    return v
+
+
+def ar_w4_experts(x, router, gate_up, down, out, choice, weight, workspace, *,
+                  scale: float = 1.0, stream=None) -> None:
+    """A mixture-of-experts layer: out (tokens, hidden) for x, router (experts,
+    hidden), and packed weights gate_up (experts, inner / 8, bytes), which are
+    the gate's rows and then the others', and down (experts, ceil(hidden / 16),
+    bytes).  The experts taken come back in choice (tokens, top_k) int32 and
+    weight (tokens, top_k) float32."""
+    rc = (_tensors or tensors()).w4_experts(x, router, gate_up, down, out, choice, weight,
+                                            workspace, scale, stream)
+    if rc:
+        raise ArError(rc, "ar_w4_experts")
 
 
 def ar_slice_range(P: int, rank: int, n: int) -> tuple:

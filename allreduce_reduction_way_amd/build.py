@@ -18,7 +18,7 @@ LIB = PKG / "libar.so"
 TENSORS = PKG / "ar_tensors.so"
 RESOURCES = PKG / "libar.resources.txt"   # per-kernel register/scratch report of the last build
 SOURCES = ["host.hip", "reduce.hip", "packet.hip", "probe.hip", "norm_rope.hip", "kv4.hip",
-           "kv4_attention.hip", "block_norm.hip"]
+           "kv4_attention.hip", "block_norm.hip", "w4.hip", "experts.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

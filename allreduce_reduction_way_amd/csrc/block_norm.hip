@@ -13,9 +13,9 @@
 // Both are bound by memory: each row is read and written once, in binary32
 // between.  A row lies in one workgroup, eight channels to a lane (twice eight
 // beyond 8192 channels), so that both norms' sums are exchanges within it.
-#include "block_norm.h"
 #include "host.h"
 #include "rows.h"
+#include "wave.h"
 
 namespace ar {
 namespace {
@@ -37,25 +37,6 @@ struct BlockArgs {
     float scale, eps;
 };
 
-// Eight channels of a row.  Rows start on any even address, and memory takes
-// 16-byte accesses there.
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
-
-template <bool NT>
-__device__ __forceinline__ u32x4 load_vec8(const uint16_t *p) {
-    const u32x4_any *v = reinterpret_cast<const u32x4_any *>(p);
-    return NT ? __builtin_nontemporal_load(v) : *v;
-}
-
-// The first n < 8 of them, zeros for the rest.
-__device__ __forceinline__ u32x4 load_few(const uint16_t *p, int n) {
-    u32x4 r = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < n) r[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
-    return r;
-}
-
 template <bool NT>
 __device__ __forceinline__ void store_vec8(uint16_t *p, const float (&f)[8], int n) {
     const u32x4 v = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
@@ -68,11 +49,6 @@ __device__ __forceinline__ void store_vec8(uint16_t *p, const float (&f)[8], int
 #pragma unroll
     for (int i = 0; i < 7; ++i)
         if (i < n) p[i] = (uint16_t)(v[i / 2] >> (i % 2 * 16));
-}
-
-__device__ __forceinline__ void widen(u32x4 v, float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[2 * i] = lo_f32(v[i]), f[2 * i + 1] = hi_f32(v[i]);
 }
 
 // Sums over the workgroup of N values, in the same order each time; every lane

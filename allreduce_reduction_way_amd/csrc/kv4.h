@@ -54,4 +54,36 @@ __device__ __forceinline__ uint32_t kv4_pair(uint32_t codes, float scale, int se
     return __builtin_bit_cast(uint32_t, r);
 }
 
+// Eight channels (four words) as codes, and the scale byte of their group;
+// four lanes side by side hold a group.
+__device__ __forceinline__ uint32_t kv4_quantise(u32x4 x, uint32_t &byte) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) most = max(most, max((x[i] << 16) & 0x7FFFFFFFu, x[i] & 0x7FFF0000u));
+    most = max(most, (uint32_t)__shfl_xor((int)most, 1));
+    most = max(most, (uint32_t)__shfl_xor((int)most, 2));
+    most >>= 16;
+    // the exponent, one more from 1.75 on (adding 0.25 carries), less two
+    const uint32_t e = (most + 0x20u) >> 7;
+    byte = min(max(e, 4u) - 2u, 252u);
+    const float scale = kv4_scale(byte);
+    const uint32_t w[4] = {x[0], x[1], x[2], x[3]};
+    uint32_t codes = 0;
+    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(codes, __builtin_bit_cast(bf16x2, w[0]), scale, 0);
+    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(codes, __builtin_bit_cast(bf16x2, w[1]), scale, 1);
+    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(codes, __builtin_bit_cast(bf16x2, w[2]), scale, 2);
+    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(codes, __builtin_bit_cast(bf16x2, w[3]), scale, 3);
+    if (most >= 0x7F80u) byte = kNanScale, codes = 0;
+    return codes;
+}
+
+// Eight codes as values.
+__device__ __forceinline__ u32x4 kv4_dequantise(uint32_t codes, uint32_t byte) {
+    const float scale = kv4_scale(byte);
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = byte == kNanScale ? 0x7FC07FC0u : kv4_pair(codes, scale, i);
+    return r;
+}
+
 }  // namespace ar

@@ -64,28 +64,6 @@ __device__ __forceinline__ uint8_t *tile_of(const Kv4Args &a, uint32_t slot, int
     return a.cache + tile * Kv4<D>::kBytes;
 }
 
-// Eight channels (four words) as codes, and the scale byte of their group.
-__device__ __forceinline__ uint32_t quantise(u32x4 x, uint32_t &byte) {
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) most = max(most, max((x[i] << 16) & 0x7FFFFFFFu, x[i] & 0x7FFF0000u));
-    most = max(most, (uint32_t)__shfl_xor((int)most, 1));
-    most = max(most, (uint32_t)__shfl_xor((int)most, 2));
-    most >>= 16;
-    // the exponent, one more from 1.75 on (adding 0.25 carries), less two
-    const uint32_t e = (most + 0x20u) >> 7;
-    byte = min(max(e, 4u) - 2u, 252u);
-    const float scale = kv4_scale(byte);
-    const uint32_t w[4] = {x[0], x[1], x[2], x[3]};
-    uint32_t codes = 0;
-    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(codes, __builtin_bit_cast(bf16x2, w[0]), scale, 0);
-    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(codes, __builtin_bit_cast(bf16x2, w[1]), scale, 1);
-    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(codes, __builtin_bit_cast(bf16x2, w[2]), scale, 2);
-    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(codes, __builtin_bit_cast(bf16x2, w[3]), scale, 3);
-    if (most >= 0x7F80u) byte = kNanScale, codes = 0;
-    return codes;
-}
-
 // Stores the codes of eight channels from c on into a V block, or two.
 template <int D>
 __device__ __forceinline__ void store_v(uint8_t *tile, int t, int c, uint32_t codes) {
@@ -127,7 +105,7 @@ __global__ __launch_bounds__(kThreads) void k_kv4_write(Kv4Args a) {
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
         uint32_t kb, vb;
-        const uint32_t kc = quantise(k[u], kb), vc = quantise(v[u], vb);
+        const uint32_t kc = kv4_quantise(k[u], kb), vc = kv4_quantise(v[u], vb);
         if (slot[u] < 0 || slot[u] >= (int64_t)a.capacity) continue;
         uint8_t *tile = tile_of<D>(a, (uint32_t)slot[u], head);
         const int t = (int)(slot[u] % kTile);
@@ -138,14 +116,6 @@ __global__ __launch_bounds__(kThreads) void k_kv4_write(Kv4Args a) {
             tile[Kv4<D>::v_scale(t, c / kGroup)] = (uint8_t)vb;
         }
     }
-}
-
-__device__ __forceinline__ u32x4 dequantise(uint32_t codes, uint32_t byte) {
-    const float scale = kv4_scale(byte);
-    u32x4 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = byte == kNanScale ? 0x7FC07FC0u : kv4_pair(codes, scale, i);
-    return r;
 }
 
 template <int D, bool VEC, int T, bool NT>
@@ -176,8 +146,8 @@ __global__ __launch_bounds__(kThreads) void k_kv4_read(Kv4Args a) {
     for (int u = 0; u < kSteps; ++u) {
         const int64_t t = first + u * kRows + lane / kLanes;
         if (t < a.tokens && u * kRows + lane / kLanes < T) {
-            store_row<VEC, NT>(a.k.p + t * a.k.ts + head * a.k.hs + c, dequantise(kc[u], kb[u]));
-            store_row<VEC, NT>(a.v.p + t * a.v.ts + head * a.v.hs + c, dequantise(vc[u], vb[u]));
+            store_row<VEC, NT>(a.k.p + t * a.k.ts + head * a.k.hs + c, kv4_dequantise(kc[u], kb[u]));
+            store_row<VEC, NT>(a.v.p + t * a.v.ts + head * a.v.hs + c, kv4_dequantise(vc[u], vb[u]));
         }
     }
 }

@@ -372,6 +372,60 @@ int block_norm_bwd(Args &a) {
     return ar_block_norm_bwd(dh, dz, y, x, post, gate, pre, dx, dy, dgate, dpost, dpre, ws, tokens, as_int(dim), scale, eps, a.stream());
 }
 
+// Tiles and bytes of a packed matrix (n_out, n_in); 0 where the C call refuses it.
+struct Packed {
+    int64_t tiles, bytes;
+    Packed(int64_t n_out, int64_t n_in) {
+        const int64_t one = ar_w4_bytes(1, n_in);
+        bytes = one < 0 ? 0 : one;
+        tiles = (n_out + 15) / 16;
+    }
+};
+
+// w, packed.
+template <bool BACK>
+int w4_pack(Args &a) {
+    const at::Tensor &w = a.peek(0, "w", 2);
+    const int64_t n_out = w.size(0), n_in = w.size(1);
+    const ar_rows r = a.plane("w", n_out, n_in);
+    const Packed size(n_out, n_in);
+    if (!size.bytes) return AR_EINVAL;
+    void *packed = a.tensor("packed", ScalarType::Byte, {size.tiles, size.bytes}).data_ptr();
+    if (BACK) return ar_w4_unpack(packed, r.p, r.token_stride, n_out, n_in, a.stream());
+    return ar_w4_pack(r.p, r.token_stride, packed, n_out, n_in, a.stream());
+}
+
+// x, packed, out.
+int w4_linear(Args &a) {
+    const at::Tensor &x = a.peek(0, "x", 2), &out = a.peek(2, "out", 2);
+    const int64_t tokens = x.size(0), n_in = x.size(1), n_out = out.size(1);
+    const ar_rows rx = a.plane("x", tokens, n_in);
+    const Packed size(n_out, n_in);
+    if (!size.bytes) return AR_EINVAL;
+    void *packed = a.tensor("packed", ScalarType::Byte, {size.tiles, size.bytes}).data_ptr();
+    const ar_rows ro = a.plane("out", tokens, n_out);
+    return ar_w4_linear(rx, packed, ro, tokens, n_out, n_in, a.stream());
+}
+
+// x, router, gate_up, down, out, choice, weight, workspace, scale.
+int w4_experts(Args &a) {
+    const at::Tensor &tx = a.peek(0, "x", 2), &tr = a.peek(1, "router", 2), &tg = a.peek(2, "gate_up", 3), &tc = a.peek(5, "choice", 2);
+    const int64_t tokens = tx.size(0), hidden = tx.size(1), experts = tr.size(0), inner = 8 * tg.size(1), top_k = tc.size(1);
+    const ar_rows x = a.plane("x", tokens, hidden);
+    void *router = a.tensor("router", ScalarType::BFloat16, {experts, hidden}).data_ptr();
+    const Packed up(2 * inner, hidden), down(hidden, inner);
+    const int64_t least = ar_w4_experts_workspace(tokens, hidden, inner, as_int(experts), as_int(top_k));
+    if (!up.bytes || !down.bytes || least < 0) return AR_EINVAL;
+    void *pu = a.tensor("gate_up", ScalarType::Byte, {experts, up.tiles, up.bytes}).data_ptr();
+    void *pd = a.tensor("down", ScalarType::Byte, {experts, down.tiles, down.bytes}).data_ptr();
+    const ar_rows out = a.plane("out", tokens, hidden);
+    void *choice = a.tensor("choice", ScalarType::Int, {tokens, top_k}).data_ptr();
+    void *weight = a.tensor("weight", ScalarType::Float, {tokens, top_k}).data_ptr();
+    void *ws = a.bytes("workspace", least).data_ptr();
+    const float scale = (float)a.number();
+    return ar_w4_experts(x, router, pu, pd, out, choice, weight, ws, tokens, hidden, inner, as_int(experts), as_int(top_k), scale, a.stream());
+}
+
 template <int (*CALL)(Args &), int COUNT>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t given) {
     try {
@@ -399,6 +453,10 @@ PyMethodDef methods[] = {
     method<kv4_attention, 15>("kv4_attention"),
     method<block_norm, 10>("block_norm"),
     method<block_norm_bwd, 16>("block_norm_bwd"),
+    method<w4_pack<false>, 3>("w4_pack"),
+    method<w4_pack<true>, 3>("w4_unpack"),
+    method<w4_linear, 4>("w4_linear"),
+    method<w4_experts, 10>("w4_experts"),
     {nullptr, nullptr, 0, nullptr},
 };
 

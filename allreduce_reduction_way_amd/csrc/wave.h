@@ -1,5 +1,5 @@
-// block_norm.h -- sums over the lanes of a wave, and bf16 pairs, for the
-// operators around a block.
+// wave.h -- for the operators around a block: sums over the lanes of a wave, bf16
+// pairs, and eight elements from any even address.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -40,6 +40,30 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     r[0] = (__bf16)lo;
     r[1] = (__bf16)hi;
     return __builtin_bit_cast(uint32_t, r);
+}
+
+// Eight elements of a row.  Rows start on any even address, and memory takes
+// 16-byte accesses there.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+template <bool NT>
+__device__ __forceinline__ u32x4 load_vec8(const uint16_t *p) {
+    const u32x4_any *v = reinterpret_cast<const u32x4_any *>(p);
+    return NT ? __builtin_nontemporal_load(v) : *v;
+}
+
+// The first n < 8 of them, zeros for the rest.
+__device__ __forceinline__ u32x4 load_few(const uint16_t *p, int n) {
+    u32x4 r = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < n) r[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
+    return r;
+}
+
+__device__ __forceinline__ void widen(u32x4 v, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[2 * i] = lo_f32(v[i]), f[2 * i + 1] = hi_f32(v[i]);
 }
 
 }  // namespace ar

@@ -482,6 +482,67 @@ int ar_block_norm_bwd(ar_rows h_grad, ar_rows z_grad, ar_rows y, ar_rows x, cons
                       float residual_scale, float eps, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * Weights of 4 bits: a matrix (n_out, n_in), n_in a multiple of 32, in
+ * ceil(n_out / 16) tiles of 1024 C + 256 ceil(C / 4) bytes, C = ceil(n_in / 128).
+ * Codes and scales are those of the 4-bit cache (see there); 32 inputs of an
+ * output share a scale.  Places in a tile, for output r of it and input
+ * k = 128 c + 32 a + i:
+ *     code byte   1024 c + (16 a + r) 16 + i/2, the even input in the low half
+ *     scale byte  1024 C + 256 (c/4) + (16 a + r) 4 + c%4
+ * What lies past n_out and n_in has codes of zero.  Scale bytes other than 2 to 252 and
+ * 255 are not specified, and of a group with 255 all weights are NaN.
+ *
+ * ar_w4_pack quantises bf16 weights by the cache's rule and writes every byte of
+ * the tiles; ar_w4_unpack gives the values back, exact in bf16.
+ *   w        (n_out, n_in) bf16, row_stride elements apart.
+ *   packed   ar_w4_bytes bytes, 16-byte aligned.
+ * n_in up to 2^20, n_out from 1 to 2^24; for packing and unpacking n_out * n_in
+ * (n_in rounded up to a multiple of 512) up to 2^33.
+ * ------------------------------------------------------------------------- */
+int64_t ar_w4_bytes(int64_t n_out, int64_t n_in);
+int ar_w4_pack(const void *w, int64_t row_stride, void *packed, int64_t n_out, int64_t n_in, void *stream);
+int ar_w4_unpack(const void *packed, void *w, int64_t row_stride, int64_t n_out, int64_t n_in, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * ar_w4_linear -- out = x W^T for packed weights: products of bf16 (exact) added
+ * up in binary32, rounded once.  Made for few tokens, whose time is that of
+ * reading the weights; more than 64 read them again for every 64.
+ *   x        (tokens, n_in), out (tokens, n_out).
+ *   packed   16-byte aligned.
+ * Up to 2^20 tokens.
+ * ------------------------------------------------------------------------- */
+int ar_w4_linear(ar_rows x, const void *packed, ar_rows out, int64_t tokens, int64_t n_out, int64_t n_in,
+                 void *stream);
+
+/* ---------------------------------------------------------------------------
+ * ar_w4_experts -- a mixture-of-experts layer of a few tokens.  For a token x:
+ *     l = R x               (products added up in 64 bits, rounded to binary32)
+ *     choice = the top_k experts of the largest l, from the largest (of two alike
+ *              the lower index first; NaN counts as larger than any number)
+ *     weight_j = scale * exp(l_j) / sum over the chosen of exp(l_i)
+ *     a_j = silu(G_j x) * (U_j x),  silu(v) = v / (1 + exp(-v))
+ *     out = sum over the chosen of weight_j * (D_j a_j)
+ * in binary32, but for a_j, which is rounded to 16 bits of its significand; out
+ * is rounded once.  An expert that a token does not take adds nothing to it,
+ * whatever its weights are.
+ *   x, out    (tokens, hidden).
+ *   router    (experts, hidden) bf16, contiguous.
+ *   gate_up   for each expert ar_w4_bytes(2 inner, hidden) bytes: the rows of G,
+ *             then those of U.
+ *   down      for each expert ar_w4_bytes(hidden, inner) bytes.
+ *   choice    (tokens, top_k) int32, weight (tokens, top_k) floats.
+ *   workspace ar_w4_experts_workspace bytes of any contents, 16-byte aligned.
+ *             Two calls in flight on one workspace are not allowed.  The size
+ *             never falls as tokens, inner or top_k grow.
+ * hidden and inner are multiples of 32, inner up to 2^19; up to 512 experts,
+ * top_k up to 16 and to experts, 2^20 tokens (64 at a time).
+ * ------------------------------------------------------------------------- */
+int64_t ar_w4_experts_workspace(int64_t tokens, int64_t hidden, int64_t inner, int experts, int top_k);
+int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void *down, ar_rows out,
+                  void *choice, void *weight, void *workspace, int64_t tokens, int64_t hidden,
+                  int64_t inner, int experts, int top_k, float scale, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Host-only helpers: no GPU needed, no HIP call made.
  * ------------------------------------------------------------------------- */
 

@@ -155,3 +155,122 @@ def test_a_gradient_that_would_be_lost_is_refused():
         ar.ar_block_norm([_bf(4, 64), x], _bf(4, 64), _bf(4, 64), stream=0)
     with torch.no_grad(), pytest.raises(TypeError, match="CUDA"):
         ar.ar_block_norm([_bf(4, 64), x], _bf(4, 64), _bf(4, 64), stream=0)
+
+
+# --------------------------------------------------------------- weights of 4 bits
+
+def test_w4_bytes():
+    assert ar.ar_w4_bytes(16, 128) == 1024 + 256
+    assert ar.ar_w4_bytes(17, 544) == 2 * (5 * 1024 + 2 * 256)
+    assert ar.ar_w4_bytes(1, 32) == 1280
+    assert ar.ar_w4_bytes(1 << 24, 1 << 20) == (1 << 20) * ((1 << 13) * 1024 + (1 << 11) * 256)
+    for bad in ((0, 128), (-1, 128), (16, 0), (16, 33), (16, 16), (16, -32), ((1 << 24) + 1, 32), (16, (1 << 20) + 32)):
+        with pytest.raises(ar.ArError):
+            ar.ar_w4_bytes(*bad)
+
+
+@pytest.mark.parametrize("fn", ["pack", "unpack"])
+def test_w4_pack_refuses(fn):
+    def call(**kw):
+        a = dict(w=FAKE, rs=160, packed=FAKE + 64 * MB, n=40, k=160)
+        a.update(kw)
+        args = (a["w"], a["rs"], a["packed"]) if fn == "pack" else (a["packed"], a["w"], a["rs"])
+        return getattr(ar.lib(), f"ar_w4_{fn}")(*args, a["n"], a["k"], 0)
+
+    for kw in (dict(w=0), dict(w=FAKE + 1), dict(rs=-160), dict(packed=0), dict(packed=FAKE + 64 * MB + 8), dict(n=0), dict(k=40), dict(k=0),
+               dict(n=1 << 24, k=1 << 14, rs=1 << 14, w=FAKE, packed=FAKE + (1 << 45))):
+        assert call(**kw) == ar.AR_EINVAL, kw
+    for kw in (dict(packed=FAKE + 160), dict(w=FAKE + 64 * MB + 512)):
+        assert call(**kw) == ar.AR_EALIAS, kw
+    if fn == "unpack":
+        assert call(rs=159) == ar.AR_EINVAL
+
+
+def test_w4_linear_refuses():
+    def call(**kw):
+        a = dict(x=rows(FAKE, 160), w=FAKE + MB, out=rows(FAKE + 2 * MB, 40), T=4, n=40, k=160)
+        a.update(kw)
+        return ar.lib().ar_w4_linear(a["x"], a["w"], a["out"], a["T"], a["n"], a["k"], 0)
+
+    for kw in (dict(T=-1), dict(T=(1 << 20) + 1), dict(n=0), dict(k=150), dict(x=rows(0, 160)), dict(x=rows(FAKE + 1, 160)), dict(x=rows(FAKE, -1)),
+               dict(w=0), dict(w=FAKE + MB + 8), dict(out=rows(0, 40)), dict(out=rows(FAKE + 2 * MB, 39)), dict(out=rows(FAKE + 2 * MB, 0))):
+        assert call(**kw) == ar.AR_EINVAL, kw
+    for kw in (dict(out=rows(FAKE, 160)), dict(out=rows(FAKE + MB, 40)), dict(out=rows(FAKE + MB + 1280 * 3 - 2, 40), k=128, x=rows(FAKE, 128))):
+        assert call(**kw) == ar.AR_EALIAS, kw
+    assert call(T=0, x=rows(0, 0), w=0) == ar.AR_OK
+
+
+def test_w4_experts_refuses():
+    def call(**kw):
+        a = dict(x=rows(FAKE, 160), r=FAKE + MB, gu=FAKE + 2 * MB, dn=FAKE + 4 * MB, out=rows(FAKE + 6 * MB, 160), c=FAKE + 7 * MB, w=FAKE + 8 * MB,
+                 ws=FAKE + 9 * MB, T=4, H=160, I=96, E=8, k=3, scale=1.0)
+        a.update(kw)
+        return ar.lib().ar_w4_experts(a["x"], a["r"], a["gu"], a["dn"], a["out"], a["c"], a["w"], a["ws"], a["T"], a["H"], a["I"], a["E"], a["k"],
+                                      a["scale"], 0)
+
+    for kw in (dict(T=-1), dict(T=(1 << 20) + 1), dict(H=0), dict(H=150), dict(I=0), dict(I=100), dict(I=(1 << 19) + 32), dict(E=0), dict(E=513),
+               dict(k=0), dict(k=9), dict(k=17, E=40), dict(scale=float("nan")), dict(scale=float("inf")), dict(x=rows(0, 160)), dict(x=rows(FAKE + 1, 160)),
+               dict(r=0), dict(r=FAKE + MB + 1), dict(gu=0), dict(gu=FAKE + 2 * MB + 8), dict(dn=0), dict(dn=FAKE + 4 * MB + 4),
+               dict(out=rows(0, 160)), dict(out=rows(FAKE + 6 * MB, 159)), dict(c=0), dict(c=FAKE + 7 * MB + 2), dict(w=0), dict(w=FAKE + 8 * MB + 1),
+               dict(ws=0), dict(ws=FAKE + 9 * MB + 8)):
+        assert call(**kw) == ar.AR_EINVAL, kw
+    for kw in (dict(out=rows(FAKE, 160)), dict(out=rows(FAKE + MB, 160)), dict(c=FAKE + 2 * MB), dict(w=FAKE + 4 * MB + 64), dict(ws=FAKE + 16),
+               dict(c=FAKE + 8 * MB + 4), dict(c=FAKE + 6 * MB), dict(ws=FAKE + 6 * MB), dict(w=FAKE + 9 * MB + 4096), dict(ws=FAKE + 3 * MB + 512 * 1024)):
+        assert call(**kw) == ar.AR_EALIAS, kw
+    assert call(T=0, x=rows(0, 0), r=0) == ar.AR_OK
+
+
+def test_w4_experts_workspace_never_falls():
+    for bad in ((-1, 64, 64, 4, 2), (1, 65, 64, 4, 2), (1, 64, 63, 4, 2), (1, 64, 64, 0, 1), (1, 64, 64, 4, 5), (1, 64, 64, 513, 2), (1, 64, 64, 64, 17)):
+        with pytest.raises(ar.ArError):
+            ar.ar_w4_experts_workspace(*bad)
+    axes = ([0, 1, 2, 63, 64, 65, 1000], [32, 512, 7168], [32, 96, 1024], [16, 64, 512], [1, 2, 8, 16])
+    import itertools
+    for n in range(5):
+        for rest in itertools.product(*(a for i, a in enumerate(axes) if i != n)):
+            sizes = [ar.ar_w4_experts_workspace(*rest[:n], v, *rest[n:]) for v in axes[n]]
+            assert sizes == sorted(sizes), (n, rest)
+
+
+def test_binding_checks_w4():
+    u8 = torch.uint8
+    w, packed = _bf(40, 160), torch.zeros(3, ar.ar_w4_bytes(16, 160), dtype=u8)
+    for fn in (lambda w, p: ar.ar_w4_pack(w, p, stream=0), lambda w, p: ar.ar_w4_unpack(p, w, stream=0)):
+        for bad, match in ((dict(w=w.float()), "bfloat16"), (dict(w=_bf(40, 4, 40)), "dimensions"), (dict(w=_bf(160, 40).t()), "contiguous"),
+                           (dict(p=packed[:2]), "packed: shape"), (dict(p=packed[:, 1:]), "packed: shape"), (dict(p=packed.int()), "uint8")):
+            with pytest.raises(ValueError, match=match):
+                fn(**{"w": w, "p": packed, **bad})
+        with pytest.raises(TypeError, match="CUDA"):
+            fn(w, packed)
+        with pytest.raises(ar.ArError):
+            fn(_bf(40, 50), packed)
+    x, out = _bf(4, 160), _bf(4, 40)
+    for bad, match in (((x.float(), packed, out), "bfloat16"), ((x, packed, _bf(5, 40)), "out: shape"), ((x, packed, _bf(4, 49)), "packed: shape"),
+                       ((_bf(4, 320)[:, ::2], packed, out), "contiguous"), ((_bf(4, 288), packed, out), "packed: shape"), ((x, packed, out.view(160)), "dim")):
+        with pytest.raises(ValueError, match=match):
+            ar.ar_w4_linear(*bad, stream=0)
+    with pytest.raises(TypeError, match="CUDA"):
+        ar.ar_w4_linear(x, packed, out, stream=0)
+    with pytest.raises(ar.ArError):
+        ar.ar_w4_linear(_bf(4, 33), packed, out, stream=0)
+
+
+def test_binding_checks_experts():
+    u8, H, I, E, k, T = torch.uint8, 160, 96, 8, 3, 4
+    good = dict(x=_bf(T, H), router=_bf(E, H), gate_up=torch.zeros(E, 2 * I // 16, ar.ar_w4_bytes(16, H), dtype=u8),
+                down=torch.zeros(E, H // 16, ar.ar_w4_bytes(16, I), dtype=u8), out=_bf(T, H), choice=torch.zeros(T, k, dtype=torch.int32),
+                weight=torch.zeros(T, k), workspace=torch.zeros(ar.ar_w4_experts_workspace(T, H, I, E, k), dtype=u8))
+    for bad, match in ((dict(x=_bf(T, 192)), "router: shape"), (dict(router=_bf(7, H)), "gate_up: shape"), (dict(router=_bf(E, 2 * H)[:, ::2]), "contiguous"),
+                       (dict(gate_up=good["gate_up"][:, :4]), "down: shape|gate_up"), (dict(down=good["down"][:, :9]), "down: shape"), (dict(out=_bf(T, 32)), "out: shape"),
+                       (dict(choice=torch.zeros(T, k)), "int32"), (dict(choice=torch.zeros(3, k, dtype=torch.int32)), "choice: shape"),
+                       (dict(weight=torch.zeros(T, 2)), "weight: shape"), (dict(workspace=torch.zeros(64, dtype=u8)), "workspace"),
+                       (dict(gate_up=good["gate_up"][0]), "dimensions")):
+        with pytest.raises(ValueError, match=match):
+            ar.ar_w4_experts(**{**good, **bad}, stream=0)
+    with pytest.raises(TypeError, match="CUDA"):
+        ar.ar_w4_experts(**good, stream=0)
+    with pytest.raises(ar.ArError):
+        ar.ar_w4_experts(**{**good, "choice": torch.zeros(T, 9, dtype=torch.int32), "weight": torch.zeros(T, 9)}, stream=0)
+    x = _bf(T, H).requires_grad_()
+    with pytest.raises(ValueError, match="requires a gradient"):
+        ar.ar_w4_experts(**{**good, "x": x}, stream=0)
