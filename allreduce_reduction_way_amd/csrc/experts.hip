@@ -7,22 +7,22 @@
 // For a few tokens it is bound by the bytes of the experts that some token takes,
 // each read once however many tokens do.
 //
-// Four launches, each waiting for the one before:
+// Five launches, each waiting for the one before:
 // k_router: logits, with sums in 64 bits, so that what an expert's place among a
 //   token's turns on is the logit and not the order of a sum.  Matrix
 //   instructions for 64 bits; the inputs are split over many workgroups.
-// k_choose: joins the splits, and a token's experts by counting how many come
-//   before each.
+// k_choose: joins the splits, and takes a token's experts from the largest logit
+//   down.
 // k_experts_up: a workgroup has one expert that is taken, some tiles of its gate
 //   and the same of its up part, and all the tokens that take it as columns.  The
 //   result goes on in two bf16 parts, whose sum is off by 2^-17 of it at most:
 //   rounding it to one would add as much to the output's error as the output's
-//   own rounding.
-// k_experts_down: a workgroup has some outputs of all experts; its waves take
-//   the experts' chunks in turn.  Eight tokens of an expert are a column tile,
-//   first parts in columns 0 to 7, second parts in 8 to 15.  Each wave adds what
-//   a token gets into rows of its own in LDS, so that no sum depends on which
-//   wave is first.
+//   own rounding.  Up to eight tokens of an expert are a group, which lies in
+//   memory as the next product takes it: first parts in columns 0 to 7, second
+//   parts in 8 to 15.
+// k_experts_down: a workgroup has one expert, some tiles of its outputs, and its
+//   groups one or two at a time in LDS.  Each token's result is left in binary32.
+// k_experts_sum: a token's results by weight, in the order of its experts.
 #include "host.h"
 #include "rows.h"
 #include "w4.h"
@@ -34,7 +34,8 @@ constexpr int kMaxExperts = 512, kMaxTopK = 16;
 constexpr int kTogether = 64;  // tokens of a pass
 constexpr int kMaxPairs = kTogether * kMaxTopK;
 constexpr int kLogits = 65536;  // partial logits of a pass, at most
-constexpr int kRouterWaves = 4, kUpWaves = 8, kDownWaves = 8;
+constexpr int kRouterWaves = 4, kChooseWaves = 8, kUpWaves = 8, kDownWaves = 8;
+constexpr int kColumns = 8;  // tokens of a group
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
@@ -46,7 +47,11 @@ struct ExpertsArgs {
     double *logits;  // [splits][tokens][experts]
     int32_t *choice;
     float *weight;
-    uint16_t *act;  // [tokens top_k][2][inner]
+    int32_t *used;        // how many experts are taken
+    int4 *taken;          // each of them: expert, first group, tokens
+    int32_t *group_pair;  // the pairs (token, place) of each group
+    uint16_t *act;        // [groups][chunks of inner][4 steps][64 lanes][8]
+    float *y;             // [pairs][hidden]
     int tokens, hidden, inner, experts, top_k, splits;
     float scale;
 };
@@ -63,57 +68,34 @@ __global__ __launch_bounds__(64 * kRouterWaves) void k_router(ExpertsArgs a) {
     const int units = a.hidden / 32, all = gridDim.z * kRouterWaves, mine = blockIdx.z * kRouterWaves + wave;
     const int begin = (int)((int64_t)units * mine / all), end = (int)((int64_t)units * (mine + 1) / all);
     f64x4 acc = {0, 0, 0, 0};
-    for (int u = begin; u < end; ++u) {
-        const u32x4 vw = load_vec8<false>(w + u * 32), vx = load_vec8<false>(x + u * 32);
-        float fw[8], fx[8];
-        widen(vw, fw);
-        widen(vx, fx);
+    for (int first = begin; first < end; first += 4) {
+        u32x4 vw[4], vx[4];
 #pragma unroll
-        for (int s = 0; s < 8; ++s) acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)fw[s], (double)fx[s], acc, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+            const int u = min(first + i, end - 1);
+            vw[i] = load_vec8<false>(w + u * 32);
+            vx[i] = load_vec8<false>(x + u * 32);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (first + i >= end) break;
+            float fw[8], fx[8];
+            widen(vw[i], fw);
+            widen(vx[i], fx);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)fw[s], (double)fx[s], acc, 0, 0, 0);
+        }
     }
     // a lane has experts q, 4 + q, 8 + q, 12 + q of token r
 #pragma unroll
     for (int i = 0; i < 4; ++i) part[wave][r][4 * i + q] = acc[i];
     __syncthreads();
     const int t = threadIdx.x / 16, e = threadIdx.x % 16;
-    if (token0 + t >= a.tokens || expert0 + e >= a.experts) return;
+    if (t >= 16 || token0 + t >= a.tokens || expert0 + e >= a.experts) return;
     double v = part[0][t][e];
 #pragma unroll
     for (int i = 1; i < kRouterWaves; ++i) v += part[i][t][e];
     a.logits[((int64_t)blockIdx.z * a.tokens + token0 + t) * a.experts + expert0 + e] = v;
-}
-
-// A token's experts.  The order is that of the logits from the largest, NaN
-// before all numbers, and of two alike the lower index first: a total one, so
-// that each place has one expert.
-__global__ __launch_bounds__(kMaxExperts) void k_choose(ExpertsArgs a) {
-    __shared__ uint32_t keys[kMaxExperts];
-    __shared__ float top[kMaxTopK];
-    const int token = blockIdx.x, e = threadIdx.x;
-    double v = 0;
-    if (e < a.experts)
-        for (int s = 0; s < a.splits; ++s) v += a.logits[((int64_t)s * a.tokens + token) * a.experts + e];
-    const float logit = (float)v + 0.0f;  // no negative zero
-    const uint32_t bits = __float_as_uint(logit);
-    // rising with the logit; nothing past the experts is taken
-    const uint32_t key = e >= a.experts ? 0 : logit != logit ? 0xFFFFFFFFu : bits >> 31 ? ~bits : bits | 0x80000000u;
-    keys[e] = key;
-    __syncthreads();
-    int place = 0;
-    for (int i = 0; i < a.experts; ++i) {
-        const uint32_t other = keys[i];
-        place += other > key || (other == key && i < e);
-    }
-    const bool taken = e < a.experts && place < a.top_k;
-    if (taken) {
-        a.choice[token * a.top_k + place] = e;
-        top[place] = logit;
-    }
-    __syncthreads();
-    if (e >= a.top_k) return;
-    float sum = 0;
-    for (int i = 0; i < a.top_k; ++i) sum += expf(top[i] - top[0]);
-    a.weight[token * a.top_k + e] = expf(top[e] - top[0]) / sum * a.scale;
 }
 
 // How many of the lower lanes are in the mask.
@@ -121,54 +103,155 @@ __device__ __forceinline__ int below(uint64_t mask) {
     return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
 
+// The largest of the wave's values.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
+    uint32_t r = __builtin_amdgcn_readlane((int)v, 0);
+    r = max(r, (uint32_t)__builtin_amdgcn_readlane((int)v, 16));
+    r = max(r, (uint32_t)__builtin_amdgcn_readlane((int)v, 32));
+    return max(r, (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
+}
+
+// A token's experts are taken from the largest logit down, NaN before all numbers,
+// and of two alike the lower index first: a total order, so that each is taken once.
+// A workgroup to a token: its waves add up the splits, the first one chooses.
+__global__ __launch_bounds__(64 * kChooseWaves) void k_choose(ExpertsArgs a) {
+    constexpr int kEach = kMaxExperts / 64;  // lane l has experts l, 64 + l, ...
+    __shared__ double part[kChooseWaves][64];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), token = blockIdx.x;
+    // a wave has 64 experts, and a part of the splits where there are fewer words
+    // of 64 than waves
+    const int words = a.experts <= 64 ? 1 : a.experts <= 128 ? 2 : a.experts <= 256 ? 4 : 8, parts = kChooseWaves / words;
+    const int64_t step = (int64_t)a.tokens * a.experts;
+    const double *p = a.logits + (int64_t)token * a.experts + min(wave % words * 64 + lane, a.experts - 1);
+    double sum = 0;
+    for (int s = wave / words; s < a.splits; s += 8 * parts) {
+        double t[8];  // all on their way at once
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = p[min(s + i * parts, a.splits - 1) * step];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += s + i * parts < a.splits ? t[i] : 0.0;
+    }
+    part[wave][lane] = sum;
+    __syncthreads();
+    if (wave) return;
+    uint32_t key[kEach];
+#pragma unroll
+    for (int w = 0; w < kEach; ++w) {
+        key[w] = 0;  // past the experts: below every logit's
+        if (w * 64 >= a.experts) continue;
+        const int e = w * 64 + lane;
+        if (e < a.experts) {
+            double v = part[w][lane];
+            for (int i = 1; i < parts; ++i) v += part[w + i * words][lane];
+            const float logit = (float)v + 0.0f;  // no negative zero
+            const uint32_t bits = __float_as_uint(logit);
+            // rises with the logit
+            key[w] = logit != logit ? 0xFFFFFFFFu : bits >> 31 ? ~bits : bits | 0x80000000u;
+        }
+    }
+    int expert = 0;
+    uint32_t mine = 0;
+    for (int j = 0; j < a.top_k; ++j) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int w = 0; w < kEach; ++w) top = max(top, key[w]);
+        top = wave_max(top);
+        int found = -1;
+#pragma unroll
+        for (int w = 0; w < kEach; ++w) {
+            if (w * 64 >= a.experts) break;
+            const uint64_t mask = __ballot(key[w] == top);
+            if (found < 0 && mask) {
+                const int at = __builtin_ctzll(mask);
+                found = w * 64 + at;
+                if (lane == at) key[w] = 0;
+            }
+        }
+        if (lane == j) expert = found, mine = top;
+    }
+    const float logit = mine == 0xFFFFFFFFu ? __builtin_nanf("") : __uint_as_float(mine >> 31 ? mine & 0x7FFFFFFFu : ~mine);
+    const float first = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(logit)));
+    const float e = lane < a.top_k ? expf(logit - first) : 0.0f;
+    const float weight = e / row16_sum(e) * a.scale;  // kMaxTopK lanes side by side
+    if (lane < a.top_k) {
+        a.choice[token * a.top_k + lane] = expert;
+        a.weight[token * a.top_k + lane] = weight;
+    }
+}
+
 // One expert's tiles [tile0, tile0 + N) of the gate and of the up part, for all
-// tokens that take it.
+// tokens that take it.  U: chunks that a wave has on their way at once.
 template <int N, int U>
 __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(ExpertsArgs a) {
-    __shared__ int taken[kMaxExperts];
-    __shared__ int list[kMaxPairs];  // the pairs (token, place) that take the expert
+    __shared__ int chosen[kMaxPairs], counts[kMaxExperts];
+    __shared__ int list[kTogether];  // the pairs (token, place) that take the expert
     __shared__ f32x4 part[kUpWaves][2 * N][64];
     const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int pairs = a.tokens * a.top_k;
 
-    // the expert: the blockIdx.y-th of those that are taken
-    for (int i = threadIdx.x; i < kMaxExperts; i += blockDim.x) taken[i] = 0;
+    // the expert: the blockIdx.y-th of those that are taken, and the groups before its
+    for (int i = threadIdx.x; i < kMaxExperts; i += blockDim.x) counts[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < pairs; i += blockDim.x) taken[a.choice[i]] = 1;
+    for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
+        const int e = a.choice[i];
+        chosen[i] = e;
+        atomicAdd(&counts[e], 1);
+    }
     __syncthreads();
-    int expert = -1, before = 0;
+    int expert = -1, base = 0, before = 0, groups = 0;
     for (int w = 0; w < a.experts; w += 64) {
-        const uint64_t mask = __ballot(w + lane < a.experts && taken[min(w + lane, kMaxExperts - 1)]);
-        const int at = (int)blockIdx.y - before, n = __popcll(mask);
-        if (at < n) {
-            expert = w + __builtin_ctzll(__ballot((mask >> lane & 1) && below(mask) == at));
-            break;
+        const int n = w + lane < a.experts ? counts[min(w + lane, kMaxExperts - 1)] : 0, g = (n + kColumns - 1) / kColumns;
+        const uint64_t mask = __ballot(n > 0);
+        int left = 0, sum = 0;  // groups of the lanes below, of all lanes
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {  // at most kTogether / kColumns = 8 to an expert
+            const uint64_t bit = __ballot(g >> b & 1);
+            left += below(bit) << b;
+            sum += __popcll(bit) << b;
         }
-        before += n;
+        const int at = (int)blockIdx.y - before;
+        if (at >= 0 && at < (int)__popcll(mask)) {
+            const int l = __builtin_ctzll(__ballot((mask >> lane & 1) && below(mask) == at));
+            expert = w + l;
+            base = groups + __builtin_amdgcn_readlane(left, l);
+        }
+        before += __popcll(mask);
+        groups += sum;
     }
     if (expert < 0) return;
-    expert = __builtin_amdgcn_readfirstlane(expert);
     int count = 0;
     for (int p = 0; p < pairs; p += 64) {
-        const bool mine = p + lane < pairs && a.choice[min(p + lane, pairs - 1)] == expert;
+        const bool mine = p + lane < pairs && chosen[min(p + lane, pairs - 1)] == expert;
         const uint64_t mask = __ballot(mine);
         if (mine && wave == 0) list[count + below(mask)] = p + lane;
         count += __popcll(mask);
     }
     __syncthreads();
+    if (blockIdx.x == 0 && (int)threadIdx.x < count) {
+        if (threadIdx.x == 0) {
+            a.taken[blockIdx.y] = int4{expert, base, count, 0};
+            if (blockIdx.y == 0) *a.used = before;
+        }
+        a.group_pair[base * kColumns + threadIdx.x] = list[threadIdx.x];
+    }
 
     const int half = a.inner / 16;  // tiles of the gate
     const int tile0 = blockIdx.x * N;
-    const uint8_t *base = a.gate_up + expert * a.up.bytes();
+    const uint8_t *from = a.gate_up + expert * a.up.bytes();
     const uint8_t *tile[2 * N];
 #pragma unroll
     for (int t = 0; t < N; ++t) {
         const int at = min(tile0 + t, half - 1);
-        tile[t] = base + at * a.up.tile_bytes;
-        tile[N + t] = base + (half + at) * a.up.tile_bytes;
+        tile[t] = from + at * a.up.tile_bytes;
+        tile[N + t] = from + (half + at) * a.up.tile_bytes;
     }
     for (int first = 0; first < count; first += 16) {
-        const uint16_t *row = a.x.p + list[min(first + r, count - 1)] / a.top_k * a.x.ts;
+        const bool mine = first + r < count;
+        const uint16_t *row = a.x.p + list[min(first + r, count - 1)] / a.top_k * a.x.ts + q * 32;
         f32x4 acc[2 * N];
 #pragma unroll
         for (int t = 0; t < 2 * N; ++t) acc[t] = f32x4{0, 0, 0, 0};
@@ -181,18 +264,25 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(ExpertsArgs a) {
                 const int c = chunk + u * kUpWaves;
 #pragma unroll
                 for (int t = 0; t < 2 * N; ++t) {
-                    codes[u][t] = *reinterpret_cast<const u32x4 *>(tile[t] + w4_code_at(c, lane));
-                    byte[u][t] = tile[t][w4_scale_at(a.up.chunks, c, lane)];
+                    codes[u][t] = w4_codes(tile[t], c, lane);
+                    byte[u][t] = w4_scale(tile[t], a.up.chunks, c, lane);
                 }
-                load_inputs(x[u], row, c * kW4Chunk + q * 32, a.hidden);
+                const int at = min(c * kW4Chunk, a.hidden - 32 - q * 32);  // past the row: inside it
+                load_few_inputs(x[u], row + at, 8, mine);
             }
 #pragma unroll
-            for (int u = 0; u < M; ++u)
+            for (int u = 0; u < M; ++u) {
+                const int c = chunk + u * kUpWaves;
+                if ((c + 1) * kW4Chunk > a.hidden && c * kW4Chunk + q * 32 >= a.hidden) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) x[u][s] = u32x4{0, 0, 0, 0};
+                }
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
 #pragma unroll
                     for (int t = 0; t < 2 * N; ++t)
                         acc[t] = w4_product(w4_operand(codes[u][t], kv4_scale(byte[u][t]), s), x[u][s], acc[t]);
+            }
         };
         int c = wave;
         for (; c + (U - 1) * kUpWaves < a.up.chunks; c += U * kUpWaves) step(c, std::integral_constant<int, U>());
@@ -201,13 +291,16 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(ExpertsArgs a) {
 #pragma unroll
         for (int t = 0; t < 2 * N; ++t) part[wave][t][lane] = acc[t];
         __syncthreads();
-        for (int item = threadIdx.x; item < N * 64; item += blockDim.x) {
+        for (int item = threadIdx.x; item < N * 64; item += 64 * kUpWaves) {
             const int t = item / 64, at = item % 64, column = first + at % 16;
             if (column >= count || tile0 + t >= half) continue;
             f32x4 g = part[0][t][at], u = part[0][N + t][at];
 #pragma unroll
             for (int w = 1; w < kUpWaves; ++w) g += part[w][t][at], u += part[w][N + t][at];
-            uint16_t *to = a.act + (int64_t)list[column] * 2 * a.inner + (tile0 + t) * 16 + at / 16 * 4;
+            // element k of chunk c is one of step s of lane (column, k's 32)
+            const int k = (tile0 + t) * 16 + at / 16 * 4, c = k / kW4Chunk, s = k % 32 / 8;
+            uint16_t *to = a.act + ((((int64_t)(base + column / kColumns) * a.down.chunks + c) * 4 + s) * 64 +
+                                    k % kW4Chunk / 32 * 16 + column % kColumns) * 8 + k % 8;
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -224,119 +317,135 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(ExpertsArgs a) {
                 lo[i] = bf16_pair(rest[0], rest[1]);
             }
             *reinterpret_cast<uint2 *>(to) = uint2{hi[0], hi[1]};
-            *reinterpret_cast<uint2 *>(to + a.inner) = uint2{lo[0], lo[1]};
+            *reinterpret_cast<uint2 *>(to + kColumns * 8) = uint2{lo[0], lo[1]};
         }
     }
 }
 
-// N tiles of the outputs.
-template <int N>
+// One expert's tiles, N to a wave, for up to G groups at a time.  Chunks come to LDS
+// in blocks of kBlock / G.
+constexpr int kBlock = 16;
+
+template <int N, int G>
 __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(ExpertsArgs a) {
-    extern __shared__ f32x4 sums[];  // [waves][tokens][4 N]
-    __shared__ int counts[kMaxExperts], starts[kMaxExperts];
-    __shared__ int expert_of[kMaxExperts], used;
-    __shared__ int list[kMaxPairs];
-    __shared__ float weights[kMaxPairs];
+    extern __shared__ u32x4 act[];  // [groups][chunks of a block][4 steps][64 lanes]
+    if ((int)blockIdx.y >= *a.used) return;
     const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int pairs = a.tokens * a.top_k;
-
-    // The pairs by expert.  Their order within one is left open: it says which
-    // column a token is in, and no more.
-    for (int i = threadIdx.x; i < kMaxExperts; i += blockDim.x) counts[i] = 0;
-    for (int i = threadIdx.x; i < kDownWaves * a.tokens * 4 * N; i += blockDim.x) sums[i] = f32x4{0, 0, 0, 0};
-    __syncthreads();
-    constexpr int kEach = kMaxPairs / (64 * kDownWaves);
-    int place[kEach], expert[kEach];
+    const int4 mine = a.taken[blockIdx.y];
+    const int expert = __builtin_amdgcn_readfirstlane(mine.x), base = __builtin_amdgcn_readfirstlane(mine.y), count = __builtin_amdgcn_readfirstlane(mine.z);
+    const int chunks = a.down.chunks, groups = (count + kColumns - 1) / kColumns;
+    const int tile0 = (blockIdx.x * kDownWaves + wave) * N;
+    const uint8_t *tile[N];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int p = threadIdx.x + i * 64 * kDownWaves;
-        expert[i] = p < pairs ? a.choice[p] : -1;
-        if (expert[i] >= 0) place[i] = atomicAdd(&counts[expert[i]], 1);
-    }
-    __syncthreads();
-    if (wave == 0) {
-        int start = 0, slot = 0;
-        for (int w = 0; w < a.experts; w += 64) {
-            const int e = w + lane, n = e < a.experts ? counts[min(e, kMaxExperts - 1)] : 0;
-            int sum = n;
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) {
-                const int left = __shfl_up(sum, d);
-                if (lane >= d) sum += left;
-            }
-            const uint64_t mask = __ballot(n > 0);
-            if (n > 0) {
-                expert_of[slot + below(mask)] = e;
-                starts[e] = start + sum - n;
-            }
-            start += __shfl(sum, 63);
-            slot += __popcll(mask);
-        }
-        if (lane == 0) used = slot;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int p = threadIdx.x + i * 64 * kDownWaves;
-        if (expert[i] >= 0) {
-            list[starts[expert[i]] + place[i]] = p;
-            weights[starts[expert[i]] + place[i]] = a.weight[p];
-        }
-    }
-    __syncthreads();
-
-    const int tile0 = blockIdx.x * N, chunks = a.down.chunks, items = used * chunks;
-    f32x4 *mine = sums + wave * a.tokens * 4 * N;
-    for (int item = wave; item < items; item += kDownWaves) {
-        const int e = __builtin_amdgcn_readfirstlane(expert_of[item / chunks]), c = item % chunks;
-        const int start = __builtin_amdgcn_readfirstlane(starts[e]), count = __builtin_amdgcn_readfirstlane(counts[e]);
-        const uint8_t *base = a.dn + e * a.down.bytes();
-        u32x4 codes[N];
-        uint32_t byte[N];
+    for (int t = 0; t < N; ++t) tile[t] = a.dn + expert * a.down.bytes() + min(tile0 + t, a.down.tiles - 1) * a.down.tile_bytes;
+    u32x4 codes[2][N];
+    uint32_t byte[2][N];
+    const auto load = [&](int b, int c) {
 #pragma unroll
         for (int t = 0; t < N; ++t) {
-            const uint8_t *tile = base + min(tile0 + t, a.down.tiles - 1) * a.down.tile_bytes;
-            codes[t] = *reinterpret_cast<const u32x4 *>(tile + w4_code_at(c, lane));
-            byte[t] = tile[w4_scale_at(chunks, c, lane)];
+            codes[b][t] = w4_codes(tile[t], c, lane);
+            byte[b][t] = w4_scale(tile[t], chunks, c, lane);
         }
-        for (int first = 0; first < count; first += 8) {
-            const int at = start + min(first + r % 8, count - 1), pair = list[at];
-            u32x4 x[4];
-            load_inputs(x, a.act + ((int64_t)pair * 2 + r / 8) * a.inner, c * kW4Chunk + q * 32, a.inner);
-            const float weight = weights[at];
-            const int token = pair / a.top_k;
+    };
+    for (int first = 0; first < groups; first += G) {
+        f32x4 acc[N][G];
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+#pragma unroll
+            for (int g = 0; g < G; ++g) acc[t][g] = f32x4{0, 0, 0, 0};
+        for (int block = 0; block < chunks; block += kBlock / G) {
+            const int some = min(chunks - block, kBlock / G);
+            load(0, block);
+            if (first + block) __syncthreads();
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const u32x4 *from = reinterpret_cast<const u32x4 *>(a.act) + ((int64_t)(base + min(first + g, groups - 1)) * chunks + block) * 256;
+                for (int i = threadIdx.x; i < some * 256; i += 64 * kDownWaves) {
+                    const int k = (block + i / 256) * kW4Chunk + i % 64 / 16 * 32;
+                    act[g * (some * 256) + i] = k < a.inner ? from[i] : u32x4{0, 0, 0, 0};  // nothing was written past it
+                }
+            }
+            __syncthreads();
+            for (int at = 0; at < some; at += 2) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int c = at + b;
+                    if (c >= some) break;
+                    load(1 - b, block + min(c + 1, some - 1));  // past the end: again what is there
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        u32x4 x[G];
+#pragma unroll
+                        for (int g = 0; g < G; ++g) x[g] = act[(g * some + c) * 256 + s * 64 + lane];
+#pragma unroll
+                        for (int t = 0; t < N; ++t) {
+                            const bf16x8 w = w4_operand(codes[b][t], kv4_scale(byte[b][t]), s);
+#pragma unroll
+                            for (int g = 0; g < G; ++g) acc[t][g] = w4_product(w, x[g], acc[t][g]);
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int column = (first + g) * kColumns + r;
+            const bool store = r < kColumns && column < count;
+            const int pair = a.group_pair[base * kColumns + (store ? column : 0)];
 #pragma unroll
             for (int t = 0; t < N; ++t) {
-                f32x4 d = {0, 0, 0, 0};
-#pragma unroll
-                for (int s = 0; s < 4; ++s) d = w4_product(w4_operand(codes[t], kv4_scale(byte[t]), s), x[s], d);
+                f32x4 d = acc[t][g];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) d[i] = dpp_add<0x128, 0xf>(d[i]);  // the two parts
-                if (r < 8 && first + r < count) {
-                    f32x4 &to = mine[(token * N + t) * 4 + q];
-                    to += weight * d;
-                }
-                // the next expert's columns are others: its lanes read what these wrote
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                if (store && tile0 + t < a.down.tiles)  // hidden is a multiple of 32
+                    *reinterpret_cast<f32x4 *>(a.y + (int64_t)pair * a.hidden + (tile0 + t) * 16 + q * 4) = d;
             }
         }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.tokens * 4 * N; i += blockDim.x) {
-        f32x4 v = sums[i];
-        for (int w = 1; w < kDownWaves; ++w) v += sums[w * a.tokens * 4 * N + i];
-        const int token = i / (4 * N);
-        const int64_t n = (int64_t)tile0 * 16 + i % (4 * N) * 4;
-        if (n >= a.hidden) continue;  // n_out is a multiple of 32
-        uint16_t *to = const_cast<uint16_t *>(a.out.p) + token * a.out.ts + n;
-        typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
-        *reinterpret_cast<u32x2_any *>(to) = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-    }
+}
+
+// Four outputs of a token to a lane.
+__global__ __launch_bounds__(kThreads) void k_experts_sum(ExpertsArgs a) {
+    const int n = (blockIdx.x * kThreads + threadIdx.x) * 4, token = blockIdx.y;
+    if (n >= a.hidden) return;
+    const float *y = a.y + (int64_t)token * a.top_k * a.hidden + n;
+    f32x4 v = {0, 0, 0, 0};
+    for (int j = 0; j < a.top_k; ++j) v += a.weight[token * a.top_k + j] * *reinterpret_cast<const f32x4 *>(y + (int64_t)j * a.hidden);
+    typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+    uint16_t *to = const_cast<uint16_t *>(a.out.p) + token * a.out.ts + n;
+    *reinterpret_cast<u32x2_any *>(to) = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
 }
 
 int launch3(const void *fn, dim3 grid, unsigned block, unsigned lds, ExpertsArgs &a, void *stream) {
     void *args[] = {&a};
     return hipLaunchKernel(fn, grid, dim3(block), args, lds, static_cast<hipStream_t>(stream)) == hipSuccess ? AR_OK : AR_ELAUNCH;
+}
+
+// Groups of a pass, at most: one for every pair, and for every expert one that is
+// not full.
+int64_t most_groups(int64_t tokens, int experts, int top_k) {
+    const int64_t pairs = (tokens < kTogether ? tokens : kTogether) * top_k, full = experts + pairs / kColumns;
+    return pairs < full ? pairs : full;
+}
+
+// The workspace: logits, the experts that are taken, the groups' pairs, what goes
+// into the second product, and what comes out.
+struct Places {
+    int64_t used, taken, pair, act, y, end;
+    Places(int64_t tokens, int64_t hidden, int chunks, int experts, int top_k) {
+        const int64_t most = most_groups(tokens, experts, top_k), pairs = (tokens < kTogether ? tokens : kTogether) * top_k;
+        used = kLogits * 8;
+        taken = used + 16;
+        pair = taken + most * 16;
+        act = pair + most * kColumns * 4;
+        y = act + most * chunks * 4 * 64 * 16;
+        end = y + pairs * hidden * 4;
+    }
+};
+
+template <int N>
+const void *pick_down(bool two) {
+    return two ? reinterpret_cast<const void *>(&k_experts_down<N, 2>) : reinterpret_cast<const void *>(&k_experts_down<N, 1>);
 }
 
 bool valid_sizes(int64_t tokens, int64_t hidden, int64_t inner, int experts, int top_k, W4Shape *up, W4Shape *down) {
@@ -354,8 +463,7 @@ extern "C" {
 int64_t ar_w4_experts_workspace(int64_t tokens, int64_t hidden, int64_t inner, int experts, int top_k) {
     W4Shape up, down;
     if (!valid_sizes(tokens, hidden, inner, experts, top_k, &up, &down)) return AR_EINVAL;
-    const int64_t pairs = (tokens < kTogether ? tokens : kTogether) * top_k;
-    return kLogits * 8 + pairs * 4 * inner;
+    return Places(tokens, hidden, down.chunks, experts, top_k).end;
 }
 
 int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void *down, ar_rows out, void *choice, void *weight,
@@ -380,8 +488,12 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
     if (ro.overlaps(rx)) return AR_EALIAS;
     a.gate_up = static_cast<const uint8_t *>(gate_up), a.dn = static_cast<const uint8_t *>(down);
     a.router = static_cast<const uint16_t *>(router);
-    a.logits = static_cast<double *>(workspace);
-    a.act = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(workspace) + kLogits * 8);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const Places at_ws(tokens, hidden, a.down.chunks, experts, top_k);
+    a.logits = reinterpret_cast<double *>(ws);
+    a.used = reinterpret_cast<int32_t *>(ws + at_ws.used), a.taken = reinterpret_cast<int4 *>(ws + at_ws.taken);
+    a.group_pair = reinterpret_cast<int32_t *>(ws + at_ws.pair);
+    a.act = reinterpret_cast<uint16_t *>(ws + at_ws.act), a.y = reinterpret_cast<float *>(ws + at_ws.y);
     a.hidden = (int)hidden, a.inner = (int)inner, a.experts = experts, a.top_k = top_k, a.scale = scale;
     for (int64_t at = 0; at < tokens; at += kTogether) {
         a.tokens = (int)(tokens - at < kTogether ? tokens - at : kTogether);
@@ -394,17 +506,23 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         if (a.splits < 1) a.splits = 1;
         int rc = launch3(reinterpret_cast<const void *>(&k_router), dim3(expert_tiles, token_tiles, a.splits), 64 * kRouterWaves, 0, a, stream);
         if (rc != AR_OK) return rc;
-        rc = launch3(reinterpret_cast<const void *>(&k_choose), dim3(a.tokens), (unsigned)round_up(experts, 64), 0, a, stream);
+        rc = launch3(reinterpret_cast<const void *>(&k_choose), dim3(a.tokens), 64 * kChooseWaves, 0, a, stream);
         if (rc != AR_OK) return rc;
         const int slots = a.tokens * top_k < experts ? a.tokens * top_k : experts;
         const int half = (int)inner / 16;
-        const bool wide = (int64_t)slots * half >= 2048;
-        rc = launch3(wide ? reinterpret_cast<const void *>(&k_experts_up<2, 2>) : reinterpret_cast<const void *>(&k_experts_up<1, 4>),
-                     dim3(wide ? (half + 1) / 2 : half, slots), 64 * kUpWaves, 0, a, stream);
+        const bool two_up = (int64_t)slots * half >= 1024 || a.tokens * top_k >= 8 * experts;
+        rc = launch3(two_up ? reinterpret_cast<const void *>(&k_experts_up<2, 1>) : reinterpret_cast<const void *>(&k_experts_up<1, 2>),
+                     dim3(two_up ? (half + 1) / 2 : half, slots), 64 * kUpWaves, 0, a, stream);
         if (rc != AR_OK) return rc;
-        const int n = 1;
-        rc = launch3(reinterpret_cast<const void *>(&k_experts_down<1>), dim3((a.down.tiles + n - 1) / n), 64 * kDownWaves,
-                     kDownWaves * a.tokens * 64 * n, a, stream);
+        const int64_t tiles = (int64_t)slots * a.down.tiles;
+        const int n = tiles >= 4 * 8192 ? 4 : tiles >= 2 * 4096 ? 2 : 1;
+        const bool two = a.tokens > kColumns;
+        const int per = n * kDownWaves;
+        const int block = a.down.chunks < kBlock / (two ? 2 : 1) ? a.down.chunks : kBlock / (two ? 2 : 1);
+        rc = launch3(n == 4 ? pick_down<4>(two) : n == 2 ? pick_down<2>(two) : pick_down<1>(two), dim3((a.down.tiles + per - 1) / per, slots),
+                     64 * kDownWaves, block * (two ? 2 : 1) * 4096, a, stream);
+        if (rc != AR_OK) return rc;
+        rc = launch3(reinterpret_cast<const void *>(&k_experts_sum), dim3(((int)hidden + 4 * kThreads - 1) / (4 * kThreads), a.tokens), kThreads, 0, a, stream);
         if (rc != AR_OK) return rc;
     }
     return AR_OK;

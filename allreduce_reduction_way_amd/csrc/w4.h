@@ -41,10 +41,13 @@ inline bool w4_shape(int64_t n_out, int64_t n_in, W4Shape *s) {
     return true;
 }
 
-// Where a lane's codes and scale of chunk c lie in a tile.
-__device__ __forceinline__ int w4_code_at(int c, int lane) { return c * kW4Codes + lane * 16; }
-__device__ __forceinline__ int w4_scale_at(int chunks, int c, int lane) {
-    return chunks * kW4Codes + c / 4 * kW4Scales + lane * 4 + c % 4;
+// A lane's codes and scale byte of chunk c of a tile.  (The tile and the chunk are
+// the same in all lanes: scalar registers hold the address, and a lane its offset.)
+__device__ __forceinline__ u32x4 w4_codes(const uint8_t *tile, int c, int lane) {
+    return *reinterpret_cast<const u32x4 *>(tile + c * kW4Codes + (uint32_t)lane * 16u);
+}
+__device__ __forceinline__ uint32_t w4_scale(const uint8_t *tile, int chunks, int c, int lane) {
+    return (tile + chunks * kW4Codes + c / 4 * kW4Scales + c % 4)[(uint32_t)lane * 4u];
 }
 
 // The weights' operand of step s: eight codes of a lane as bf16, exactly.
@@ -55,17 +58,73 @@ __device__ __forceinline__ bf16x8 w4_operand(u32x4 codes, float scale, int s) {
     return __builtin_bit_cast(bf16x8, v);
 }
 
-// The 32 elements from k on of a row of n, the other operand of four steps; zeros
-// past the row, where codes are zeros too, but what memory holds need not be a
-// number.
-__device__ __forceinline__ void load_inputs(u32x4 (&x)[4], const uint16_t *row, int k, int n) {
+// The other operand of a chunk's four steps comes from rows of n elements, sixteen
+// of them as columns.  A compute unit takes 64 bytes in a cycle where four lanes side
+// by side ask for them, and 16 where each asks for another row, as the steps
+// need them.  So lane l asks for 16 bytes of row l / 4, from element 8 (l % 4) on,
+// and a wave turns what it gets through a piece of LDS of its own: x[i] is elements
+// 32 i + 8 (l % 4) .. + 7 of row l / 4 until a Stage has made it 32 a + 8 i .. + 7
+// of row r.  (Asking as the steps need them, 16 tokens times 8192 x 28672
+// took 59 us, and RIGHT_US with this.)  Past the row the stage leaves zeros:
+// codes are zeros there too, but infinity times zero is none.
+//
+// The loads stand behind no branch, where the compiler would wait for each: past a
+// row's end they take its last elements again.
+__device__ __forceinline__ void load_inputs(u32x4 (&x)[4], const uint16_t *row, int chunk, int n) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) x[s] = u32x4{0, 0, 0, 0};
-    if (k < n) {
+    for (int i = 0; i < 4; ++i) x[i] = load_vec8<false>(row + min(chunk * kW4Chunk + 32 * i, n - 32));
+}
+
+// The same for few columns, of which lane (r, q) has `row`, from element 32 q on:
+// loaded as the steps need them by the lanes that have a column, so that nothing is
+// turned.  Four columns take a quarter of the time of sixteen.  What the other lanes
+// have is left open: it stays in their columns.
+__device__ __forceinline__ void load_few_inputs(u32x4 (&x)[4], const uint16_t *row, int step, bool mine) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) x[s] = load_vec8<false>(row + k + 8 * s);
+    for (int s = 0; s < 4; ++s) asm("" : "=v"(x[s]));
+    if (mine) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) x[s] = load_vec8<false>(row + s * step);
     }
 }
+
+// A wave's piece of LDS: 16 rows of 256 bytes, 320 apart, with the 16-byte blocks of
+// every 64 bytes in another order from four rows to the next.  Eight lanes at a time
+// write two rows' 64 bytes, and read a block of eight rows: neither meets in a bank.
+constexpr int kStageRow = 320 / 16, kStage = 16 * kStageRow;  // in 16 bytes
+
+struct Stage {
+    u32x4 *to;
+    const u32x4 *from[4];
+
+    __device__ __forceinline__ Stage(u32x4 *p, int lane) {
+        const int row = lane / 4, r = lane % 16;
+        to = p + row * kStageRow + (lane % 4 ^ row / 4);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) from[s] = p + r * kStageRow + lane / 16 * 4 + (s ^ r / 4);
+    }
+    // Inputs of chunk `chunk`, of rows of n.
+    __device__ __forceinline__ void put(u32x4 (&x)[4], int chunk, int n) const {
+        if ((chunk + 1) * kW4Chunk > n) {  // the same in all lanes
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+                if (chunk * kW4Chunk + 32 * i >= n) x[i] = u32x4{0, 0, 0, 0};
+        }
+        // one wave's accesses to LDS stay in order; the fences keep the compiler's
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[4 * i] = x[i];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    __device__ __forceinline__ void get(u32x4 (&x)[4]) const {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) x[s] = *from[s];
+    }
+    __device__ __forceinline__ void turn(u32x4 (&x)[4], int chunk, int n) const {
+        put(x, chunk, n);
+        get(x);
+    }
+};
 
 __device__ __forceinline__ f32x4 w4_product(bf16x8 w, u32x4 x, f32x4 acc) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);

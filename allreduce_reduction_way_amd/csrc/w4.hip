@@ -32,8 +32,8 @@ __global__ __launch_bounds__(kThreads) void k_w4_pack(PackArgs a) {
     const uint32_t codes = kv4_quantise(x, byte);
     uint8_t *tile = a.packed + n / 16 * a.s.tile_bytes;
     const int c = k / kW4Chunk, lane = k % kW4Chunk / 32 * 16 + (int)(n % 16);
-    if (c < a.s.chunks) *reinterpret_cast<uint32_t *>(tile + w4_code_at(c, lane) + k % 32 / 2) = codes;
-    if (k % 32 == 0) tile[w4_scale_at(a.s.chunks, c, lane)] = (uint8_t)byte;
+    if (c < a.s.chunks) *reinterpret_cast<uint32_t *>(tile + c * kW4Codes + lane * 16 + k % 32 / 2) = codes;
+    if (k % 32 == 0) tile[a.s.chunks * kW4Codes + c / 4 * kW4Scales + lane * 4 + c % 4] = (uint8_t)byte;
 }
 
 struct UnpackArgs {
@@ -51,9 +51,11 @@ __global__ __launch_bounds__(kThreads) void k_w4_unpack(UnpackArgs a) {
     if (n >= a.s.n_out) return;
     const uint8_t *tile = a.packed + n / 16 * a.s.tile_bytes;
     const int c = k / kW4Chunk, lane = k % kW4Chunk / 32 * 16 + (int)(n % 16);
-    const uint32_t codes = *reinterpret_cast<const uint32_t *>(tile + w4_code_at(c, lane) + k % 32 / 2);
-    *reinterpret_cast<u32x4_any *>(a.w + n * a.row_stride + k) = kv4_dequantise(codes, tile[w4_scale_at(a.s.chunks, c, lane)]);
+    const uint32_t codes = *reinterpret_cast<const uint32_t *>(tile + c * kW4Codes + lane * 16 + k % 32 / 2);
+    *reinterpret_cast<u32x4_any *>(a.w + n * a.row_stride + k) = kv4_dequantise(codes, w4_scale(tile, a.s.chunks, c, lane));
 }
+
+constexpr int kCus = 256;
 
 struct LinearArgs {
     W4Shape s;
@@ -62,71 +64,26 @@ struct LinearArgs {
     int64_t tokens;
 };
 
-// A workgroup computes RT tiles of outputs for C times 16 tokens.  Its waves take
-// the chunks in turn, each with sums of its own, and join them through LDS.  U:
-// chunks that a wave has on their way at once.
-template <int RT, int C, int U>
-__global__ __launch_bounds__(512) void k_w4_linear(LinearArgs a) {
-    extern __shared__ f32x4 part[];  // [waves][min(RT C, 4)][64]
-    const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
-    const int tile0 = blockIdx.x * RT;
-    const int64_t token0 = (int64_t)blockIdx.y * (16 * C);
-    const uint8_t *tile[RT];
-    const uint16_t *row[C];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) tile[t] = a.packed + min(tile0 + t, a.s.tiles - 1) * a.s.tile_bytes;
-    // a column past the tokens is not stored; it takes the last token's row
-#pragma unroll
-    for (int c = 0; c < C; ++c) row[c] = a.x.p + min(token0 + c * 16 + r, a.tokens - 1) * a.x.ts;
-    f32x4 acc[RT][C];
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[t][c] = f32x4{0, 0, 0, 0};
+constexpr int kJoin = 8;  // tiles of sums in LDS at once
 
-    const auto step = [&](int first, auto count) {
-        constexpr int N = decltype(count)::value;
-        u32x4 codes[N][RT], x[N][C][4];
-        uint32_t byte[N][RT];
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const int c = first + u * waves;
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                codes[u][t] = *reinterpret_cast<const u32x4 *>(tile[t] + w4_code_at(c, lane));
-                byte[u][t] = tile[t][w4_scale_at(a.s.chunks, c, lane)];
-            }
-#pragma unroll
-            for (int i = 0; i < C; ++i) load_inputs(x[u][i], row[i], c * kW4Chunk + q * 32, a.s.n_in);
-        }
-#pragma unroll
-        for (int u = 0; u < N; ++u)
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const bf16x8 w = w4_operand(codes[u][t], kv4_scale(byte[u][t]), s);
-#pragma unroll
-                    for (int i = 0; i < C; ++i) acc[t][i] = w4_product(w, x[u][i][s], acc[t][i]);
-                }
-    };
-    int c = wave;
-    for (; c + (U - 1) * waves < a.s.chunks; c += U * waves) step(c, std::integral_constant<int, U>());
-    for (; c < a.s.chunks; c += waves) step(c, std::integral_constant<int, 1>());
-
-    // the waves' sums, some tiles of the output at a time
-    constexpr int kTogether = RT * C < 4 ? RT * C : 4;
+// The waves' sums of RT tiles of outputs for C times 16 tokens, joined through LDS
+// some tiles at a time, and stored.
+template <int RT, int C>
+__device__ __forceinline__ void join_waves(const LinearArgs &a, const f32x4 (&acc)[RT][C], f32x4 *part, int tile0, int64_t token0) {
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
+    constexpr int kTogether = RT * C < kJoin ? RT * C : kJoin;
 #pragma unroll
     for (int first = 0; first < RT * C; first += kTogether) {
-        if (first) __syncthreads();
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kTogether; ++i) part[(wave * kTogether + i) * 64 + lane] = acc[(first + i) / C][(first + i) % C];
+        for (int i = 0; i < kTogether; ++i)
+            if (first + i < RT * C) part[(wave * kTogether + i) * 64 + lane] = acc[(first + i) / C][(first + i) % C];
         __syncthreads();
         for (int item = threadIdx.x; item < kTogether * 64; item += blockDim.x) {
             f32x4 v = part[item];
             for (int w = 1; w < waves; ++w) v += part[w * kTogether * 64 + item];
             const int i = first + item / 64, at = item % 64;
+            if (i >= RT * C) break;
             const int64_t n = (int64_t)(tile0 + i / C) * 16 + at / 16 * 4, token = token0 + i % C * 16 + at % 16;
             if (token >= a.tokens) continue;
             uint16_t *to = const_cast<uint16_t *>(a.out.p) + token * a.out.ts + n;
@@ -143,11 +100,148 @@ __global__ __launch_bounds__(512) void k_w4_linear(LinearArgs a) {
     }
 }
 
+// A workgroup computes RT tiles of outputs for C times 16 tokens.  Its waves take
+// the chunks in turn, each with sums of its own, and join them through LDS.  U:
+// chunks that a wave has on their way at once.
+template <int RT, int C, int U>
+__global__ __launch_bounds__(512) void k_w4_linear(LinearArgs a) {
+    extern __shared__ f32x4 part[];  // [waves][min(RT C, kJoin)][64], and before that a stage of each wave
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
+    const int tile0 = blockIdx.x * RT;
+    const int64_t token0 = (int64_t)blockIdx.y * (16 * C);
+    const uint8_t *tile[RT];
+    const uint16_t *row[C];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) tile[t] = a.packed + min(tile0 + t, a.s.tiles - 1) * a.s.tile_bytes;
+    // a column past the tokens is not stored; it takes the last token's row
+#pragma unroll
+    for (int c = 0; c < C; ++c) row[c] = a.x.p + min(token0 + c * 16 + lane / 4, a.tokens - 1) * a.x.ts + lane % 4 * 8;
+    const Stage stage(reinterpret_cast<u32x4 *>(part) + wave * kStage, lane);
+    f32x4 acc[RT][C];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[t][c] = f32x4{0, 0, 0, 0};
+
+    // U chunks are on their way while U others are worked on
+    struct {
+        u32x4 codes[U][RT], x[U][C][4];
+        uint32_t byte[U][RT];
+    } buf[2];
+    const auto load = [&](int b, int chunk) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = min(chunk + u * waves, a.s.chunks - 1);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                buf[b].codes[u][t] = w4_codes(tile[t], c, lane);
+                buf[b].byte[u][t] = w4_scale(tile[t], a.s.chunks, c, lane);
+            }
+#pragma unroll
+            for (int i = 0; i < C; ++i) load_inputs(buf[b].x[u][i], row[i], c, a.s.n_in);
+        }
+    };
+    const auto work = [&](int b, int chunk) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (chunk + u * waves >= a.s.chunks) break;
+#pragma unroll
+            for (int i = 0; i < C; ++i) stage.turn(buf[b].x[u][i], chunk + u * waves, a.s.n_in);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const bf16x8 w = w4_operand(buf[b].codes[u][t], kv4_scale(buf[b].byte[u][t]), s);
+#pragma unroll
+                    for (int i = 0; i < C; ++i) acc[t][i] = w4_product(w, buf[b].x[u][i][s], acc[t][i]);
+                }
+        }
+    };
+    const int step = U * waves;
+    if (wave < a.s.chunks) load(0, wave);
+    for (int c = wave; c < a.s.chunks; c += 2 * step) {
+        if (c + step < a.s.chunks) load(1, c + step);
+        work(0, c);
+        if (c + step >= a.s.chunks) break;
+        if (c + 2 * step < a.s.chunks) load(0, c + 2 * step);
+        work(1, c + step);
+    }
+    join_waves<RT, C>(a, acc, part, tile0, token0);
+}
+
+// More than 16 tokens: C times 16 of them.  A chunk's weights are turned into
+// bf16 once, for all columns, and the inputs of 16 columns are replaced by the next
+// chunk's as soon as they have been used.  Codes are two chunks ahead, since they
+// come from further away, and are asked for after the inputs: loads are waited for
+// in their order, and inputs that stood behind codes waited for those.
+template <int RT, int C>
+__global__ __launch_bounds__(512) void k_w4_linear_wide(LinearArgs a) {
+    extern __shared__ f32x4 part[];  // [waves][min(RT C, kJoin)][64], and before that a stage of each wave
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
+    const int tile0 = blockIdx.x * RT;
+    const int64_t token0 = (int64_t)blockIdx.y * (16 * C);
+    const uint8_t *tile[RT];
+    const uint16_t *row[C];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) tile[t] = a.packed + min(tile0 + t, a.s.tiles - 1) * a.s.tile_bytes;
+    // a column past the tokens is not stored; it takes the last token's row
+#pragma unroll
+    for (int c = 0; c < C; ++c) row[c] = a.x.p + min(token0 + c * 16 + lane / 4, a.tokens - 1) * a.x.ts + lane % 4 * 8;
+    const Stage stage(reinterpret_cast<u32x4 *>(part) + wave * kStage, lane);
+    f32x4 acc[RT][C];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[t][c] = f32x4{0, 0, 0, 0};
+    u32x4 codes[2][RT], x[C][4];
+    uint32_t byte[2][RT];
+    const auto load_codes = [&](int b, int c) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            codes[b][t] = w4_codes(tile[t], c, lane);
+            byte[b][t] = w4_scale(tile[t], a.s.chunks, c, lane);
+        }
+    };
+    const int last = a.s.chunks - 1;
+    if (wave <= last) {
+        load_codes(0, wave);
+#pragma unroll
+        for (int i = 0; i < C; ++i) load_inputs(x[i], row[i], wave, a.s.n_in);
+        load_codes(1, min(wave + waves, last));
+    }
+    for (int first = wave; first <= last; first += 2 * waves) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int c = first + b * waves, next = min(c + waves, last);  // past the end: again what is there
+            if (c > last) break;
+            bf16x8 w[RT][4];
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) w[t][s] = w4_operand(codes[b][t], kv4_scale(byte[b][t]), s);
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                stage.turn(x[i], c, a.s.n_in);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) acc[t][i] = w4_product(w[t][s], x[i][s], acc[t][i]);
+                load_inputs(x[i], row[i], next, a.s.n_in);
+            }
+            load_codes(b, min(c + 2 * waves, last));
+        }
+    }
+    join_waves<RT, C>(a, acc, part, tile0, token0);
+}
+
 template <int RT>
 const void *pick_linear(int columns) {
-    return columns == 1   ? reinterpret_cast<const void *>(&k_w4_linear<RT, 1, RT == 4 ? 2 : 4>)
-           : columns == 2 ? reinterpret_cast<const void *>(&k_w4_linear<RT, 2, 2>)
-                          : reinterpret_cast<const void *>(&k_w4_linear<RT, 4, 1>);
+    return columns == 1   ? reinterpret_cast<const void *>(&k_w4_linear<RT, 1, RT <= 2 ? 2 : 1>)
+           : columns == 2 ? reinterpret_cast<const void *>(&k_w4_linear_wide<RT, 2>)
+           : columns == 3 ? reinterpret_cast<const void *>(&k_w4_linear_wide<RT, 3>)
+                          : reinterpret_cast<const void *>(&k_w4_linear_wide<RT, 4>);
 }
 
 RowsArg matrix(const void *p, int64_t stride, int64_t rows, int columns) {
@@ -200,13 +294,22 @@ int ar_w4_linear(ar_rows x, const void *packed, ar_rows out, int64_t tokens, int
     if (ro.overlaps(rx) || overlap(ro.span(), Span{addr(packed), (uintptr_t)a.s.bytes()})) return AR_EALIAS;
     a.packed = static_cast<const uint8_t *>(packed);
     a.x = rows(rx), a.out = rows(ro), a.tokens = tokens;
-    const int columns = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
+    const int columns = tokens <= 16 ? 1 : tokens <= 32 ? 2 : tokens <= 48 ? 3 : 4;
     const int64_t groups = (tokens + 16 * columns - 1) / (16 * columns);
-    const int tiles = a.s.tiles * groups >= 2048 ? 4 : a.s.tiles * groups >= 1024 ? 2 : 1;
-    const int waves = columns == 4 && tiles == 4 ? 4 : 8;
-    const unsigned lds = waves * (columns * tiles < 4 ? columns * tiles : 4) * 1024;
+    // The time of the compute unit that has most to do: for each chunk its
+    // tiles' codes, and the inputs, which cost as much as two tiles for every 16
+    // tokens however many tiles share them.
+    int tiles = 1;
+    int64_t least = 0;
+    for (int n = 1; n <= 4; ++n) {
+        const int64_t time = ((a.s.tiles + n - 1) / n * groups + kCus - 1) / kCus * (n + 2 * columns);
+        if (n == 1 || time < least) least = time, tiles = n;
+    }
+    const int waves = tiles == 4 ? 4 : 8;
+    const int stage = kStage * 16, sums = 1024 * (columns * tiles < kJoin ? columns * tiles : kJoin);
+    const unsigned lds = waves * (stage > sums ? stage : sums);
     void *args[] = {&a};
-    const void *fn = tiles == 4 ? pick_linear<4>(columns) : tiles == 2 ? pick_linear<2>(columns) : pick_linear<1>(columns);
+    const void *fn = tiles == 4 ? pick_linear<4>(columns) : tiles == 3 ? pick_linear<3>(columns) : tiles == 2 ? pick_linear<2>(columns) : pick_linear<1>(columns);
     return hipLaunchKernel(fn, dim3((a.s.tiles + tiles - 1) / tiles, (unsigned)groups), dim3(64 * waves), args, lds,
                            static_cast<hipStream_t>(stream)) == hipSuccess
                ? AR_OK
