@@ -22,7 +22,8 @@ namespace {
 
 constexpr int kMaxDim = 1 << 14;
 constexpr int kMaxThreads = 1024;
-// Above this many bytes, rows are read and written past the caches.
+// Above this many bytes, rows are read and written past the caches: 8191 tokens of
+// 7168 take 87.8 us with it, 105 without.
 constexpr int64_t kStreamBytes = (int64_t)128 << 20;
 
 struct BlockArgs {
@@ -31,6 +32,7 @@ struct BlockArgs {
     Rows dx, dy, dgate;      // backwards only
     const uint16_t *post, *pre;
     float *slots;            // backwards: sums over a workgroup's tokens, 3 dim floats each
+    float *roots;            // backwards, beyond kSumDim: a token's r1, r2 and r2 mean(q n2)
     int64_t part_stride, tokens;
     int dim;
     int shared_gate;         // backwards: all tokens have one gate
@@ -87,11 +89,11 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm(BlockArgs a) {
         x[i] = g[i] = w1[i] = w2[i] = u32x4{0, 0, 0, 0};
         if (n >= 8) {
 #pragma unroll
-            for (int p = 0; p < P; ++p) y[i][p] = load_vec8<NT>(a.part[p] + token * a.part_stride + at[i]);
-            x[i] = load_vec8<NT>(a.x.p + token * a.x.ts + at[i]);
-            if (a.gate.p) g[i] = load_vec8<false>(a.gate.p + token * a.gate.ts + at[i]);
-            if (a.post) w1[i] = load_vec8<false>(a.post + at[i]);
-            if (a.pre) w2[i] = load_vec8<false>(a.pre + at[i]);
+            for (int p = 0; p < P; ++p) y[i][p] = load_vec8<NT>(further(a.part[p] + token * a.part_stride, 2u * at[i]));
+            x[i] = load_vec8<NT>(further(a.x.p + token * a.x.ts, 2u * at[i]));
+            if (a.gate.p) g[i] = load_vec8<false>(further(a.gate.p + token * a.gate.ts, 2u * at[i]));
+            if (a.post) w1[i] = load_vec8<false>(further(a.post, 2u * at[i]));
+            if (a.pre) w2[i] = load_vec8<false>(further(a.pre, 2u * at[i]));
         } else if (n > 0) {
 #pragma unroll
             for (int p = 0; p < P; ++p) y[i][p] = load_few(a.part[p] + token * a.part_stride + at[i], n);
@@ -141,7 +143,7 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm(BlockArgs a) {
             f[i][e] = a.scale * t[e] + (a.gate.p ? f[i][e] * w[e] : f[i][e]);
             s[0] += f[i][e] * f[i][e];
         }
-        store_vec8<NT>(const_cast<uint16_t *>(a.h.p) + token * a.h.ts + at[i], f[i], a.dim - at[i]);
+        store_vec8<NT>(further(const_cast<uint16_t *>(a.h.p) + token * a.h.ts, 2u * at[i]), f[i], a.dim - at[i]);
     }
     if (!a.pre) return;
     block_sum(s, part2);
@@ -152,169 +154,262 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm(BlockArgs a) {
         widen(w2[i], w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[i][e] = f[i][e] * r * w[e];
-        store_vec8<NT>(const_cast<uint16_t *>(a.z.p) + token * a.z.ts + at[i], f[i], a.dim - at[i]);
+        store_vec8<NT>(further(const_cast<uint16_t *>(a.z.p) + token * a.z.ts, 2u * at[i]), f[i], a.dim - at[i]);
     }
 }
 
-// What a lane holds of one token's rows backwards.
-template <bool NT>
-struct GradRow {
-    u32x4 x, y, dh, dz, g;
-    __device__ __forceinline__ void load(const BlockArgs &a, int64_t token, int at) {
-        const int n = a.dim - at;
-        x = y = dh = dz = g = u32x4{0, 0, 0, 0};
-        if (n >= 8) {
-            y = load_vec8<NT>(a.part[0] + token * a.part_stride + at);
-            x = load_vec8<NT>(a.x.p + token * a.x.ts + at);
-            if (a.h.p) dh = load_vec8<NT>(a.h.p + token * a.h.ts + at);
-            if (a.pre) dz = load_vec8<NT>(a.z.p + token * a.z.ts + at);
-            if (a.gate.p) g = load_vec8<false>(a.gate.p + token * a.gate.ts + at);
-        } else if (n > 0) {
-            y = load_few(a.part[0] + token * a.part_stride + at, n);
-            x = load_few(a.x.p + token * a.x.ts + at, n);
-            if (a.h.p) dh = load_few(a.h.p + token * a.h.ts + at, n);
-            if (a.pre) dz = load_few(a.z.p + token * a.z.ts + at, n);
-            if (a.gate.p) g = load_few(a.gate.p + token * a.gate.ts + at, n);
+// Where a lane's eight channels lie backwards.  Past the row's last eight it takes
+// those, and of them as its own what no lane before it has: no load stands behind a
+// branch (with loads of single channels behind branches the kernels' registers ran
+// over).  Rows shorter than eight channels are one lane's, channel by channel.
+template <bool SHORT>
+struct Eight {
+    int at, own;  // the first channel, and of the eight the first own one
+    u32x4 mask;   // of the own ones
+
+    Eight() = default;
+    __device__ __forceinline__ Eight(int first, int dim) {
+        at = SHORT ? first : min(first, dim - 8);
+        own = SHORT ? 0 : min(first - at, 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mask[i] = (2 * i >= own ? 0xFFFFu : 0) | (2 * i + 1 >= own ? 0xFFFF0000u : 0);
+    }
+    template <bool NT>
+    __device__ __forceinline__ u32x4 load(const uint16_t *row, int dim) const {
+        return SHORT ? load_few(row + at, dim - at) : load_vec8<NT>(further(row, 2u * at));
+    }
+    template <bool NT>
+    __device__ __forceinline__ void store(uint16_t *row, const float (&f)[8], int dim) const {
+        if (!SHORT && own == 0) {
+            store_vec8<NT>(further(row, 2u * at), f, 8);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c >= own && at + c < dim) row[at + c] = (uint16_t)bf16_pair(f[c], 0.0f);
         }
     }
 };
 
-// Backwards.  A workgroup takes tokens in turn, and each lane keeps its
-// channels' sums over them; a second launch adds the workgroups' up, in a fixed
-// order.
-template <int V, bool NT>
-__global__ __launch_bounds__(kMaxThreads) void k_block_norm_grad(BlockArgs a) {
+// What a lane holds of one token's rows backwards.  What is not there is zeros, or
+// ones for a gate, so that nothing asks for it again.
+constexpr uint32_t kOnes = 0x3F803F80u;
+
+template <bool NT, bool SHORT>
+struct GradRow {
+    u32x4 x, y, dh, dz, g;
+    __device__ __forceinline__ void load(const BlockArgs &a, int64_t token, const Eight<SHORT> &at) {
+        const u32x4 none = {0, 0, 0, 0}, ones = {kOnes, kOnes, kOnes, kOnes};
+        y = at.template load<NT>(a.part[0] + token * a.part_stride, a.dim);
+        x = at.template load<NT>(a.x.p + token * a.x.ts, a.dim);
+        dh = a.h.p ? at.template load<NT>(a.h.p + token * a.h.ts, a.dim) : none;
+        dz = a.pre ? at.template load<NT>(a.z.p + token * a.z.ts, a.dim) : none;
+        g = a.gate.p ? at.template load<false>(a.gate.p + token * a.gate.ts, a.dim) : ones;
+    }
+    // Zeros for channels that are another lane's: they add nothing to a sum.
+    __device__ __forceinline__ GradRow own(const Eight<SHORT> &at, bool all) const {
+        if (SHORT || all) return *this;
+        return GradRow{x & at.mask, y & at.mask, dh & at.mask, dz & at.mask, g};
+    }
+};
+
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ void store_floats(float *to, const float (&f)[8]) {
+    f32x4_any *v = reinterpret_cast<f32x4_any *>(to);
+    v[0] = f32x4_any{f[0], f[1], f[2], f[3]};
+    v[1] = f32x4_any{f[4], f[5], f[6], f[7]};
+}
+
+// A lane's sums into a slot.
+template <bool SHORT>
+__device__ __forceinline__ void store_sums(const BlockArgs &a, int64_t slot, const Eight<SHORT> &at, const float (&sg)[8], const float (&s1)[8],
+                                           const float (&s2)[8]) {
+    float *to = a.slots + slot * 3 * a.dim + at.at;
+    if (!SHORT && at.own == 0) {
+        if (a.shared_gate) store_floats(to, sg);
+        if (a.post) store_floats(to + a.dim, s1);
+        if (a.pre) store_floats(to + 2 * a.dim, s2);
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        if (c >= at.own && at.at + c < a.dim) {
+            if (a.shared_gate) to[c] = sg[c];
+            if (a.post) to[a.dim + c] = s1[c];
+            if (a.pre) to[2 * a.dim + c] = s2[c];
+        }
+}
+
+// Backwards.  Without a norm after the block its weight and root are 1 and what its
+// mean takes off is 0; without one before the next block the root is 0.
+//
+// SUMS: a workgroup takes tokens in turn, the next one's rows on their way while it
+// works on one, and each lane keeps its channels' sums over them; a second launch
+// adds the workgroups' up.  For longer rows there are not registers enough for the
+// sums: a workgroup to a token leaves its roots, and k_block_norm_columns makes the
+// sums from the rows again.
+// T: lanes, at most.
+template <int V, int T, bool NT, bool SUMS, bool SHORT>
+__global__ __launch_bounds__(T) void k_block_norm_grad(BlockArgs a) {
     __shared__ float part1[1][kMaxThreads / 64], part2[2][kMaxThreads / 64], part3[1][kMaxThreads / 64];
     const float by = 1.0f / a.dim;
-    float sg[V][8] = {}, s1[V][8] = {}, s2[V][8] = {};
+    const bool all = a.dim == V * 8 * (int)blockDim.x;  // every lane has eight of its own
+    constexpr int kSums = SUMS ? V : 1;
+    float sg[kSums][8] = {}, s1[kSums][8] = {}, s2[kSums][8] = {};
     u32x4 w1[V], w2[V];
-    int at[V];
+    Eight<SHORT> at[V];
+    // Sixteen channels to a lane leave no room for rows in binary32 from one sum to
+    // the next, and 1024 lanes (128 registers each) none for the weights, which the
+    // caches hold.
+    constexpr bool kLean = V > 1, kHeld = T < 1024;
+    const auto weights = [&](int i) {
+        w1[i] = a.post ? at[i].template load<false>(a.post, a.dim) : u32x4{kOnes, kOnes, kOnes, kOnes};
+        w2[i] = a.pre ? at[i].template load<false>(a.pre, a.dim) : u32x4{0, 0, 0, 0};
+    };
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        at[i] = (int)(threadIdx.x + i * blockDim.x) * 8;
-        const int n = a.dim - at[i];
-        w1[i] = w2[i] = u32x4{0, 0, 0, 0};
-        if (n > 0) {
-            if (a.post) w1[i] = n >= 8 ? load_vec8<false>(a.post + at[i]) : load_few(a.post + at[i], n);
-            if (a.pre) w2[i] = n >= 8 ? load_vec8<false>(a.pre + at[i]) : load_few(a.pre + at[i], n);
-        }
+        at[i] = Eight<SHORT>((threadIdx.x + i * blockDim.x) * 8, a.dim);
+        if (kHeld) weights(i);
     }
-    // One set of rows to a lane: the next token's are on their way while this
-    // one's are worked on.  They stay packed until they are used.
-    constexpr bool kAhead = V == 1;
-    GradRow<NT> next[V];
+    constexpr bool kAhead = SUMS;
+    GradRow<NT, SHORT> next[V];
     if (kAhead) {
 #pragma unroll
         for (int i = 0; i < V; ++i) next[i].load(a, blockIdx.x, at[i]);
     }
     for (int64_t token = blockIdx.x; token < a.tokens; token += gridDim.x) {
-        GradRow<NT> row[V];
+        GradRow<NT, SHORT> row[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (kAhead) row[i] = next[i];
-            else row[i].load(a, token, at[i]);
+            if (!kAhead) next[i].load(a, token, at[i]);
+            row[i] = next[i].own(at[i], all);
+            if (!kHeld) weights(i);
         }
         if (kAhead && token + gridDim.x < a.tokens) {
 #pragma unroll
             for (int i = 0; i < V; ++i) next[i].load(a, token + gridDim.x, at[i]);
         }
-        float y[V][8], h[V][8], e[V][8];
         float r1 = 1.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) widen(row[i].y, y[i]);
         if (a.post) {
             float s[1] = {0};
 #pragma unroll
             for (int i = 0; i < V; ++i)
 #pragma unroll
-                for (int c = 0; c < 8; ++c) s[0] += y[i][c] * y[i][c];
+                for (int c = 0; c < 8; ++c) s[0] += at8(row[i].y, c) * at8(row[i].y, c);
             block_sum(s, part1);
             r1 = rsqrtf(s[0] * by + a.eps);
         }
-        // y becomes n1 (y itself without a norm after the block)
+        float h[V][8];
         float s[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float w[8], g[8], q[8];
-            widen(w1[i], w);
-            widen(row[i].g, g);
-            widen(row[i].x, h[i]);
-            widen(row[i].dz, q);
+            const u32x4 y = kLean ? again(row[i].y) : row[i].y, u1 = kLean ? again(w1[i]) : w1[i], u2 = kLean ? again(w2[i]) : w2[i];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                y[i][c] *= r1;
-                const float u = a.post ? y[i][c] * w[c] : y[i][c];
-                h[i][c] = a.scale * h[i][c] + (a.gate.p ? g[c] * u : u);
-            }
-            widen(w2[i], w);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
+                h[i][c] = a.scale * at8(row[i].x, c) + at8(row[i].g, c) * (at8(y, c) * r1 * at8(u1, c));
                 s[0] += h[i][c] * h[i][c];
-                s[1] += q[c] * w[c] * h[i][c];
+                s[1] += at8(row[i].dz, c) * at8(u2, c) * h[i][c];
             }
-            widen(row[i].dh, e[i]);
         }
+        float r2 = 0.0f, along2 = 0.0f;
         if (a.pre) {
             block_sum(s, part2);
-            const float r2 = rsqrtf(s[0] * by + a.eps), along = s[1] * by * r2;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float w[8], q[8];
-                widen(w2[i], w);
-                widen(row[i].dz, q);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float n2 = h[i][c] * r2;
-                    s2[i][c] += q[c] * n2;
-                    e[i][c] += r2 * (q[c] * w[c] - n2 * along);
-                }
-            }
+            r2 = rsqrtf(s[0] * by + a.eps);
+            along2 = s[1] * by * r2;
         }
         float d[1] = {0};
+        float(&e)[V][8] = h;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float w[8], g[8], t[8];
-            widen(w1[i], w);
-            widen(row[i].g, g);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) t[c] = a.scale * e[i][c];
-            store_vec8<NT>(const_cast<uint16_t *>(a.dx.p) + token * a.dx.ts + at[i], t, a.dim - at[i]);
+            float t[8];
+            const u32x4 z = kLean ? again(row[i].dz) : row[i].dz, u2 = kLean ? again(w2[i]) : w2[i];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                t[c] = e[i][c] * (a.post ? y[i][c] * w[c] : y[i][c]);
-                sg[i][c] += t[c];
-                if (a.gate.p) e[i][c] *= g[c];
-                s1[i][c] += e[i][c] * y[i][c];
-                if (a.post) e[i][c] *= w[c];
-                d[0] += e[i][c] * y[i][c];
+                const float n2 = h[i][c] * r2;
+                if (SUMS) s2[i % kSums][c] += at8(z, c) * n2;
+                e[i][c] = at8(row[i].dh, c) + r2 * (at8(z, c) * at8(u2, c) - n2 * along2);
+                t[c] = a.scale * e[i][c];
             }
-            if (a.dgate.p) store_vec8<NT>(const_cast<uint16_t *>(a.dgate.p) + token * a.dgate.ts + at[i], t, a.dim - at[i]);
+            at[i].template store<NT>(const_cast<uint16_t *>(a.dx.p) + token * a.dx.ts, t, a.dim);
+            const u32x4 y = kLean ? again(row[i].y) : row[i].y, g = kLean ? again(row[i].g) : row[i].g, u1 = kLean ? again(w1[i]) : w1[i];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) t[c] = e[i][c] * (at8(y, c) * r1 * at8(u1, c));
+            if (a.dgate.p) at[i].template store<NT>(const_cast<uint16_t *>(a.dgate.p) + token * a.dgate.ts, t, a.dim);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                if (SUMS) sg[i % kSums][c] += t[c];
+                e[i][c] *= at8(g, c);
+                if (SUMS) s1[i % kSums][c] += e[i][c] * (at8(y, c) * r1);
+                e[i][c] *= at8(u1, c);
+                d[0] += e[i][c] * at8(y, c);
+            }
         }
+        float along1 = 0.0f;
         if (a.post) {
             block_sum(d, part3);
-            const float along = d[0] * by;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) e[i][c] = r1 * (e[i][c] - y[i][c] * along);
+            along1 = d[0] * by * r1 * r1;
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            store_vec8<NT>(const_cast<uint16_t *>(a.dy.p) + token * a.dy.ts + at[i], e[i], a.dim - at[i]);
+        for (int i = 0; i < V; ++i) {
+            const u32x4 y = kLean ? again(row[i].y) : row[i].y;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) e[i][c] = r1 * (e[i][c] - at8(y, c) * along1);
+            at[i].template store<NT>(const_cast<uint16_t *>(a.dy.p) + token * a.dy.ts, e[i], a.dim);
+        }
+        if (!SUMS && threadIdx.x == 0) a.roots[token * 3] = r1, a.roots[token * 3 + 1] = r2, a.roots[token * 3 + 2] = along2;
         // Each sum's part is written again after the barrier of another one.
         // Where there is one sum alone, after this one.
         if (!a.post) __syncthreads();
     }
-    float *slot = a.slots + (int64_t)blockIdx.x * 3 * a.dim;
+    if (SUMS) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) store_sums(a, blockIdx.x, at[i], sg[i % kSums], s1[i % kSums], s2[i % kSums]);
+    }
+}
+
+// The sums over tokens from the rows and each token's roots: a wave has 512
+// channels, and the waves of a workgroup take its tokens in turn.
+template <bool NT>
+__global__ __launch_bounds__(kThreads) void k_block_norm_columns(BlockArgs a) {
+    constexpr int kWaves = kThreads / 64;
+    __shared__ float part[kWaves][3][512];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane8 = (blockIdx.x * 64 + lane) * 8;
+    const Eight<false> at(lane8, a.dim);
+    float sg[8] = {}, s1[8] = {}, s2[8] = {}, w1[8], w2[8];
+    widen(a.post ? at.load<false>(a.post, a.dim) : u32x4{kOnes, kOnes, kOnes, kOnes}, w1);
+    widen(a.pre ? at.load<false>(a.pre, a.dim) : u32x4{0, 0, 0, 0}, w2);
+    const int64_t begin = a.tokens * blockIdx.y / gridDim.y, end = a.tokens * (blockIdx.y + 1) / gridDim.y;
+    for (int64_t token = begin + wave; token < end; token += kWaves) {
+        GradRow<NT, false> row;
+        row.load(a, token, at);
+        row = row.own(at, a.dim % 512 == 0);
+        const float r1 = a.roots[token * 3], r2 = a.roots[token * 3 + 1], along2 = a.roots[token * 3 + 2];
+        float y[8], x[8], dh[8], q[8], g[8];
+        widen(row.y, y);
+        widen(row.x, x);
+        widen(row.dh, dh);
+        widen(row.dz, q);
+        widen(row.g, g);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if (at[i] + c < a.dim) {
-                if (a.shared_gate) slot[at[i] + c] = sg[i][c];
-                if (a.post) slot[a.dim + at[i] + c] = s1[i][c];
-                if (a.pre) slot[2 * a.dim + at[i] + c] = s2[i][c];
-            }
+        for (int c = 0; c < 8; ++c) {
+            const float n1 = y[c] * r1, u = n1 * w1[c], n2 = (a.scale * x[c] + g[c] * u) * r2;
+            const float e = dh[c] + r2 * (q[c] * w2[c] - n2 * along2);
+            sg[c] += e * u;
+            s1[c] += e * g[c] * n1;
+            s2[c] += q[c] * n2;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) part[wave][0][c * 64 + lane] = sg[c], part[wave][1][c * 64 + lane] = s1[c], part[wave][2][c * 64 + lane] = s2[c];
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        sg[c] = (part[0][0][c * 64 + lane] + part[1][0][c * 64 + lane]) + (part[2][0][c * 64 + lane] + part[3][0][c * 64 + lane]);
+        s1[c] = (part[0][1][c * 64 + lane] + part[1][1][c * 64 + lane]) + (part[2][1][c * 64 + lane] + part[3][1][c * 64 + lane]);
+        s2[c] = (part[0][2][c * 64 + lane] + part[1][2][c * 64 + lane]) + (part[2][2][c * 64 + lane] + part[3][2][c * 64 + lane]);
+    }
+    store_sums(a, blockIdx.y, at, sg, s1, s2);
 }
 
 struct SumArgs {
@@ -323,28 +418,33 @@ struct SumArgs {
     int dim, blocks;
 };
 
-// Adds the workgroups' sums up: 64 columns to a workgroup, its four waves taking
-// every fourth slot.
-__global__ __launch_bounds__(256) void k_block_norm_sums(SumArgs a) {
-    __shared__ float part[4][64];
-    const int per = (a.dim + 63) / 64, which = blockIdx.x / per;
-    const int c = blockIdx.x % per * 64 + threadIdx.x % 64, wave = threadIdx.x / 64;
+// Adds the workgroups' sums up: 64 columns to a workgroup, its 16 waves taking every
+// sixteenth slot.
+constexpr int kSumWaves = 16;
+
+__global__ __launch_bounds__(64 * kSumWaves) void k_block_norm_sums(SumArgs a) {
+    __shared__ float part[kSumWaves][64];
+    const int per = (a.dim + 63) / 64, which = blockIdx.x / per, lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int c = blockIdx.x % per * 64 + lane;
     float *out = a.out[which];
     if (!out) return;
     float t = 0;
     if (c < a.dim) {
         const float *p = a.slots + (int64_t)which * a.dim + c;
-        for (int s = wave; s < a.blocks; s += 4 * 16) {
+        for (int s = wave; s < a.blocks; s += kSumWaves * 16) {
             float v[16];  // all on their way at once
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = p[(int64_t)min(s + 4 * k, a.blocks - 1) * 3 * a.dim];
+            for (int k = 0; k < 16; ++k) v[k] = p[(int64_t)min(s + kSumWaves * k, a.blocks - 1) * 3 * a.dim];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) t += s + 4 * k < a.blocks ? v[k] : 0.0f;
+            for (int k = 0; k < 16; ++k) t += s + kSumWaves * k < a.blocks ? v[k] : 0.0f;
         }
     }
-    part[wave][threadIdx.x % 64] = t;
+    part[wave][lane] = t;
     __syncthreads();
-    if (wave == 0 && c < a.dim) out[c] = (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+    if (wave || c >= a.dim) return;
+#pragma unroll
+    for (int w = 1; w < kSumWaves; ++w) t += part[w][lane];
+    out[c] = t;
 }
 
 template <int P>
@@ -366,15 +466,27 @@ const void *pick(int P, bool wide, bool stream) {
     }
 }
 
-const void *pick_grad(bool wide, bool stream) {
-    return wide ? (stream ? reinterpret_cast<const void *>(&k_block_norm_grad<2, true>) : reinterpret_cast<const void *>(&k_block_norm_grad<2, false>))
-                : (stream ? reinterpret_cast<const void *>(&k_block_norm_grad<1, true>) : reinterpret_cast<const void *>(&k_block_norm_grad<1, false>));
+// Eight channels to a lane up to 6144, sixteen beyond that.  (8192 tokens of 5120 take
+// 99 us with eight and 110 with sixteen; 4096 of 7168, whose 896 lanes with eight
+// would have 128 registers each, 79 us with sixteen and 94 with eight.)
+constexpr int kSumDim = 8 * kMaxThreads;
+
+template <bool NT>
+const void *pick_grad(int dim) {
+    return dim < 8          ? reinterpret_cast<const void *>(&k_block_norm_grad<1, 64, false, true, true>)
+           : dim <= 6144    ? reinterpret_cast<const void *>(&k_block_norm_grad<1, 768, NT, true, false>)
+           : dim <= kSumDim ? reinterpret_cast<const void *>(&k_block_norm_grad<2, 512, NT, true, false>)
+                            : reinterpret_cast<const void *>(&k_block_norm_grad<2, 1024, NT, false, false>);
 }
 
-bool is_wide(int dim) { return dim > 8 * kMaxThreads; }
+// Sixteen channels to a lane: rows of more than 8192, and long ones that are
+// streamed, of up to four parts.  (8191 tokens of 7169: 117 us, 143 with eight; 4000 of
+// 5120 and four parts 51.3 and 52.4.  2400 of 5120 and eight parts 52.3, 49.0 with
+// eight; 8192 of 1024 16.2 and 14.8; 440 of 5120, not streamed, 5.8 and 5.3.)
+bool is_wide(int dim, int P, bool stream) { return dim > 8 * kMaxThreads || (stream && dim > 4096 && P <= 4); }
 
-unsigned threads_of(int dim) {
-    const int vecs = (dim + 7) / 8, lanes = is_wide(dim) ? (vecs + 1) / 2 : vecs;
+unsigned threads_of(int dim, bool wide) {
+    const int vecs = (dim + 7) / 8, lanes = wide ? (vecs + 1) / 2 : vecs;
     return (unsigned)round_up(lanes, 64);
 }
 
@@ -414,9 +526,34 @@ int check_output(const RowsArg &out, const Buffers &in, unsigned may_be) {
 
 bool half_aligned(const void *p) { return aligned_to(p, 2); }
 
-constexpr int kSlots = 256;  // workgroups backwards, at most: one a compute unit
+int lanes_of_grad(int dim) {
+    const int each = dim <= 6144 ? 8 : 16;
+    return (int)round_up((dim + each - 1) / each, 64);
+}
 
-int grad_blocks(int64_t tokens) { return (int)(tokens < 1 ? 1 : tokens < kSlots ? tokens : kSlots); }
+// Rows of sums that the workspace has room for.  Its size never falls as tokens or
+// channels grow: 2^20 channels of rows, or 256 rows, or one for each token.
+int64_t slot_rows(int64_t tokens, int dim) {
+    const int64_t rows = (1 << 20) / dim > 256 ? (1 << 20) / dim : 256;
+    return tokens < 1 ? 1 : tokens < rows ? tokens : rows;
+}
+
+int64_t slot_channels(int64_t tokens, int dim) {
+    const int64_t all = (tokens < 1 ? 1 : tokens) * dim, most = (int64_t)256 * dim > 1 << 20 ? (int64_t)256 * dim : 1 << 20;
+    return all < most ? all : most;
+}
+
+// Workgroups with sums of their own: one to each of 256 compute units, or for short
+// rows as many as leave eight waves to each and four tokens to a workgroup (4096
+// tokens of 1024 take 28.8 us with 256, 20.7 with 1024; 440 take 9.9 with 256, 11.4
+// with one each, whose sums take longer to join).
+int sum_slots(int64_t tokens, int dim) {
+    const int waves = lanes_of_grad(dim) / 64;
+    int64_t most = dim > kSumDim ? 32 : dim > 4096 ? 256 : waves <= 2 ? 1024 : 2048 / waves;
+    if (most > 256 && most > tokens / 4) most = tokens / 4 > 256 ? tokens / 4 : 256;
+    if (most > slot_rows(tokens, dim)) most = slot_rows(tokens, dim);
+    return (int)(tokens < 1 ? 1 : tokens < most ? tokens : most);
+}
 
 }  // namespace
 }  // namespace ar
@@ -462,12 +599,13 @@ int ar_block_norm(ar_ptrs parts, int64_t part_stride, int P, ar_rows x, const vo
     a.post = static_cast<const uint16_t *>(post_weight), a.pre = static_cast<const uint16_t *>(pre_weight);
     a.tokens = tokens, a.dim = dim, a.scale = residual_scale, a.eps = eps;
     const int64_t bytes = 2 * tokens * dim * (P + 3);
-    return launch(pick(P, is_wide(dim), bytes > kStreamBytes), (unsigned)tokens, threads_of(dim), a, stream);
+    const bool past = bytes > kStreamBytes, wide = is_wide(dim, P, past);
+    return launch(pick(P, wide, past), (unsigned)tokens, threads_of(dim, wide), a, stream);
 }
 
 int64_t ar_block_norm_bwd_workspace(int64_t tokens, int dim) {
     if (!valid_shape(tokens, dim)) return AR_EINVAL;
-    return round_up((int64_t)grad_blocks(tokens) * 3 * dim * 4, 16);
+    return round_up(slot_channels(tokens, dim) * 12, 16) + (dim > kSumDim ? round_up(tokens * 12, 16) : 0);
 }
 
 int ar_block_norm_bwd(ar_rows h_grad, ar_rows z_grad, ar_rows y, ar_rows x, const void *post_weight, ar_rows gate,
@@ -518,10 +656,11 @@ int ar_block_norm_bwd(ar_rows h_grad, ar_rows z_grad, ar_rows y, ar_rows x, cons
                            (gate_rows && overlap(apart[i], rdg.span()))))
             return AR_EALIAS;
     }
+    const int slots = sum_slots(tokens, dim);
     SumArgs sum = {static_cast<const float *>(workspace),
                    {static_cast<float *>(sums[0]), static_cast<float *>(sums[1]), static_cast<float *>(sums[2])},
                    dim,
-                   tokens ? grad_blocks(tokens) : 0};
+                   tokens ? slots : 0};
     if (tokens > 0) {
         BlockArgs a = {};
         a.part[0] = static_cast<const uint16_t *>(y.p), a.part_stride = ry.r.token_stride;
@@ -532,14 +671,23 @@ int ar_block_norm_bwd(ar_rows h_grad, ar_rows z_grad, ar_rows y, ar_rows x, cons
         if (gate_rows) a.dgate = rows(rdg);
         a.post = static_cast<const uint16_t *>(post_weight), a.pre = static_cast<const uint16_t *>(pre_weight);
         a.slots = static_cast<float *>(workspace);
+        a.roots = a.slots + (int64_t)slots * 3 * dim;
         a.shared_gate = shared;
         a.tokens = tokens, a.dim = dim, a.scale = residual_scale, a.eps = eps;
-        const int64_t bytes = 2 * tokens * dim * 6;
-        const int rc = launch(pick_grad(is_wide(dim), bytes > kStreamBytes), (unsigned)grad_blocks(tokens), threads_of(dim), a, stream);
+        const bool nt = 2 * tokens * dim * 6 > kStreamBytes, own = dim <= kSumDim;
+        // rows beyond kSumDim are read again by k_block_norm_columns: they stay in the caches
+        const int rc = launch(nt && own ? pick_grad<true>(dim) : pick_grad<false>(dim), (unsigned)(own ? slots : tokens < 512 ? tokens : 512),
+                              (unsigned)lanes_of_grad(dim), a, stream);
         if (rc != AR_OK) return rc;
+        if (!own && wanted) {
+            void *args[] = {&a};
+            if (hipLaunchKernel(reinterpret_cast<const void *>(&k_block_norm_columns<false>), dim3((dim + 511) / 512, slots), dim3(kThreads), args, 0,
+                                static_cast<hipStream_t>(stream)) != hipSuccess)
+                return AR_ELAUNCH;
+        }
     }
     if (!wanted) return AR_OK;
-    return launch(reinterpret_cast<const void *>(&k_block_norm_sums), (unsigned)(3 * ((dim + 63) / 64)), 256, sum, stream);
+    return launch(reinterpret_cast<const void *>(&k_block_norm_sums), (unsigned)(3 * ((dim + 63) / 64)), 64 * kSumWaves, sum, stream);
 }
 
 }  // extern "C"

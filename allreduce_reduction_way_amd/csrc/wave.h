@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device.h"
 
 namespace ar {
@@ -27,11 +29,13 @@ __device__ __forceinline__ float row16_sum(float v) {
     return dpp_add<0x121, 0xf>(v);
 }
 
-// Sum over the wave; every lane gets it.
+// Sum over the wave; every lane gets it, by the same pairs.
 __device__ __forceinline__ float wave_sum(float v) {
     v = row16_sum(v);
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -65,5 +69,23 @@ __device__ __forceinline__ void widen(u32x4 v, float (&f)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[2 * i] = lo_f32(v[i]), f[2 * i + 1] = hi_f32(v[i]);
 }
+
+// `bytes` on from an address that is the same in all lanes: scalar registers hold
+// that, and a lane its offset.
+template <typename T>
+__device__ __forceinline__ T *further(T *p, uint32_t bytes) {
+    typedef typename std::conditional<std::is_const<T>::value, const char, char>::type Byte;
+    return reinterpret_cast<T *>(reinterpret_cast<Byte *>(p) + bytes);
+}
+
+// The same value, which the compiler takes for another one: what was made of it
+// before is made again where it is used, and takes no registers until then.
+__device__ __forceinline__ u32x4 again(u32x4 v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Element c of eight.
+__device__ __forceinline__ float at8(u32x4 v, int c) { return c % 2 ? hi_f32(v[c / 2]) : lo_f32(v[c / 2]); }
 
 }  // namespace ar

@@ -218,3 +218,23 @@ def test_past_128_mib(T, D, P):
             sizes[k] += w[k][1].cpu()
     for got, k in ((dpost, "post"), (dpre, "pre")):
         close(got, (sums[k], sizes[k]), 2.0 ** -16, k)
+
+
+@pytest.mark.parametrize("T,D", [(4096, 7168), (1500, 6145), (1500, 6144), (3000, 8192), (4096, 1024), (5000, 256), (2000, 1025), (700, 2048), (2100, 2560),
+                                 (300, 9000), (1, 5), (40, 7)])
+def test_nothing_past_the_workspace_is_written(T, D):
+    """Each rule's number of workgroups with sums of their own, in a workspace of the size asked for."""
+    announce(f"block_norm_grad workspace {T} {D}")
+    g = torch.Generator(device=DEV).manual_seed(T + D)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV).bfloat16()  # noqa: E731
+    size, guard = ar.ar_block_norm_bwd_workspace(T, D), 32 << 20
+    ws = torch.full((size + guard,), 255, dtype=torch.uint8, device=DEV)
+    y, x, dh, dz, gate, post, pre = n(T, D), n(T, D), n(T, D), n(T, D), n(D), n(D), n(D)
+    dx, dy = torch.empty_like(x), torch.empty_like(x)
+    grads = [torch.empty(D, device=DEV) for _ in range(3)]
+    ar.ar_block_norm_bwd(dh, dz, y, x, dx, dy, ws[:size], post_weight=post, gate=gate, pre_weight=pre, gate_grad=grads[0], post_grad=grads[1],
+                         pre_grad=grads[2], eps=EPS)
+    assert bool((ws[size:] == 255).all())
+    want = R.block_norm_grad(dh, dz, y, x, post, gate, pre, 1.0, EPS)
+    for k, v in (("dx", dx), ("dy", dy), ("gate", grads[0]), ("post", grads[1]), ("pre", grads[2])):
+        close(v, tuple(w.cpu() for w in want[k]), 2.0 ** -17 if v.dim() > 1 else 2.0 ** -16, k)
