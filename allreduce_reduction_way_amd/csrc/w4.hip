@@ -170,6 +170,46 @@ __global__ __launch_bounds__(512) void k_w4_linear(LinearArgs a) {
     join_waves<RT, C>(a, acc, part, tile0, token0);
 }
 
+// Up to eight tokens and two tiles or more: the lanes that have a token load its
+// inputs as the steps take them, with no turn through LDS, and with no chunk ahead
+// there are twice as many waves.  (One token x 7168 x 7168 takes 8.4 us, 9.9 by
+// k_w4_linear; eight 9.0 and 10.2; sixteen would take 11.1, and 10.7 there; with one
+// tile to a workgroup 14336 x 4096 takes 13.8, and 12.0 there.)
+template <int RT>
+__global__ __launch_bounds__(512) void k_w4_linear_few(LinearArgs a) {
+    extern __shared__ f32x4 part[];  // [waves][RT][64]
+    const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
+    const int tile0 = blockIdx.x * RT;
+    const uint8_t *tile[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) tile[t] = a.packed + min(tile0 + t, a.s.tiles - 1) * a.s.tile_bytes;
+    const bool mine = r < a.tokens;
+    const uint16_t *row = a.x.p + (mine ? r : 0) * a.x.ts + q * 32;
+    f32x4 acc[RT][1];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t][0] = f32x4{0, 0, 0, 0};
+    for (int c = wave; c < a.s.chunks; c += waves) {
+        u32x4 codes[RT], x[4];
+        uint32_t byte[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            codes[t] = w4_codes(tile[t], c, lane);
+            byte[t] = w4_scale(tile[t], a.s.chunks, c, lane);
+        }
+        load_few_inputs(x, row + min(c * kW4Chunk, a.s.n_in - 32 - q * 32), 8, mine);  // past the row: inside it
+        if ((c + 1) * kW4Chunk > a.s.n_in && c * kW4Chunk + q * 32 >= a.s.n_in) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) x[s] = u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) acc[t][0] = w4_product(w4_operand(codes[t], kv4_scale(byte[t]), s), x[s], acc[t][0]);
+    }
+    join_waves<RT, 1>(a, acc, part, tile0, 0);
+}
+
 // More than 16 tokens: C times 16 of them.  A chunk's weights are turned into
 // bf16 once, for all columns, and the inputs of 16 columns are replaced by the next
 // chunk's as soon as they have been used.  Codes are two chunks ahead, since they
@@ -237,7 +277,8 @@ __global__ __launch_bounds__(512) void k_w4_linear_wide(LinearArgs a) {
 }
 
 template <int RT>
-const void *pick_linear(int columns) {
+const void *pick_linear(int columns, bool few) {
+    if (few && RT > 1) return reinterpret_cast<const void *>(&k_w4_linear_few<RT>);
     return columns == 1   ? reinterpret_cast<const void *>(&k_w4_linear<RT, 1, RT <= 2 ? 2 : 1>)
            : columns == 2 ? reinterpret_cast<const void *>(&k_w4_linear_wide<RT, 2>)
            : columns == 3 ? reinterpret_cast<const void *>(&k_w4_linear_wide<RT, 3>)
@@ -305,12 +346,17 @@ int ar_w4_linear(ar_rows x, const void *packed, ar_rows out, int64_t tokens, int
         const int64_t time = ((a.s.tiles + n - 1) / n * groups + kCus - 1) / kCus * (n + 2 * columns);
         if (n == 1 || time < least) least = time, tiles = n;
     }
-    const int waves = tiles == 4 ? 4 : 8;
+    const int64_t blocks = (a.s.tiles + tiles - 1) / tiles;
+    const bool few = tokens <= 8;
+    // Four waves where compute units get more than one workgroup of four tiles: 64
+    // tokens x 8192 x 28672 take 52.5 us, and 56.0 with eight; with one, eight (one
+    // token x 4096 x 14336: 8.4, and 10.5 with four).
+    const int waves = tiles == 4 && blocks * groups > kCus ? 4 : 8;
     const int stage = kStage * 16, sums = 1024 * (columns * tiles < kJoin ? columns * tiles : kJoin);
     const unsigned lds = waves * (stage > sums ? stage : sums);
     void *args[] = {&a};
-    const void *fn = tiles == 4 ? pick_linear<4>(columns) : tiles == 3 ? pick_linear<3>(columns) : tiles == 2 ? pick_linear<2>(columns) : pick_linear<1>(columns);
-    return hipLaunchKernel(fn, dim3((a.s.tiles + tiles - 1) / tiles, (unsigned)groups), dim3(64 * waves), args, lds,
+    const void *fn = tiles == 4 ? pick_linear<4>(columns, few) : tiles == 3 ? pick_linear<3>(columns, few) : tiles == 2 ? pick_linear<2>(columns, few) : pick_linear<1>(columns, false);
+    return hipLaunchKernel(fn, dim3((unsigned)blocks, (unsigned)groups), dim3(64 * waves), args, lds,
                            static_cast<hipStream_t>(stream)) == hipSuccess
                ? AR_OK
                : AR_ELAUNCH;
