@@ -22,7 +22,8 @@
 //   parts in 8 to 15.
 // k_experts_down: a workgroup has one expert, some tiles of its outputs, and its
 //   groups one or two at a time in LDS.  Each token's result is left in binary32.
-// k_experts_sum: a token's results by weight, in the order of its experts.
+// k_experts_sum: a token's results by weight, in the order of its experts.  Of a
+// single token k_experts_down_one makes the sum at once.
 #include "host.h"
 #include "rows.h"
 #include "w4.h"
@@ -404,6 +405,54 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(ExpertsArgs a)
     }
 }
 
+// A single token: a workgroup has a tile of outputs of all its experts, whose chunks
+// its waves take in turn, two on their way at once.
+__global__ __launch_bounds__(64 * kDownWaves) void k_experts_down_one(ExpertsArgs a) {
+    __shared__ f32x4 part[kDownWaves][4];
+    const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int chunks = a.down.chunks, items = a.top_k * chunks;
+    const uint8_t *tile = a.dn + blockIdx.x * a.down.tile_bytes;
+    f32x4 sum = {0, 0, 0, 0};
+    for (int first = wave; first < items; first += 2 * kDownWaves) {
+        u32x4 codes[2], x[2][4];
+        uint32_t byte[2];
+        float weight[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int item = min(first + u * kDownWaves, items - 1), slot = item / chunks, c = item - slot * chunks;
+            const int4 taken = a.taken[slot];
+            const int expert = __builtin_amdgcn_readfirstlane(taken.x), base = __builtin_amdgcn_readfirstlane(taken.y);
+            weight[u] = a.weight[a.group_pair[base * kColumns]];
+            codes[u] = w4_codes(tile + expert * a.down.bytes(), c, lane);
+            byte[u] = w4_scale(tile + expert * a.down.bytes(), chunks, c, lane);
+            load_few_inputs(x[u], a.act + ((int64_t)base * chunks + c) * 4 * 64 * 8 + lane * 8, 64 * 8, r % kColumns == 0);
+            if (c * kW4Chunk + q * 32 >= a.inner) {  // nothing was written there
+#pragma unroll
+                for (int s = 0; s < 4; ++s) x[u][s] = u32x4{0, 0, 0, 0};
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (first + u * kDownWaves >= items) break;
+            f32x4 d = {0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) d = w4_product(w4_operand(codes[u], kv4_scale(byte[u]), s), x[u][s], d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = dpp_add<0x128, 0xf>(d[i]);  // the two parts
+            sum += weight[u] * d;
+        }
+    }
+    if (r == 0) part[wave][q] = sum;
+    __syncthreads();
+    if (threadIdx.x >= 4) return;
+    f32x4 v = part[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kDownWaves; ++w) v += part[w][threadIdx.x];
+    typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+    uint16_t *to = const_cast<uint16_t *>(a.out.p) + blockIdx.x * 16 + threadIdx.x * 4;  // hidden is a multiple of 32
+    *reinterpret_cast<u32x2_any *>(to) = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+}
+
 // Four outputs of a token to a lane.
 __global__ __launch_bounds__(kThreads) void k_experts_sum(ExpertsArgs a) {
     const int n = (blockIdx.x * kThreads + threadIdx.x) * 4, token = blockIdx.y;
@@ -514,6 +563,11 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         rc = launch3(two_up ? reinterpret_cast<const void *>(&k_experts_up<2, 1>) : reinterpret_cast<const void *>(&k_experts_up<1, 2>),
                      dim3(two_up ? (half + 1) / 2 : half, slots), 64 * kUpWaves, 0, a, stream);
         if (rc != AR_OK) return rc;
+        if (a.tokens == 1) {
+            rc = launch3(reinterpret_cast<const void *>(&k_experts_down_one), dim3(a.down.tiles), 64 * kDownWaves, 0, a, stream);
+            if (rc != AR_OK) return rc;
+            continue;
+        }
         const int64_t tiles = (int64_t)slots * a.down.tiles;
         const int n = tiles >= 4 * 8192 ? 4 : tiles >= 2 * 4096 ? 2 : 1;
         const bool two = a.tokens > kColumns;
