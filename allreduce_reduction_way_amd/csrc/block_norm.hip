@@ -36,6 +36,7 @@ struct BlockArgs {
     int64_t part_stride, tokens;
     int dim;
     int shared_gate;         // backwards: all tokens have one gate
+    int roots_only;          // backwards, beyond kSumDim: nothing but the roots is written
     float scale, eps;
 };
 
@@ -317,6 +318,11 @@ __global__ __launch_bounds__(T) void k_block_norm_grad(BlockArgs a) {
             r2 = rsqrtf(s[0] * by + a.eps);
             along2 = s[1] * by * r2;
         }
+        if (!SUMS && threadIdx.x == 0) a.roots[token * 3] = r1, a.roots[token * 3 + 1] = r2, a.roots[token * 3 + 2] = along2;
+        if (!SUMS && a.roots_only) {
+            __syncthreads();
+            continue;
+        }
         float d[1] = {0};
         float(&e)[V][8] = h;
 #pragma unroll
@@ -356,7 +362,6 @@ __global__ __launch_bounds__(T) void k_block_norm_grad(BlockArgs a) {
             for (int c = 0; c < 8; ++c) e[i][c] = r1 * (e[i][c] - at8(y, c) * along1);
             at[i].template store<NT>(const_cast<uint16_t *>(a.dy.p) + token * a.dy.ts, e[i], a.dim);
         }
-        if (!SUMS && threadIdx.x == 0) a.roots[token * 3] = r1, a.roots[token * 3 + 1] = r2, a.roots[token * 3 + 2] = along2;
         // Each sum's part is written again after the barrier of another one.
         // Where there is one sum alone, after this one.
         if (!a.post) __syncthreads();
@@ -369,7 +374,6 @@ __global__ __launch_bounds__(T) void k_block_norm_grad(BlockArgs a) {
 
 // The sums over tokens from the rows and each token's roots: a wave has 512
 // channels, and the waves of a workgroup take its tokens in turn.
-template <bool NT>
 __global__ __launch_bounds__(kThreads) void k_block_norm_columns(BlockArgs a) {
     constexpr int kWaves = kThreads / 64;
     __shared__ float part[kWaves][3][512];
@@ -380,7 +384,7 @@ __global__ __launch_bounds__(kThreads) void k_block_norm_columns(BlockArgs a) {
     widen(a.pre ? at.load<false>(a.pre, a.dim) : u32x4{0, 0, 0, 0}, w2);
     const int64_t begin = a.tokens * blockIdx.y / gridDim.y, end = a.tokens * (blockIdx.y + 1) / gridDim.y;
     for (int64_t token = begin + wave; token < end; token += kWaves) {
-        GradRow<NT, false> row;
+        GradRow<false, false> row;
         row.load(a, token, at);
         row = row.own(at, a.dim % 512 == 0);
         const float r1 = a.roots[token * 3], r2 = a.roots[token * 3 + 1], along2 = a.roots[token * 3 + 2];
@@ -471,12 +475,18 @@ const void *pick(int P, bool wide, bool stream) {
 // would have 128 registers each, 79 us with sixteen and 94 with eight.)
 constexpr int kSumDim = 8 * kMaxThreads;
 
+// Rows beyond kSumDim are read again by k_block_norm_columns: they stay in the caches.
 template <bool NT>
-const void *pick_grad(int dim) {
-    return dim < 8          ? reinterpret_cast<const void *>(&k_block_norm_grad<1, 64, false, true, true>)
-           : dim <= 6144    ? reinterpret_cast<const void *>(&k_block_norm_grad<1, 768, NT, true, false>)
-           : dim <= kSumDim ? reinterpret_cast<const void *>(&k_block_norm_grad<2, 512, NT, true, false>)
-                            : reinterpret_cast<const void *>(&k_block_norm_grad<2, 1024, NT, false, false>);
+const void *pick_sums(int dim) {
+    return dim <= 6144 ? reinterpret_cast<const void *>(&k_block_norm_grad<1, 768, NT, true, false>)
+                       : reinterpret_cast<const void *>(&k_block_norm_grad<2, 512, NT, true, false>);
+}
+
+const void *pick_grad(int dim, bool stream) {
+    return dim < 8         ? reinterpret_cast<const void *>(&k_block_norm_grad<1, 64, false, true, true>)
+           : dim > kSumDim ? reinterpret_cast<const void *>(&k_block_norm_grad<2, 1024, false, false, false>)
+           : stream        ? pick_sums<true>(dim)
+                           : pick_sums<false>(dim);
 }
 
 // Sixteen channels to a lane: rows of more than 8192, and long ones that are
@@ -674,17 +684,30 @@ int ar_block_norm_bwd(ar_rows h_grad, ar_rows z_grad, ar_rows y, ar_rows x, cons
         a.roots = a.slots + (int64_t)slots * 3 * dim;
         a.shared_gate = shared;
         a.tokens = tokens, a.dim = dim, a.scale = residual_scale, a.eps = eps;
-        const bool nt = 2 * tokens * dim * 6 > kStreamBytes, own = dim <= kSumDim;
-        // rows beyond kSumDim are read again by k_block_norm_columns: they stay in the caches
-        const int rc = launch(nt && own ? pick_grad<true>(dim) : pick_grad<false>(dim), (unsigned)(own ? slots : tokens < 512 ? tokens : 512),
-                              (unsigned)lanes_of_grad(dim), a, stream);
-        if (rc != AR_OK) return rc;
-        if (!own && wanted) {
+        const bool own = dim <= kSumDim;
+        const unsigned blocks = own ? slots : tokens < 512 ? tokens : 512, lanes = lanes_of_grad(dim);
+        const void *fn = pick_grad(dim, 2 * tokens * dim * 6 > kStreamBytes);
+        const auto columns = [&] {
             void *args[] = {&a};
-            if (hipLaunchKernel(reinterpret_cast<const void *>(&k_block_norm_columns<false>), dim3((dim + 511) / 512, slots), dim3(kThreads), args, 0,
-                                static_cast<hipStream_t>(stream)) != hipSuccess)
-                return AR_ELAUNCH;
+            return hipLaunchKernel(reinterpret_cast<const void *>(&k_block_norm_columns), dim3((dim + 511) / 512, slots), dim3(kThreads), args, 0,
+                                   static_cast<hipStream_t>(stream)) == hipSuccess
+                       ? AR_OK
+                       : AR_ELAUNCH;
+        };
+        // k_block_norm_columns needs the rows as they came in: where dx or dy take
+        // one's place it goes before them, with roots from a pass of their own.
+        bool before = false;
+        for (int i = 0; !own && wanted && i < in.count; ++i) before = before || rdx.overlaps(in.rows[i]) || rdy.overlaps(in.rows[i]);
+        int rc = AR_OK;
+        if (before) {
+            a.roots_only = 1;
+            rc = launch(fn, blocks, lanes, a, stream);
+            a.roots_only = 0;
+            if (rc == AR_OK) rc = columns();
         }
+        if (rc == AR_OK) rc = launch(fn, blocks, lanes, a, stream);
+        if (rc == AR_OK && !own && wanted && !before) rc = columns();
+        if (rc != AR_OK) return rc;
     }
     if (!wanted) return AR_OK;
     return launch(reinterpret_cast<const void *>(&k_block_norm_sums), (unsigned)(3 * ((dim + 63) / 64)), 64 * kSumWaves, sum, stream);

@@ -238,3 +238,62 @@ def test_nothing_past_the_workspace_is_written(T, D):
     want = R.block_norm_grad(dh, dz, y, x, post, gate, pre, 1.0, EPS)
     for k, v in (("dx", dx), ("dy", dy), ("gate", grads[0]), ("post", grads[1]), ("pre", grads[2])):
         close(v, tuple(w.cpu() for w in want[k]), 2.0 ** -17 if v.dim() > 1 else 2.0 ** -16, k)
+
+
+@pytest.mark.parametrize("D", [264, 7000, 9000, 16384])
+@pytest.mark.parametrize("post,pre", [(True, True), (False, True), (True, False), (False, False)])
+def test_gradient_in_place_of_what_it_reads(D, post, pre):
+    """dx and dy over each of the rows, all gradients wanted: as apart from them."""
+    T = 37
+    announce(f"block_norm_grad in place {D} {post} {pre}")
+    s = make(T, D, 1, post, "shared", pre, D)
+    ws = torch.zeros(ar.ar_block_norm_bwd_workspace(T, D), dtype=torch.uint8, device=DEV)
+    names = ["h_grad", "x", "y"] + (["z_grad"] if pre else [])
+
+    def call(at_x, at_y):
+        t = {k: dev(s[k], D) for k in ("x", "h_grad", "z_grad", "post", "gate", "pre")}
+        t["y"] = dev(s["parts"][0], D)
+        dx = t[at_x] if at_x else torch.empty_like(t["x"])
+        dy = t[at_y] if at_y else torch.empty_like(t["x"])
+        grads = [torch.full((D,), 5.0, device=DEV) for _ in range(3)]
+        ar.ar_block_norm_bwd(t["h_grad"], t["z_grad"], t["y"], t["x"], dx, dy, ws, post_weight=t["post"], gate=t["gate"], pre_weight=t["pre"],
+                             gate_grad=grads[0], post_grad=grads[1] if post else None, pre_grad=grads[2] if pre else None, eps=EPS)
+        return dx, dy, *grads
+
+    want = call(None, None)
+    for at_x in names:
+        for at_y in names:
+            if at_x != at_y:
+                assert all(torch.equal(a, b) for a, b in zip(call(at_x, at_y), want)), (at_x, at_y)
+
+
+@pytest.mark.parametrize("D", [1000, 8200])
+def test_rows_far_apart(D):
+    """Strides past 2^31 elements."""
+    announce(f"block_norm with long strides {D}")
+    T, far = 3, (1 << 30) + 12345
+    s = make(T, D, 2, True, "token", True, D)
+
+    def spread(t):
+        base = torch.empty(far * (T - 1) + D, dtype=torch.bfloat16, device=DEV)
+        v = base.as_strided((T, D), (far, 1))
+        if t is not None:
+            v.copy_(t[:, :D])
+        return v
+
+    parts, x, gate, h, z = [spread(p) for p in s["parts"]], spread(s["x"]), spread(s["gate"]), spread(None), spread(None)
+    w = dict(post_weight=dev(s["post"], D), gate=gate, pre_weight=dev(s["pre"], D), eps=EPS)
+    ar.ar_block_norm(parts, x, h, z, **w)
+    want = R.block_norm(s["parts"], s["x"], s["post"], s["gate"], s["pre"], 1.0, EPS)
+    close(h, want[0], 2.0 ** -18, "h")
+    close(z, want[1], 2.0 ** -18, "z")
+    ws = torch.zeros(ar.ar_block_norm_bwd_workspace(T, D), dtype=torch.uint8, device=DEV)
+    dg, sums = spread(None), [torch.empty(D, device=DEV) for _ in range(2)]
+    h.copy_(s["h_grad"])
+    z.copy_(s["z_grad"])
+    ar.ar_block_norm_bwd(h, z, parts[0], x, x, parts[1], ws, **w, gate_grad=dg, post_grad=sums[0], pre_grad=sums[1])
+    want = R.block_norm_grad(s["h_grad"], s["z_grad"], s["parts"][0], s["x"], s["post"], s["gate"], s["pre"], 1.0, EPS)
+    for got, k in ((x, "dx"), (parts[1], "dy"), (dg, "gate")):
+        close(got, want[k], 2.0 ** -17, k)
+    for got, k in zip(sums, ("post", "pre")):
+        close(got, want[k], 2.0 ** -16, k)
