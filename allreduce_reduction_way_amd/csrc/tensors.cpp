@@ -97,8 +97,8 @@ class Args {
         const at::Tensor &t = next(what);
         if (t.dim() == 1) return ar_rows{fitting(t, what, ScalarType::BFloat16, {dim}, true).data_ptr(), 0, 0};
         ar_rows r = as_plane(fitting(t, what, ScalarType::BFloat16, {tokens, dim}, false), what);
-        if (tokens == 1) r.token_stride = dim;
-        else if (tokens > 1 && r.token_stride == 0)
+        if (tokens <= 1) r.token_stride = dim;
+        else if (r.token_stride == 0)
             fail(PyExc_ValueError, "%s: one gate for all tokens is a tensor of shape (%lld)", what, (long long)dim);
         return r;
     }

@@ -278,7 +278,9 @@ __global__ __launch_bounds__(512) void k_w4_linear_wide(LinearArgs a) {
 
 template <int RT>
 const void *pick_linear(int columns, bool few) {
-    if (few && RT > 1) return reinterpret_cast<const void *>(&k_w4_linear_few<RT>);
+    if constexpr (RT > 1) {
+        if (few) return reinterpret_cast<const void *>(&k_w4_linear_few<RT>);
+    }
     return columns == 1   ? reinterpret_cast<const void *>(&k_w4_linear<RT, 1, RT <= 2 ? 2 : 1>)
            : columns == 2 ? reinterpret_cast<const void *>(&k_w4_linear_wide<RT, 2>)
            : columns == 3 ? reinterpret_cast<const void *>(&k_w4_linear_wide<RT, 3>)
@@ -355,7 +357,10 @@ int ar_w4_linear(ar_rows x, const void *packed, ar_rows out, int64_t tokens, int
     const int stage = kStage * 16, sums = 1024 * (columns * tiles < kJoin ? columns * tiles : kJoin);
     const unsigned lds = waves * (stage > sums ? stage : sums);
     void *args[] = {&a};
-    const void *fn = tiles == 4 ? pick_linear<4>(columns, few) : tiles == 3 ? pick_linear<3>(columns, few) : tiles == 2 ? pick_linear<2>(columns, few) : pick_linear<1>(columns, false);
+    const void *fn = tiles == 4   ? pick_linear<4>(columns, few)
+                     : tiles == 3 ? pick_linear<3>(columns, few)
+                     : tiles == 2 ? pick_linear<2>(columns, few)
+                                  : pick_linear<1>(columns, few);
     return hipLaunchKernel(fn, dim3((unsigned)blocks, (unsigned)groups), dim3(64 * waves), args, lds,
                            static_cast<hipStream_t>(stream)) == hipSuccess
                ? AR_OK
