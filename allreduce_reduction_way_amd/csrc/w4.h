@@ -65,7 +65,7 @@ __device__ __forceinline__ bf16x8 w4_operand(u32x4 codes, float scale, int s) {
 // and a wave turns what it gets through a piece of LDS of its own: x[i] is elements
 // 32 i + 8 (l % 4) .. + 7 of row l / 4 until a Stage has made it 32 a + 8 i .. + 7
 // of row r.  (Asking as the steps need them, 16 tokens times 8192 x 28672
-// took 59 us, and RIGHT_US with this.)  Past the row the stage leaves zeros:
+// took 59 us, and 29.5 with this.)  Past the row the stage leaves zeros:
 // codes are zeros there too, but infinity times zero is none.
 //
 // The loads stand behind no branch, where the compiler would wait for each: past a
@@ -103,8 +103,8 @@ struct Stage {
 #pragma unroll
         for (int s = 0; s < 4; ++s) from[s] = p + r * kStageRow + lane / 16 * 4 + (s ^ r / 4);
     }
-    // Inputs of chunk `chunk`, of rows of n.
-    __device__ __forceinline__ void put(u32x4 (&x)[4], int chunk, int n) const {
+    // Inputs of chunk `chunk`, of rows of n, into the steps' order.
+    __device__ __forceinline__ void turn(u32x4 (&x)[4], int chunk, int n) const {
         if ((chunk + 1) * kW4Chunk > n) {  // the same in all lanes
 #pragma unroll
             for (int i = 1; i < 4; ++i)
@@ -115,14 +115,8 @@ struct Stage {
 #pragma unroll
         for (int i = 0; i < 4; ++i) to[4 * i] = x[i];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
-    __device__ __forceinline__ void get(u32x4 (&x)[4]) const {
 #pragma unroll
         for (int s = 0; s < 4; ++s) x[s] = *from[s];
-    }
-    __device__ __forceinline__ void turn(u32x4 (&x)[4], int chunk, int n) const {
-        put(x, chunk, n);
-        get(x);
     }
 };
 

@@ -100,83 +100,13 @@ __device__ __forceinline__ void join_waves(const LinearArgs &a, const f32x4 (&ac
     }
 }
 
-// A workgroup computes RT tiles of outputs for C times 16 tokens.  Its waves take
-// the chunks in turn, each with sums of its own, and join them through LDS.  U:
-// chunks that a wave has on their way at once.
-template <int RT, int C, int U>
-__global__ __launch_bounds__(512) void k_w4_linear(LinearArgs a) {
-    extern __shared__ f32x4 part[];  // [waves][min(RT C, kJoin)][64], and before that a stage of each wave
-    const int lane = threadIdx.x % 64;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
-    const int tile0 = blockIdx.x * RT;
-    const int64_t token0 = (int64_t)blockIdx.y * (16 * C);
-    const uint8_t *tile[RT];
-    const uint16_t *row[C];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) tile[t] = a.packed + min(tile0 + t, a.s.tiles - 1) * a.s.tile_bytes;
-    // a column past the tokens is not stored; it takes the last token's row
-#pragma unroll
-    for (int c = 0; c < C; ++c) row[c] = a.x.p + min(token0 + c * 16 + lane / 4, a.tokens - 1) * a.x.ts + lane % 4 * 8;
-    const Stage stage(reinterpret_cast<u32x4 *>(part) + wave * kStage, lane);
-    f32x4 acc[RT][C];
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[t][c] = f32x4{0, 0, 0, 0};
-
-    // U chunks are on their way while U others are worked on
-    struct {
-        u32x4 codes[U][RT], x[U][C][4];
-        uint32_t byte[U][RT];
-    } buf[2];
-    const auto load = [&](int b, int chunk) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = min(chunk + u * waves, a.s.chunks - 1);
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                buf[b].codes[u][t] = w4_codes(tile[t], c, lane);
-                buf[b].byte[u][t] = w4_scale(tile[t], a.s.chunks, c, lane);
-            }
-#pragma unroll
-            for (int i = 0; i < C; ++i) load_inputs(buf[b].x[u][i], row[i], c, a.s.n_in);
-        }
-    };
-    const auto work = [&](int b, int chunk) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (chunk + u * waves >= a.s.chunks) break;
-#pragma unroll
-            for (int i = 0; i < C; ++i) stage.turn(buf[b].x[u][i], chunk + u * waves, a.s.n_in);
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const bf16x8 w = w4_operand(buf[b].codes[u][t], kv4_scale(buf[b].byte[u][t]), s);
-#pragma unroll
-                    for (int i = 0; i < C; ++i) acc[t][i] = w4_product(w, buf[b].x[u][i][s], acc[t][i]);
-                }
-        }
-    };
-    const int step = U * waves;
-    if (wave < a.s.chunks) load(0, wave);
-    for (int c = wave; c < a.s.chunks; c += 2 * step) {
-        if (c + step < a.s.chunks) load(1, c + step);
-        work(0, c);
-        if (c + step >= a.s.chunks) break;
-        if (c + 2 * step < a.s.chunks) load(0, c + 2 * step);
-        work(1, c + step);
-    }
-    join_waves<RT, C>(a, acc, part, tile0, token0);
-}
-
-// Up to eight tokens and two tiles or more: the lanes that have a token load its
-// inputs as the steps take them, with no turn through LDS, and with no chunk ahead
-// there are twice as many waves.  (One token x 7168 x 7168 takes 8.4 us, 9.9 by
-// k_w4_linear; eight 9.0 and 10.2; sixteen would take 11.1, and 10.7 there; with one
-// tile to a workgroup 14336 x 4096 takes 13.8, and 12.0 there.)
-template <int RT>
+// Up to eight tokens, and four tiles to a workgroup: the lanes that have a token load
+// its inputs as the steps take them, with no turn through LDS, and with fewer
+// registers.  (One token x 4096 x 14336 takes 8.6 us, 9.3 by k_w4_linear; eight x
+// 8192 x 14336 15.1 and 15.4.  With fewer tiles the loads, which take 16 bytes of each
+// row, weigh more: eight x 8192 x 5120 would take 9.2, and 8.1 there.)
 __global__ __launch_bounds__(512) void k_w4_linear_few(LinearArgs a) {
+    constexpr int RT = 4;
     extern __shared__ f32x4 part[];  // [waves][RT][64]
     const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
@@ -210,13 +140,16 @@ __global__ __launch_bounds__(512) void k_w4_linear_few(LinearArgs a) {
     join_waves<RT, 1>(a, acc, part, tile0, 0);
 }
 
-// More than 16 tokens: C times 16 of them.  A chunk's weights are turned into
-// bf16 once, for all columns, and the inputs of 16 columns are replaced by the next
-// chunk's as soon as they have been used.  Codes are two chunks ahead, since they
-// come from further away, and are asked for after the inputs: loads are waited for
-// in their order, and inputs that stood behind codes waited for those.
+// A workgroup computes RT tiles of outputs for C times 16 tokens.  Its waves take
+// the chunks in turn, each with sums of its own, and join them through LDS.  A
+// chunk's weights are turned into bf16 once, for all columns.  While it works on 16
+// columns a wave has the next 16's inputs on their way, and from a chunk's first
+// columns on the next chunk's codes.  What bounds it is the rate at which a compute
+// unit gets inputs from L2, some 28 bytes in a cycle (RT = 1 with eight, twelve and
+// sixteen waves: 64 tokens x 7168 x 7168 28.7, 29.8 and 30.7 us): with a whole chunk's
+// inputs ahead the same took 20.5 us for 18.9 with RT = 2.
 template <int RT, int C>
-__global__ __launch_bounds__(512) void k_w4_linear_wide(LinearArgs a) {
+__global__ __launch_bounds__(512) void k_w4_linear(LinearArgs a) {
     extern __shared__ f32x4 part[];  // [waves][min(RT C, kJoin)][64], and before that a stage of each wave
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
@@ -235,21 +168,19 @@ __global__ __launch_bounds__(512) void k_w4_linear_wide(LinearArgs a) {
     for (int t = 0; t < RT; ++t)
 #pragma unroll
         for (int c = 0; c < C; ++c) acc[t][c] = f32x4{0, 0, 0, 0};
-    u32x4 codes[2][RT], x[C][4];
-    uint32_t byte[2][RT];
-    const auto load_codes = [&](int b, int c) {
+    u32x4 codes[RT], x[2][4];
+    uint32_t byte[RT];
+    const auto load_codes = [&](int c) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            codes[b][t] = w4_codes(tile[t], c, lane);
-            byte[b][t] = w4_scale(tile[t], a.s.chunks, c, lane);
+            codes[t] = w4_codes(tile[t], c, lane);
+            byte[t] = w4_scale(tile[t], a.s.chunks, c, lane);
         }
     };
     const int last = a.s.chunks - 1;
     if (wave <= last) {
-        load_codes(0, wave);
-#pragma unroll
-        for (int i = 0; i < C; ++i) load_inputs(x[i], row[i], wave, a.s.n_in);
-        load_codes(1, min(wave + waves, last));
+        load_codes(wave);
+        load_inputs(x[0], row[0], wave, a.s.n_in);
     }
     for (int first = wave; first <= last; first += 2 * waves) {
 #pragma unroll
@@ -260,31 +191,29 @@ __global__ __launch_bounds__(512) void k_w4_linear_wide(LinearArgs a) {
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) w[t][s] = w4_operand(codes[b][t], kv4_scale(byte[b][t]), s);
+                for (int s = 0; s < 4; ++s) w[t][s] = w4_operand(codes[t], kv4_scale(byte[t]), s);
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                stage.turn(x[i], c, a.s.n_in);
+                u32x4(&now)[4] = x[(b * C + i) & 1];
+                load_inputs(x[(b * C + i + 1) & 1], row[(i + 1) % C], i + 1 < C ? c : next, a.s.n_in);
+                if (i == 0) load_codes(next);
+                stage.turn(now, c, a.s.n_in);
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
 #pragma unroll
-                    for (int t = 0; t < RT; ++t) acc[t][i] = w4_product(w[t][s], x[i][s], acc[t][i]);
-                load_inputs(x[i], row[i], next, a.s.n_in);
+                    for (int t = 0; t < RT; ++t) acc[t][i] = w4_product(w[t][s], now[s], acc[t][i]);
             }
-            load_codes(b, min(c + 2 * waves, last));
         }
     }
     join_waves<RT, C>(a, acc, part, tile0, token0);
 }
 
 template <int RT>
-const void *pick_linear(int columns, bool few) {
-    if constexpr (RT > 1) {
-        if (few) return reinterpret_cast<const void *>(&k_w4_linear_few<RT>);
-    }
-    return columns == 1   ? reinterpret_cast<const void *>(&k_w4_linear<RT, 1, RT <= 2 ? 2 : 1>)
-           : columns == 2 ? reinterpret_cast<const void *>(&k_w4_linear_wide<RT, 2>)
-           : columns == 3 ? reinterpret_cast<const void *>(&k_w4_linear_wide<RT, 3>)
-                          : reinterpret_cast<const void *>(&k_w4_linear_wide<RT, 4>);
+const void *pick_linear(int columns) {
+    return columns == 1   ? reinterpret_cast<const void *>(&k_w4_linear<RT, 1>)
+           : columns == 2 ? reinterpret_cast<const void *>(&k_w4_linear<RT, 2>)
+           : columns == 3 ? reinterpret_cast<const void *>(&k_w4_linear<RT, 3>)
+                          : reinterpret_cast<const void *>(&k_w4_linear<RT, 4>);
 }
 
 RowsArg matrix(const void *p, int64_t stride, int64_t rows, int columns) {
@@ -341,7 +270,9 @@ int ar_w4_linear(ar_rows x, const void *packed, ar_rows out, int64_t tokens, int
     const int64_t groups = (tokens + 16 * columns - 1) / (16 * columns);
     // The time of the compute unit that has most to do: for each chunk its
     // tiles' codes, and the inputs, which cost as much as two tiles for every 16
-    // tokens however many tiles share them.
+    // tokens however many tiles share them.  (64 tokens x 7168 x 7168 take 28.7, 18.9,
+    // 21.7 and 23.6 us with one to four tiles, x 5120 x 10240 33.8, 27.1, 17.9 and 19.2,
+    // x 8192 x 28672 106.8, 77.7, 66.1 and 51.8.)
     int tiles = 1;
     int64_t least = 0;
     for (int n = 1; n <= 4; ++n) {
@@ -349,18 +280,19 @@ int ar_w4_linear(ar_rows x, const void *packed, ar_rows out, int64_t tokens, int
         if (n == 1 || time < least) least = time, tiles = n;
     }
     const int64_t blocks = (a.s.tiles + tiles - 1) / tiles;
-    const bool few = tokens <= 8;
-    // Four waves where compute units get more than one workgroup of four tiles: 64
-    // tokens x 8192 x 28672 take 52.5 us, and 56.0 with eight; with one, eight (one
-    // token x 4096 x 14336: 8.4, and 10.5 with four).
-    const int waves = tiles == 4 && blocks * groups > kCus ? 4 : 8;
+    const bool few = tokens <= 8 && tiles == 4;
+    // Four waves where compute units get more than one workgroup: 64 tokens x 8192 x
+    // 28672 take 51.8 us, and 54.1 with eight; x 5120 x 17408, three tiles, 31.6 and
+    // 34.3.  With one, eight: one token x 4096 x 14336 8.6, and 10.8 with four.
+    const int waves = blocks * groups > kCus ? 4 : 8;
     const int stage = kStage * 16, sums = 1024 * (columns * tiles < kJoin ? columns * tiles : kJoin);
     const unsigned lds = waves * (stage > sums ? stage : sums);
     void *args[] = {&a};
-    const void *fn = tiles == 4   ? pick_linear<4>(columns, few)
-                     : tiles == 3 ? pick_linear<3>(columns, few)
-                     : tiles == 2 ? pick_linear<2>(columns, few)
-                                  : pick_linear<1>(columns, few);
+    const void *fn = few          ? reinterpret_cast<const void *>(&k_w4_linear_few)
+                     : tiles == 4 ? pick_linear<4>(columns)
+                     : tiles == 3 ? pick_linear<3>(columns)
+                     : tiles == 2 ? pick_linear<2>(columns)
+                                  : pick_linear<1>(columns);
     return hipLaunchKernel(fn, dim3((unsigned)blocks, (unsigned)groups), dim3(64 * waves), args, lds,
                            static_cast<hipStream_t>(stream)) == hipSuccess
                ? AR_OK
