@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include "kv4.h"
+#include "rows.h"
 #include "wave.h"
 
 namespace ar {
@@ -59,21 +60,30 @@ __device__ __forceinline__ bf16x8 w4_operand(u32x4 codes, float scale, int s) {
 }
 
 // The other operand of a chunk's four steps comes from rows of n elements, sixteen
-// of them as columns.  A compute unit takes 64 bytes in a cycle where four lanes side
-// by side ask for them, and 16 where each asks for another row, as the steps
-// need them.  So lane l asks for 16 bytes of row l / 4, from element 8 (l % 4) on,
-// and a wave turns what it gets through a piece of LDS of its own: x[i] is elements
-// 32 i + 8 (l % 4) .. + 7 of row l / 4 until a Stage has made it 32 a + 8 i .. + 7
-// of row r.  (Asking as the steps need them, 16 tokens times 8192 x 28672
-// took 59 us, and 29.5 with this.)  Past the row the stage leaves zeros:
-// codes are zeros there too, but infinity times zero is none.
+// of them as columns.  A compute unit takes 64 bytes in a cycle where lanes side by
+// side ask for them, and 16 where each asks for another row, as the steps need
+// them.  So eight lanes ask for 128 bytes of a row, a line of the cache, and a wave
+// turns what it gets through a piece of LDS of its own: x[i] is elements
+// 64 (i / 2) + 8 (l % 8) .. + 7 of row 8 (i % 2) + l / 8 until a Stage has made it
+// 32 a + 8 i .. + 7 of row r.  (Asking as the steps need them, 16 tokens times
+// 8192 x 28672 took 59 us, and 29.5 with this; with four lanes to a row 64 tokens took
+// 51.3, and 50.1 with this.)  Past the row the stage leaves zeros: codes are
+// zeros there too, but infinity times zero is none.
 //
 // The loads stand behind no branch, where the compiler would wait for each: past a
 // row's end they take its last elements again.
-__device__ __forceinline__ void load_inputs(u32x4 (&x)[4], const uint16_t *row, int chunk, int n) {
+struct Inputs {
+    const uint16_t *row[2];
+
+    Inputs() = default;
+    // Of tokens [first, first + 16) of x; past `last` they are that one's.
+    __device__ __forceinline__ Inputs(const Rows &x, int64_t first, int64_t last, int lane)
+        : row{x.p + min(first + lane / 8, last) * x.ts, x.p + min(first + 8 + lane / 8, last) * x.ts} {}
+    __device__ __forceinline__ void load(u32x4 (&x)[4], int chunk, int lane, int n) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = load_vec8<false>(row + min(chunk * kW4Chunk + 32 * i, n - 32));
-}
+        for (int i = 0; i < 4; ++i) x[i] = load_vec8<false>(row[i % 2] + min(chunk * kW4Chunk + i / 2 * 64 + lane % 8 * 8, n - 8));
+    }
+};
 
 // The same for few columns, of which lane (r, q) has `row`, from element 32 q on:
 // loaded as the steps need them by the lanes that have a column, so that nothing is
@@ -90,16 +100,21 @@ __device__ __forceinline__ void load_few_inputs(u32x4 (&x)[4], const uint16_t *r
 
 // A wave's piece of LDS: 16 rows of 256 bytes, 320 apart, with the 16-byte blocks of
 // every 64 bytes in another order from four rows to the next.  Eight lanes at a time
-// write two rows' 64 bytes, and read a block of eight rows: neither meets in a bank.
+// write 128 bytes of a row, and read a block of eight rows: neither meets in a bank.
 constexpr int kStageRow = 320 / 16, kStage = 16 * kStageRow;  // in 16 bytes
 
 struct Stage {
-    u32x4 *to;
+    u32x4 *to[2];
     const u32x4 *from[4];
+    int lane;
 
-    __device__ __forceinline__ Stage(u32x4 *p, int lane) {
-        const int row = lane / 4, r = lane % 16;
-        to = p + row * kStageRow + (lane % 4 ^ row / 4);
+    __device__ __forceinline__ Stage(u32x4 *p, int lane) : lane(lane) {
+        const int r = lane % 16;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = i * 8 + lane / 8;
+            to[i] = p + row * kStageRow + lane % 8 / 4 * 4 + (lane % 4 ^ row / 4);
+        }
 #pragma unroll
         for (int s = 0; s < 4; ++s) from[s] = p + r * kStageRow + lane / 16 * 4 + (s ^ r / 4);
     }
@@ -107,13 +122,13 @@ struct Stage {
     __device__ __forceinline__ void turn(u32x4 (&x)[4], int chunk, int n) const {
         if ((chunk + 1) * kW4Chunk > n) {  // the same in all lanes
 #pragma unroll
-            for (int i = 1; i < 4; ++i)
-                if (chunk * kW4Chunk + 32 * i >= n) x[i] = u32x4{0, 0, 0, 0};
+            for (int i = 0; i < 4; ++i)
+                if (chunk * kW4Chunk + i / 2 * 64 + lane % 8 * 8 >= n) x[i] = u32x4{0, 0, 0, 0};
         }
         // one wave's accesses to LDS stay in order; the fences keep the compiler's
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int i = 0; i < 4; ++i) to[4 * i] = x[i];
+        for (int i = 0; i < 4; ++i) to[i % 2][i / 2 * 8] = x[i];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
         for (int s = 0; s < 4; ++s) x[s] = *from[s];

@@ -156,12 +156,12 @@ __global__ __launch_bounds__(512) void k_w4_linear(LinearArgs a) {
     const int tile0 = blockIdx.x * RT;
     const int64_t token0 = (int64_t)blockIdx.y * (16 * C);
     const uint8_t *tile[RT];
-    const uint16_t *row[C];
+    Inputs in[C];
 #pragma unroll
     for (int t = 0; t < RT; ++t) tile[t] = a.packed + min(tile0 + t, a.s.tiles - 1) * a.s.tile_bytes;
     // a column past the tokens is not stored; it takes the last token's row
 #pragma unroll
-    for (int c = 0; c < C; ++c) row[c] = a.x.p + min(token0 + c * 16 + lane / 4, a.tokens - 1) * a.x.ts + lane % 4 * 8;
+    for (int c = 0; c < C; ++c) in[c] = Inputs(a.x, token0 + c * 16, a.tokens - 1, lane);
     const Stage stage(reinterpret_cast<u32x4 *>(part) + wave * kStage, lane);
     f32x4 acc[RT][C];
 #pragma unroll
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(512) void k_w4_linear(LinearArgs a) {
     const int last = a.s.chunks - 1;
     if (wave <= last) {
         load_codes(wave);
-        load_inputs(x[0], row[0], wave, a.s.n_in);
+        in[0].load(x[0], wave, lane, a.s.n_in);
     }
     for (int first = wave; first <= last; first += 2 * waves) {
 #pragma unroll
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(512) void k_w4_linear(LinearArgs a) {
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 u32x4(&now)[4] = x[(b * C + i) & 1];
-                load_inputs(x[(b * C + i + 1) & 1], row[(i + 1) % C], i + 1 < C ? c : next, a.s.n_in);
+                in[(i + 1) % C].load(x[(b * C + i + 1) & 1], i + 1 < C ? c : next, lane, a.s.n_in);
                 if (i == 0) load_codes(next);
                 stage.turn(now, c, a.s.n_in);
 #pragma unroll
