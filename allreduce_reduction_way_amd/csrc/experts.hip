@@ -34,7 +34,8 @@ namespace {
 constexpr int kMaxExperts = 512, kMaxTopK = 16;
 constexpr int kTogether = 64;  // tokens of a pass
 constexpr int kMaxPairs = kTogether * kMaxTopK;
-constexpr int kLogits = 65536;  // partial logits of a pass, at most
+constexpr int kRouterParts = 512;           // workgroups of the router, but for the smallest and largest sizes
+constexpr int kLogits = kRouterParts * 256;  // partial logits of a pass, at most
 constexpr int kRouterWaves = 4, kChooseWaves = 8, kUpWaves = 8, kDownWaves = 8;
 constexpr int kColumns = 8;  // tokens of a group
 
@@ -550,7 +551,9 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         a.x.p += at * a.x.ts, a.out.p += at * a.out.ts;
         a.choice = static_cast<int32_t *>(choice) + at * top_k, a.weight = static_cast<float *>(weight) + at * top_k;
         const int expert_tiles = (experts + 15) / 16, token_tiles = (a.tokens + 15) / 16, units = (int)hidden / 32;
-        a.splits = 256 / (expert_tiles * token_tiles);
+        // 40 tokens x 7168 through 256 experts of 256: 133.2 us in all with 512, 135.4 with
+        // 256, 145.2 with 128.
+        a.splits = kRouterParts / (expert_tiles * token_tiles);
         if (a.splits > (units + kRouterWaves - 1) / kRouterWaves) a.splits = (units + kRouterWaves - 1) / kRouterWaves;
         if (a.splits < 1) a.splits = 1;
         int rc = launch3(reinterpret_cast<const void *>(&k_router), dim3(expert_tiles, token_tiles, a.splits), 64 * kRouterWaves, 0, a, stream);
@@ -559,6 +562,10 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         if (rc != AR_OK) return rc;
         const int slots = a.tokens * top_k < experts ? a.tokens * top_k : experts;
         const int half = (int)inner / 16;
+        // Two tiles of each where that leaves the chip full, or where an expert has
+        // several tokens, whose inputs weigh more than its weights.  (5 tokens x 7168, 256
+        // experts of 256: 44.4 us in all with one, 46.3 with two; 8 x 5120, 128 of 768:
+        // 88.0 and 80.4; 64 x 2048, 64 of 1408: 106.0 and 86.6.)
         const bool two_up = (int64_t)slots * half >= 1024 || a.tokens * top_k >= 8 * experts;
         rc = launch3(two_up ? reinterpret_cast<const void *>(&k_experts_up<2, 1>) : reinterpret_cast<const void *>(&k_experts_up<1, 2>),
                      dim3(two_up ? (half + 1) / 2 : half, slots), 64 * kUpWaves, 0, a, stream);
@@ -568,12 +575,15 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
             if (rc != AR_OK) return rc;
             continue;
         }
-        const int64_t tiles = (int64_t)slots * a.down.tiles;
-        const int n = tiles >= 4 * 8192 ? 4 : tiles >= 2 * 4096 ? 2 : 1;
-        const bool two = a.tokens > kColumns;
-        const int per = n * kDownWaves;
+        // Two tiles to a wave from some 32 to a compute unit on (16 tokens x 2048, 64
+        // experts of 1024: 59.1 us in all, 61.8 with one; 12 x 4096, 8 of 1536: 31.5 and 30.3),
+        // and two groups where experts have more than five tokens on average (64 x 2048,
+        // 64 of 1408: 86.5, 91.4 with one; 12 x 4096, 8 of 1536: 33.1 and 30.3).
+        const bool wide = (int64_t)slots * a.down.tiles >= 8192;
+        const bool two = a.tokens * top_k > 5 * experts;
+        const int per = (wide ? 2 : 1) * kDownWaves;
         const int block = a.down.chunks < kBlock / (two ? 2 : 1) ? a.down.chunks : kBlock / (two ? 2 : 1);
-        rc = launch3(n == 4 ? pick_down<4>(two) : n == 2 ? pick_down<2>(two) : pick_down<1>(two), dim3((a.down.tiles + per - 1) / per, slots),
+        rc = launch3(wide ? pick_down<2>(two) : pick_down<1>(two), dim3((a.down.tiles + per - 1) / per, slots),
                      64 * kDownWaves, block * (two ? 2 : 1) * 4096, a, stream);
         if (rc != AR_OK) return rc;
         rc = launch3(reinterpret_cast<const void *>(&k_experts_sum), dim3(((int)hidden + 4 * kThreads - 1) / (4 * kThreads), a.tokens), kThreads, 0, a, stream);

@@ -38,11 +38,11 @@ def test_linear(K, N, T):
     assert bool((out[-1] == 7.0).all())
 
 
-# tokens, hidden, inner, experts, top_k: one, two and four tiles to a wave of the second
+# tokens, hidden, inner, experts, top_k: one and two tiles to a wave of the second
 # product, with one and two groups of tokens; inner sizes past a block of chunks
 @pytest.mark.parametrize("T,H,I,E,k", [
     (8, 1056, 32, 128, 16), (10, 1056, 32, 128, 16), (8, 4128, 32, 128, 16), (10, 4128, 32, 128, 16), (2, 64, 2208, 3, 2), (12, 64, 2208, 3, 2),
-    (30, 96, 1120, 2, 2), (1, 96, 2208, 4, 3), (66, 64, 1056, 3, 2), (3, 2208, 64, 4, 2), (64, 1056, 64, 64, 8)])
+    (30, 96, 1120, 2, 2), (1, 96, 2208, 4, 3), (66, 64, 1056, 3, 2), (3, 2208, 64, 4, 2), (64, 1056, 64, 64, 8), (64, 2080, 32, 64, 8)])
 def test_experts(T, H, I, E, k):
     announce(f"w4_experts rules {T} {H} {I} {E} {k}")
     layer = Layer(T, H, I, E, T + H + I)
