@@ -562,7 +562,9 @@ int sum_slots(int64_t tokens, int dim) {
     int64_t most = dim > kSumDim ? 32 : dim > 4096 ? 256 : waves <= 2 ? 1024 : 2048 / waves;
     if (most > 256 && most > tokens / 4) most = tokens / 4 > 256 ? tokens / 4 : 256;
     if (most > slot_rows(tokens, dim)) most = slot_rows(tokens, dim);
-    return (int)(tokens < 1 ? 1 : tokens < most ? tokens : most);
+    if (tokens <= most) return (int)(tokens < 1 ? 1 : tokens);
+    const int64_t each = (tokens + most - 1) / most;  // of the workgroup with most: no more workgroups than that needs
+    return (int)((tokens + each - 1) / each);
 }
 
 }  // namespace
