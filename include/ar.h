@@ -489,8 +489,9 @@ int ar_block_norm_bwd(ar_rows h_grad, ar_rows z_grad, ar_rows y, ar_rows x, cons
  * k = 128 c + 32 a + i:
  *     code byte   1024 c + (16 a + r) 16 + i/2, the even input in the low half
  *     scale byte  1024 C + 256 (c/4) + (16 a + r) 4 + c%4
- * What lies past n_out and n_in has codes of zero.  Scale bytes other than 2 to 252 and
- * 255 are not specified, and of a group with 255 all weights are NaN.
+ * What lies past n_out and n_in has codes of zero and a scale byte that is not 255.
+ * Scale bytes other than 2 to 252 and 255 are not specified for a group of weights, and
+ * of one with 255 all weights are NaN.
  *
  * ar_w4_pack quantises bf16 weights by the cache's rule and writes every byte of
  * the tiles; ar_w4_unpack gives the values back, exact in bf16.
