@@ -9,12 +9,12 @@
 // take 172 us (4.6 TB/s), five x 7168 through 256 of 256 48 us, one x 5120 through 64 of
 // 192, which is latency, 17.5 us.
 //
-// Five launches, each waiting for the one before:
+// Three to five launches, each waiting for the one before:
 // k_router: logits, with sums in 64 bits, so that what an expert's place among a
 //   token's turns on is the logit and not the order of a sum.  Matrix
 //   instructions for 64 bits; the inputs are split over many workgroups.
 // k_choose: joins the splits, and takes a token's experts from the largest logit
-//   down.
+//   down.  For a small router k_route does both.
 // k_experts_up: a workgroup has one expert that is taken, some tiles of its gate
 //   and the same of its up part, and all the tokens that take it as columns.  The
 //   result goes on in two bf16 parts, whose sum is off by 2^-17 of it at most:
@@ -24,8 +24,8 @@
 //   parts in 8 to 15.
 // k_experts_down: a workgroup has one expert, some tiles of its outputs, and its
 //   groups one or two at a time in LDS.  Each token's result is left in binary32.
-// k_experts_sum: a token's results by weight, in the order of its experts.  Of a
-// single token k_experts_down_one makes the sum at once.
+// k_experts_sum: a token's results by weight, in the order of its experts.
+// Of up to eight tokens k_experts_down_few makes products and sums at once.
 #include "host.h"
 #include "rows.h"
 #include "w4.h"
@@ -37,8 +37,9 @@ constexpr int kMaxExperts = 512, kMaxTopK = 16;
 constexpr int kTogether = 64;  // tokens of a pass
 constexpr int kMaxPairs = kTogether * kMaxTopK;
 constexpr int kRouterParts = 512;           // workgroups of the router, but for the smallest and largest sizes
+constexpr int kRouteAlone = 1 << 15;          // weights of a router whose logits one workgroup makes
 constexpr int kLogits = kRouterParts * 256;  // partial logits of a pass, at most
-constexpr int kRouterWaves = 4, kChooseWaves = 8, kUpWaves = 8, kDownWaves = 8;
+constexpr int kRouterWaves = 4, kChooseWaves = 8, kRouteWaves = 16, kUpWaves = 8, kDownWaves = 8, kFewWaves = 16;
 constexpr int kColumns = 8;  // tokens of a group
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
@@ -52,11 +53,13 @@ struct ExpertsArgs {
     int32_t *choice;
     float *weight;
     int32_t *used;        // how many experts are taken
-    int4 *taken;          // each of them: expert, first group, tokens
+    int4 *taken;          // each of them: expert, first group, tokens, and a bit for each token where there are few
     int32_t *group_pair;  // the pairs (token, place) of each group
+    float *group_weight;  // where there are few, in its place: what each token weighs
     uint16_t *act;        // [groups][chunks of inner][4 steps][64 lanes][8]
     float *y;             // [pairs][hidden]
     int tokens, hidden, inner, experts, top_k, splits;
+    int few;              // up to kColumns tokens, whose columns are the same in every expert
     float scale;
 };
 
@@ -121,9 +124,54 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 
 // A token's experts are taken from the largest logit down, NaN before all numbers,
 // and of two alike the lower index first: a total order, so that each is taken once.
-// A workgroup to a token: its waves add up the splits, the first one chooses.
+// By one wave, whose lane l has the logits of experts l, 64 + l, ...
+constexpr int kEach = kMaxExperts / 64;
+
+struct Keys {
+    uint32_t of[kEach];  // rise with the logits
+
+    __device__ __forceinline__ void set(int w, bool there, double sum) {
+        of[w] = 0;  // past the experts: below every logit's
+        if (!there) return;
+        const float logit = (float)sum + 0.0f;  // no negative zero
+        const uint32_t bits = __float_as_uint(logit);
+        of[w] = logit != logit ? 0xFFFFFFFFu : bits >> 31 ? ~bits : bits | 0x80000000u;
+    }
+    __device__ __forceinline__ void choose(const ExpertsArgs &a, int token, int lane) {
+        int expert = 0;
+        uint32_t mine = 0;
+        for (int j = 0; j < a.top_k; ++j) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int w = 0; w < kEach; ++w) top = max(top, of[w]);
+            top = wave_max(top);
+            int found = -1;
+#pragma unroll
+            for (int w = 0; w < kEach; ++w) {
+                if (w * 64 >= a.experts) break;
+                const uint64_t mask = __ballot(of[w] == top);
+                if (found < 0 && mask) {
+                    const int at = __builtin_ctzll(mask);
+                    found = w * 64 + at;
+                    if (lane == at) of[w] = 0;
+                }
+            }
+            if (lane == j) expert = found, mine = top;
+        }
+        const float logit = mine == 0xFFFFFFFFu ? __builtin_nanf("") : __uint_as_float(mine >> 31 ? mine & 0x7FFFFFFFu : ~mine);
+        const float first = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(logit)));
+        const float e = lane < a.top_k ? expf(logit - first) : 0.0f;
+        const float weight = e / row16_sum(e) * a.scale;  // kMaxTopK lanes side by side
+        if (lane < a.top_k) {
+            a.choice[token * a.top_k + lane] = expert;
+            a.weight[token * a.top_k + lane] = weight;
+        }
+    }
+};
+
+// Joins the splits.  A workgroup to a token: its waves add them up, the first one
+// chooses.
 __global__ __launch_bounds__(64 * kChooseWaves) void k_choose(ExpertsArgs a) {
-    constexpr int kEach = kMaxExperts / 64;  // lane l has experts l, 64 + l, ...
     __shared__ double part[kChooseWaves][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), token = blockIdx.x;
     // a wave has 64 experts, and a part of the splits where there are fewer words
@@ -142,49 +190,69 @@ __global__ __launch_bounds__(64 * kChooseWaves) void k_choose(ExpertsArgs a) {
     part[wave][lane] = sum;
     __syncthreads();
     if (wave) return;
-    uint32_t key[kEach];
+    Keys keys;
 #pragma unroll
     for (int w = 0; w < kEach; ++w) {
-        key[w] = 0;  // past the experts: below every logit's
-        if (w * 64 >= a.experts) continue;
-        const int e = w * 64 + lane;
-        if (e < a.experts) {
-            double v = part[w][lane];
+        const bool there = w * 64 + lane < a.experts;
+        double v = 0;
+        if (there) {
+            v = part[w][lane];
             for (int i = 1; i < parts; ++i) v += part[w + i * words][lane];
-            const float logit = (float)v + 0.0f;  // no negative zero
-            const uint32_t bits = __float_as_uint(logit);
-            // rises with the logit
-            key[w] = logit != logit ? 0xFFFFFFFFu : bits >> 31 ? ~bits : bits | 0x80000000u;
         }
+        keys.set(w, there, v);
     }
-    int expert = 0;
-    uint32_t mine = 0;
-    for (int j = 0; j < a.top_k; ++j) {
-        uint32_t top = 0;
+    keys.choose(a, token, lane);
+}
+
+__device__ __forceinline__ double dpp_sum16(double v) {
+    const auto step = [](double v, auto control) {
+        constexpr int C = decltype(control)::value;
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, C, 0xf, 0xf, false);
+        const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), C, 0xf, 0xf, false);
+        return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    };
+    v = step(v, std::integral_constant<int, 0x128>());
+    v = step(v, std::integral_constant<int, 0x124>());
+    v = step(v, std::integral_constant<int, 0x122>());
+    return step(v, std::integral_constant<int, 0x121>());
+}
+
+// Logits and choice at once, where the router is small.  A workgroup to a token: a
+// wave takes experts in turn, or parts of their inputs where there are fewer experts
+// than waves.
+__global__ __launch_bounds__(64 * kRouteWaves) void k_route(ExpertsArgs a) {
+    __shared__ double part[kMaxExperts][4];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), token = blockIdx.x;
+    const int parts = a.experts >= kRouteWaves ? 1 : kRouteWaves / a.experts;
+    const uint16_t *x = a.x.p + token * a.x.ts;
+    for (int item = wave; item < a.experts * parts; item += kRouteWaves) {
+        const uint16_t *w = a.router + (int64_t)(item / parts) * a.hidden;
+        double sum = 0;
+        for (int k = (item % parts * 64 + lane) * 8; k < a.hidden; k += parts * 512) {
+            const u32x4 vw = load_vec8<false>(w + k), vx = load_vec8<false>(x + k);
+            float fw[8], fx[8];
+            widen(vw, fw);
+            widen(vx, fx);
 #pragma unroll
-        for (int w = 0; w < kEach; ++w) top = max(top, key[w]);
-        top = wave_max(top);
-        int found = -1;
-#pragma unroll
-        for (int w = 0; w < kEach; ++w) {
-            if (w * 64 >= a.experts) break;
-            const uint64_t mask = __ballot(key[w] == top);
-            if (found < 0 && mask) {
-                const int at = __builtin_ctzll(mask);
-                found = w * 64 + at;
-                if (lane == at) key[w] = 0;
-            }
+            for (int i = 0; i < 8; ++i) sum = __builtin_fma((double)fw[i], (double)fx[i], sum);
         }
-        if (lane == j) expert = found, mine = top;
+        sum = dpp_sum16(sum);
+        if (lane % 16 == 0) part[item][lane / 16] = sum;
     }
-    const float logit = mine == 0xFFFFFFFFu ? __builtin_nanf("") : __uint_as_float(mine >> 31 ? mine & 0x7FFFFFFFu : ~mine);
-    const float first = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(logit)));
-    const float e = lane < a.top_k ? expf(logit - first) : 0.0f;
-    const float weight = e / row16_sum(e) * a.scale;  // kMaxTopK lanes side by side
-    if (lane < a.top_k) {
-        a.choice[token * a.top_k + lane] = expert;
-        a.weight[token * a.top_k + lane] = weight;
+    __syncthreads();
+    if (wave) return;
+    Keys keys;
+#pragma unroll
+    for (int w = 0; w < kEach; ++w) {
+        const int expert = w * 64 + lane;
+        double v = 0;
+        if (expert < a.experts) {
+            for (int i = expert * parts; i < (expert + 1) * parts; ++i) v += (part[i][0] + part[i][1]) + (part[i][2] + part[i][3]);
+        }
+        keys.set(w, expert < a.experts, v);
     }
+    keys.choose(a, token, lane);
 }
 
 // One expert's tiles [tile0, tile0 + N) of the gate and of the up part, for all
@@ -236,11 +304,17 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(ExpertsArgs a) {
     }
     __syncthreads();
     if (blockIdx.x == 0 && (int)threadIdx.x < count) {
-        if (threadIdx.x == 0) {
-            a.taken[blockIdx.y] = int4{expert, base, count, 0};
-            if (blockIdx.y == 0) *a.used = before;
+        const int pair = list[threadIdx.x], token = pair / a.top_k;
+        if (a.few) a.group_weight[base * kColumns + token] = a.weight[pair];
+        else a.group_pair[base * kColumns + threadIdx.x] = pair;
+        if (wave == 0) {
+            int tokens = 0;  // few tokens are in one wave
+            for (int t = 0; a.few && t < a.tokens; ++t) tokens |= (__ballot(token == t) != 0) << t;
+            if (lane == 0) {
+                a.taken[blockIdx.y] = int4{expert, base, count, tokens};
+                if (blockIdx.y == 0) *a.used = before;
+            }
         }
-        a.group_pair[base * kColumns + threadIdx.x] = list[threadIdx.x];
     }
 
     const int half = a.inner / 16;  // tiles of the gate
@@ -303,8 +377,9 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(ExpertsArgs a) {
             for (int w = 1; w < kUpWaves; ++w) g += part[w][t][at], u += part[w][N + t][at];
             // element k of chunk c is one of step s of lane (column, k's 32)
             const int k = (tile0 + t) * 16 + at / 16 * 4, c = k / kW4Chunk, s = k % 32 / 8;
+            const int place = a.few ? list[column] / a.top_k : column % kColumns;
             uint16_t *to = a.act + ((((int64_t)(base + column / kColumns) * a.down.chunks + c) * 4 + s) * 64 +
-                                    k % kW4Chunk / 32 * 16 + column % kColumns) * 8 + k % 8;
+                                    k % kW4Chunk / 32 * 16 + place) * 8 + k % 8;
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -408,51 +483,54 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(ExpertsArgs a)
     }
 }
 
-// A single token: a workgroup has a tile of outputs of all its experts, whose chunks
-// its waves take in turn, two on their way at once.
-__global__ __launch_bounds__(64 * kDownWaves) void k_experts_down_one(ExpertsArgs a) {
-    __shared__ f32x4 part[kDownWaves][4];
+// Up to eight tokens: a workgroup has a tile of outputs of all experts that are taken,
+// whose chunks its waves take in turn.  Each expert is one
+// group, with the same columns for the same tokens: what an expert gives a token
+// that does not take it is left out, whatever it is.  Each tile reads all the
+// activations, four times the weights' bytes with eight tokens, and where the chunks
+// are many, those weigh more than a launch: five tokens x 7168 through 256 experts of 256
+// (80 chunks) take 48.2 us in all, 49.2 with k_experts_down and k_experts_sum, four x
+// 4096 through 8 of 1536 (96) 21.1 and 25.2, but seven x 2624 through 16 of 1504 (192)
+// 37.0 and 36.0, eight x 2048 through 64 of 1408 (528) 70.9 and 53.4.  A single token
+// takes an eighth of them.  (Two and four chunks on their way with eight waves: 49.1 and
+// 50.0 us for the 48.2.)
+__global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_few(ExpertsArgs a) {
+    __shared__ f32x4 part[kFewWaves][4][kColumns];
     const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int chunks = a.down.chunks, items = a.top_k * chunks;
+    const int chunks = a.down.chunks, token = r % kColumns;
     const uint8_t *tile = a.dn + blockIdx.x * a.down.tile_bytes;
+    const int items = *a.used * chunks;
     f32x4 sum = {0, 0, 0, 0};
-    for (int first = wave; first < items; first += 2 * kDownWaves) {
-        u32x4 codes[2], x[2][4];
-        uint32_t byte[2];
-        float weight[2];
+    for (int item = wave; item < items; item += kFewWaves) {
+        const int slot = item / chunks, c = item - slot * chunks;  // a group to a slot
+        const int4 taken = a.taken[slot];
+        const uint8_t *from = tile + __builtin_amdgcn_readfirstlane(taken.x) * a.down.bytes();
+        const float weight = a.group_weight[slot * kColumns + token];
+        u32x4 x[4];
+        load_few_inputs(x, a.act + ((int64_t)slot * chunks + c) * 4 * 64 * 8 + lane * 8, 64 * 8, token < a.tokens);
+        const u32x4 codes = w4_codes(from, c, lane);
+        const uint32_t byte = w4_scale(from, chunks, c, lane);
+        if (c * kW4Chunk + q * 32 >= a.inner) {  // nothing was written there
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int item = min(first + u * kDownWaves, items - 1), slot = item / chunks, c = item - slot * chunks;
-            const int4 taken = a.taken[slot];
-            const int expert = __builtin_amdgcn_readfirstlane(taken.x), base = __builtin_amdgcn_readfirstlane(taken.y);
-            weight[u] = a.weight[a.group_pair[base * kColumns]];
-            codes[u] = w4_codes(tile + expert * a.down.bytes(), c, lane);
-            byte[u] = w4_scale(tile + expert * a.down.bytes(), chunks, c, lane);
-            load_few_inputs(x[u], a.act + ((int64_t)base * chunks + c) * 4 * 64 * 8 + lane * 8, 64 * 8, r % kColumns == 0);
-            if (c * kW4Chunk + q * 32 >= a.inner) {  // nothing was written there
-#pragma unroll
-                for (int s = 0; s < 4; ++s) x[u][s] = u32x4{0, 0, 0, 0};
-            }
+            for (int s = 0; s < 4; ++s) x[s] = u32x4{0, 0, 0, 0};
         }
+        f32x4 d = {0, 0, 0, 0};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (first + u * kDownWaves >= items) break;
-            f32x4 d = {0, 0, 0, 0};
+        for (int s = 0; s < 4; ++s) d = w4_product(w4_operand(codes, kv4_scale(byte), s), x[s], d);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) d = w4_product(w4_operand(codes[u], kv4_scale(byte[u]), s), x[u][s], d);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] = dpp_add<0x128, 0xf>(d[i]);  // the two parts
-            sum += weight[u] * d;
-        }
+        for (int i = 0; i < 4; ++i) sum[i] += taken.w >> token & 1 ? weight * d[i] : 0.0f;
     }
-    if (r == 0) part[wave][q] = sum;
-    __syncthreads();
-    if (threadIdx.x >= 4) return;
-    f32x4 v = part[0][threadIdx.x];
 #pragma unroll
-    for (int w = 1; w < kDownWaves; ++w) v += part[w][threadIdx.x];
+    for (int i = 0; i < 4; ++i) sum[i] = dpp_add<0x128, 0xf>(sum[i]);  // the two parts
+    if (r < kColumns) part[wave][q][r] = sum;
+    __syncthreads();
+    const int n = threadIdx.x / kColumns, to_token = threadIdx.x % kColumns;
+    if (n >= 4 || to_token >= a.tokens) return;
+    f32x4 v = part[0][n][to_token];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) v += part[w][n][to_token];
     typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
-    uint16_t *to = const_cast<uint16_t *>(a.out.p) + blockIdx.x * 16 + threadIdx.x * 4;  // hidden is a multiple of 32
+    uint16_t *to = const_cast<uint16_t *>(a.out.p) + to_token * a.out.ts + blockIdx.x * 16 + n * 4;  // hidden is a multiple of 32
     *reinterpret_cast<u32x2_any *>(to) = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
 }
 
@@ -544,7 +622,7 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
     const Places at_ws(tokens, hidden, a.down.chunks, experts, top_k);
     a.logits = reinterpret_cast<double *>(ws);
     a.used = reinterpret_cast<int32_t *>(ws + at_ws.used), a.taken = reinterpret_cast<int4 *>(ws + at_ws.taken);
-    a.group_pair = reinterpret_cast<int32_t *>(ws + at_ws.pair);
+    a.group_pair = reinterpret_cast<int32_t *>(ws + at_ws.pair), a.group_weight = reinterpret_cast<float *>(ws + at_ws.pair);
     a.act = reinterpret_cast<uint16_t *>(ws + at_ws.act), a.y = reinterpret_cast<float *>(ws + at_ws.y);
     a.hidden = (int)hidden, a.inner = (int)inner, a.experts = experts, a.top_k = top_k, a.scale = scale;
     for (int64_t at = 0; at < tokens; at += kTogether) {
@@ -552,17 +630,26 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         a.x = rows(rx), a.out = rows(ro);
         a.x.p += at * a.x.ts, a.out.p += at * a.out.ts;
         a.choice = static_cast<int32_t *>(choice) + at * top_k, a.weight = static_cast<float *>(weight) + at * top_k;
-        const int expert_tiles = (experts + 15) / 16, token_tiles = (a.tokens + 15) / 16, units = (int)hidden / 32;
-        // 40 tokens x 7168 through 256 experts of 256: 133.2 us in all with 512, 135.4 with
-        // 256, 145.2 with 128.
-        a.splits = kRouterParts / (expert_tiles * token_tiles);
-        if (a.splits > (units + kRouterWaves - 1) / kRouterWaves) a.splits = (units + kRouterWaves - 1) / kRouterWaves;
-        if (a.splits < 1) a.splits = 1;
-        int rc = launch3(reinterpret_cast<const void *>(&k_router), dim3(expert_tiles, token_tiles, a.splits), 64 * kRouterWaves, 0, a, stream);
-        if (rc != AR_OK) return rc;
-        rc = launch3(reinterpret_cast<const void *>(&k_choose), dim3(a.tokens), 64 * kChooseWaves, 0, a, stream);
-        if (rc != AR_OK) return rc;
+        int rc;
+        // A small router's logits are made where the choice is: through 16 experts 2048 x
+        // 16 take 1.6 us less of the call, 7392 x 8 0.2 us more.
+        if ((int64_t)experts * hidden <= kRouteAlone) {
+            rc = launch3(reinterpret_cast<const void *>(&k_route), dim3(a.tokens), 64 * kRouteWaves, 0, a, stream);
+            if (rc != AR_OK) return rc;
+        } else {
+            const int expert_tiles = (experts + 15) / 16, token_tiles = (a.tokens + 15) / 16, units = (int)hidden / 32;
+            // 40 tokens x 7168 through 256 experts of 256: 133.2 us in all with 512, 135.4 with
+            // 256, 145.2 with 128.
+            a.splits = kRouterParts / (expert_tiles * token_tiles);
+            if (a.splits > (units + kRouterWaves - 1) / kRouterWaves) a.splits = (units + kRouterWaves - 1) / kRouterWaves;
+            if (a.splits < 1) a.splits = 1;
+            rc = launch3(reinterpret_cast<const void *>(&k_router), dim3(expert_tiles, token_tiles, a.splits), 64 * kRouterWaves, 0, a, stream);
+            if (rc != AR_OK) return rc;
+            rc = launch3(reinterpret_cast<const void *>(&k_choose), dim3(a.tokens), 64 * kChooseWaves, 0, a, stream);
+            if (rc != AR_OK) return rc;
+        }
         const int slots = a.tokens * top_k < experts ? a.tokens * top_k : experts;
+        a.few = a.tokens == 1 || (a.tokens <= kColumns && slots * a.down.chunks <= 128);  // see k_experts_down_few
         const int half = (int)inner / 16;
         // Two tiles of each where that leaves the chip full, or where an expert has
         // several tokens, whose inputs weigh more than its weights.  (5 tokens x 7168, 256
@@ -572,8 +659,8 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         rc = launch3(two_up ? reinterpret_cast<const void *>(&k_experts_up<2, 1>) : reinterpret_cast<const void *>(&k_experts_up<1, 2>),
                      dim3(two_up ? (half + 1) / 2 : half, slots), 64 * kUpWaves, 0, a, stream);
         if (rc != AR_OK) return rc;
-        if (a.tokens == 1) {
-            rc = launch3(reinterpret_cast<const void *>(&k_experts_down_one), dim3(a.down.tiles), 64 * kDownWaves, 0, a, stream);
+        if (a.few) {
+            rc = launch3(reinterpret_cast<const void *>(&k_experts_down_few), dim3(a.down.tiles), 64 * kFewWaves, 0, a, stream);
             if (rc != AR_OK) return rc;
             continue;
         }

@@ -42,7 +42,9 @@ def test_linear(K, N, T):
 # product, with one and two groups of tokens; inner sizes past a block of chunks
 @pytest.mark.parametrize("T,H,I,E,k", [
     (8, 1056, 32, 128, 16), (10, 1056, 32, 128, 16), (8, 4128, 32, 128, 16), (10, 4128, 32, 128, 16), (2, 64, 2208, 3, 2), (12, 64, 2208, 3, 2),
-    (30, 96, 1120, 2, 2), (1, 96, 2208, 4, 3), (66, 64, 1056, 3, 2), (3, 2208, 64, 4, 2), (64, 1056, 64, 64, 8), (64, 2080, 32, 64, 8)])
+    (30, 96, 1120, 2, 2), (1, 96, 2208, 4, 3), (66, 64, 1056, 3, 2), (3, 2208, 64, 4, 2), (64, 1056, 64, 64, 8), (64, 2080, 32, 64, 8),
+    (9, 64, 2208, 4, 1), (8, 544, 1056, 13, 8), (8, 160, 2208, 8, 8), (1, 96, 2208, 8, 8), (2, 1056, 64, 40, 3), (3, 2048, 32, 16, 4), (3, 2080, 32, 16, 4),
+    (7, 32, 32, 15, 5), (5, 8192, 32, 3, 2)])
 def test_experts(T, H, I, E, k):
     announce(f"w4_experts rules {T} {H} {I} {E} {k}")
     layer = Layer(T, H, I, E, T + H + I)
@@ -108,3 +110,33 @@ def test_experts_past_4_gib(T):
     if len(taken) >= k:
         assert torch.equal(local, c.apply_(lambda e: index[e]))
     close(out, value, size, "out", 2.0 ** -15)
+
+
+@pytest.mark.parametrize("T,H", [(3, 64), (8, 64), (8, 1056), (9, 64), (9, 1056)])
+def test_an_expert_of_nan(T, H):
+    """Weights of NaN in either product reach the tokens that take the expert, and no other."""
+    announce(f"w4_experts with an expert of NaN {T} {H}")
+    I, E, k = 160, 40, 3
+    layer = Layer(T, H, I, E, T + H)
+    clean, c, _ = layer.run(k)
+    for packed, scales in ((layer.packed_up, 256 * -(-H // 512)), (layer.packed_down, 256)):
+        kept, bad = packed.clone(), int(c[0, 1])
+        packed[bad, :, -scales:] = 255
+        out, choice, _ = layer.run(k)
+        takes = (choice == bad).any(1)
+        assert torch.equal(choice, c) and 0 < int(takes.sum()) < T
+        assert bool(torch.isnan(out.cpu()[takes]).all()) and torch.equal(out.cpu()[~takes], clean.cpu()[~takes])
+        packed.copy_(kept)
+
+
+@pytest.mark.parametrize("T", [1, 6, 20])
+def test_equal_logits_of_a_large_router(T):
+    announce(f"w4_experts with equal logits {T}")
+    layer = Layer(T, 544, 32, 70, 5)
+    layer.router[:] = layer.router[3]
+    layer.router[40] *= 2
+    layer.router[50] = -layer.router[40]
+    _, choice, weight = layer.run(5)
+    for t in range(T):
+        assert choice[t, 0].item() in (40, 50) and choice[t, 1:].tolist() == [0, 1, 2, 3]
+        assert weight[t, 1:].unique().numel() == 1
