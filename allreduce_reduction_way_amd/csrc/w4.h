@@ -51,6 +51,11 @@ __device__ __forceinline__ uint32_t w4_scale(const uint8_t *tile, int chunks, in
     return (tile + chunks * kW4Codes + c / 4 * kW4Scales + c % 4)[(uint32_t)lane * 4u];
 }
 
+// Those of chunks c and c + 1, c even, in two bytes.
+__device__ __forceinline__ uint32_t w4_two_scales(const uint8_t *tile, int chunks, int c, int lane) {
+    return *reinterpret_cast<const uint16_t *>(tile + chunks * kW4Codes + c / 4 * kW4Scales + c % 4 + (uint32_t)lane * 4u);
+}
+
 // The weights' operand of step s: eight codes of a lane as bf16, exactly.
 __device__ __forceinline__ bf16x8 w4_operand(u32x4 codes, float scale, int s) {
     u32x4 v;

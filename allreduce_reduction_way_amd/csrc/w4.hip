@@ -102,6 +102,77 @@ __device__ __forceinline__ void join_waves(const LinearArgs &a, const f32x4 (&ac
     }
 }
 
+// One or two tokens, and up to four with one tile to a workgroup: all inputs are held in
+// LDS, so that what a wave loads for a chunk is its codes and a byte of scales to a
+// lane, of two chunks side by side at once.  Sixteen tokens' worth of loads for one token
+// are what bounds k_w4_linear there: one token x 14336 x 4096 takes 8.5 us, 11.7 by that,
+// x 7168 x 7168 7.7 and 8.5, x 5120 x 20480 12.6 and 14.2, two tokens 9.3 and 11.6, 8.1
+// and 8.4, 13.0 and 14.2, four 11.0 and 11.6, but 8.9 and 8.4, 14.7 and 14.3.  With four
+// tiles and one workgroup to a compute unit k_w4_linear_few takes less: one token x 4096 x
+// 14336 8.6 us, and 9.1 this.
+constexpr int kHeldPad = 8;            // elements between tokens
+constexpr int kHeldBytes = 150 << 10;  // of LDS, at most
+
+int held_row(const W4Shape &s) { return s.chunks * kW4Chunk + kHeldPad; }
+
+template <int RT>
+__global__ __launch_bounds__(RT == 1 ? 1024 : 512) void k_w4_linear_held(LinearArgs a) {
+    extern __shared__ f32x4 part[];  // the inputs of each token, and after that [waves][RT][64]
+    uint16_t *held = reinterpret_cast<uint16_t *>(part);
+    const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
+    const int tile0 = blockIdx.x * RT;
+    const uint8_t *tile[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) tile[t] = a.packed + min(tile0 + t, a.s.tiles - 1) * a.s.tile_bytes;
+    const int last = a.s.chunks - 1, vecs = a.s.chunks * kW4Chunk / 8, row = a.s.chunks * kW4Chunk + kHeldPad;
+    u32x4 codes[2][RT];
+    uint32_t bytes[RT];
+    const auto load = [&](int chunk) {
+        const int c = min(chunk, last & ~1);  // past the end: again what is there
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            codes[0][t] = w4_codes(tile[t], c, lane);
+            codes[1][t] = w4_codes(tile[t], min(c + 1, last), lane);
+            bytes[t] = w4_two_scales(tile[t], a.s.chunks, c, lane);
+        }
+    };
+    load(2 * wave);
+    for (int i = threadIdx.x; i < (int)a.tokens * vecs; i += blockDim.x) {
+        const int t = i / vecs, k = (i - t * vecs) * 8;
+        u32x4 v = {0, 0, 0, 0};
+        if (k < a.s.n_in) v = load_vec8<false>(a.x.p + t * a.x.ts + k);
+        *reinterpret_cast<u32x4 *>(held + t * row + k) = v;
+    }
+    __syncthreads();
+    // a column past the tokens is not stored; it takes the last token's row
+    const u32x4 *x = reinterpret_cast<const u32x4 *>(held + min(r, (int)a.tokens - 1) * row + q * 32);
+    f32x4 acc[RT][1];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t][0] = f32x4{0, 0, 0, 0};
+    for (int c = 2 * wave; c <= last; c += 2 * waves) {
+        bf16x8 w[2][RT][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) w[u][t][s] = w4_operand(codes[u][t], kv4_scale(bytes[t] >> 8 * u & 255), s);
+        load(c + 2 * waves);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (c + u > last) break;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const u32x4 v = x[(c + u) * (kW4Chunk / 8) + s];
+#pragma unroll
+                for (int t = 0; t < RT; ++t) acc[t][0] = w4_product(w[u][t][s], v, acc[t][0]);
+            }
+        }
+    }
+    join_waves<RT, 1>(a, acc, part, tile0, 0);
+}
+
 // Up to eight tokens, and four tiles to a workgroup: the lanes that have a token load
 // its inputs as the steps take them, with no turn through LDS, and with fewer
 // registers.  (One token x 4096 x 14336 takes 8.6 us, 9.3 by k_w4_linear; eight x
@@ -218,6 +289,13 @@ const void *pick_linear(int columns) {
                           : reinterpret_cast<const void *>(&k_w4_linear<RT, 4>);
 }
 
+const void *pick_held(int tiles) {
+    return tiles == 4   ? reinterpret_cast<const void *>(&k_w4_linear_held<4>)
+           : tiles == 3 ? reinterpret_cast<const void *>(&k_w4_linear_held<3>)
+           : tiles == 2 ? reinterpret_cast<const void *>(&k_w4_linear_held<2>)
+                        : reinterpret_cast<const void *>(&k_w4_linear_held<1>);
+}
+
 RowsArg matrix(const void *p, int64_t stride, int64_t rows, int columns) {
     return RowsArg{ar_rows{const_cast<void *>(p), rows > 1 ? stride : 0, 0}, rows, 1, columns};
 }
@@ -282,15 +360,23 @@ int ar_w4_linear(ar_rows x, const void *packed, ar_rows out, int64_t tokens, int
         if (n == 1 || time < least) least = time, tiles = n;
     }
     const int64_t blocks = (a.s.tiles + tiles - 1) / tiles;
-    const bool few = tokens <= 8 && tiles == 4;
+    const bool shared = blocks * groups > kCus;  // compute units get more than one workgroup
+    const int64_t held_bytes = tokens * held_row(a.s) * 2;
+    const bool held = tokens <= (tiles == 1 ? 4 : 2) && (tiles < 4 || shared) && held_bytes <= kHeldBytes;
+    const bool few = !held && tokens <= 8 && tiles == 4;
     // Four waves where compute units get more than one workgroup: 64 tokens x 8192 x
     // 28672 take 51.8 us, and 54.1 with eight; x 5120 x 17408, three tiles, 31.6 and
-    // 34.3.  With one, eight: one token x 4096 x 14336 8.6, and 10.8 with four.
-    const int waves = blocks * groups > kCus ? 4 : 8;
-    const int stage = kStage * 16, sums = 1024 * (columns * tiles < kJoin ? columns * tiles : kJoin);
-    const unsigned lds = waves * (stage > sums ? stage : sums);
+    // 34.3.  With one, eight: one token x 4096 x 14336 8.6, and 10.8 with four.  Where the
+    // inputs are held, eight in both (one token x 8192 x 28672 24.4, and 25.7 with four),
+    // and sixteen to single tiles of more than 16 chunks (x 7168 x 2112 4.2, 4.6 with
+    // eight; x 2048 x 2048 3.3 and 3.0).
+    const int waves = held ? (tiles == 1 && a.s.chunks > 16 ? 16 : 8) : shared ? 4 : 8;
+    const int sums = 1024 * (columns * tiles < kJoin ? columns * tiles : kJoin);
+    const int inputs = held ? (int)held_bytes : few ? 0 : waves * kStage * 16;
+    const unsigned lds = inputs > waves * sums ? inputs : waves * sums;
     void *args[] = {&a};
-    const void *fn = few          ? reinterpret_cast<const void *>(&k_w4_linear_few)
+    const void *fn = held         ? pick_held(tiles)
+                     : few        ? reinterpret_cast<const void *>(&k_w4_linear_few)
                      : tiles == 4 ? pick_linear<4>(columns)
                      : tiles == 3 ? pick_linear<3>(columns)
                      : tiles == 2 ? pick_linear<2>(columns)

@@ -26,7 +26,7 @@ def weights(K, N):
 # one to four tiles of outputs to a workgroup, four of them with one workgroup to a
 # compute unit (eight waves) and with more (four)
 @pytest.mark.parametrize("K,N", [(2208, 900), (1184, 4790), (1184, 11190), (1184, 15990), (672, 32630)])
-@pytest.mark.parametrize("T", [1, 8, 9, 16, 30, 45, 63, 130])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9, 16, 30, 45, 63, 130])
 def test_linear(K, N, T):
     announce(f"w4_linear rules {T} {K} {N}")
     packed, w = weights(K, N)
@@ -52,6 +52,22 @@ def test_experts(T, H, I, E, k):
     (value, size), c, w = R.experts(layer.x, layer.router, layer.up, layer.down, k, 1.0)
     assert torch.equal(choice.long(), c) and bool(((weight.double() - w).abs() <= 2.0 ** -20 * w).all())
     close(out, value, size, "out", 2.0 ** -15)
+
+
+@pytest.mark.parametrize("T,K", [(1, 76640), (1, 76960), (2, 38240), (2, 38560), (4, 19040), (4, 19360), (1, 32), (4, 160), (3, 2016), (4, 2080)])
+def test_linear_of_long_rows(T, K):
+    """Inputs that just fit into LDS, and some that do not; odd counts of chunks.  Of 602
+    chunks a wave adds up to 301 instructions one after another: with an instruction's
+    own terms and the waves' sums 350 times 2^-24, below 2^-15."""
+    announce(f"w4_linear long rows {T} {K}")
+    g = torch.Generator().manual_seed(K)
+    packed, w = R.random_weights(37, K, g, K ** -0.5)
+    x = torch.full((T, K + 40), float("inf"), dtype=torch.bfloat16)
+    x[:, 5:5 + K] = torch.randn(T, K, generator=g).bfloat16()
+    out = torch.empty(T, 37, dtype=torch.bfloat16, device=DEV)
+    ar.ar_w4_linear(x.to(DEV)[:, 5:5 + K], packed.to(DEV), out)
+    value, size = R.linear(x[:, 5:5 + K], w)
+    close(out, value, size, "out", 2.0 ** -15 if K > 30000 else 2.0 ** -17)
 
 
 def random_packed(tiles, n_in, g):
