@@ -41,6 +41,7 @@ constexpr int kRouteAlone = 1 << 15;          // weights of a router whose logit
 constexpr int kLogits = kRouterParts * 256;  // partial logits of a pass, at most
 constexpr int kRouterWaves = 4, kChooseWaves = 8, kRouteWaves = 16, kUpWaves = 8, kDownWaves = 8, kFewWaves = 16;
 constexpr int kColumns = 8;  // tokens of a group
+constexpr int kCus = 256;
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
@@ -485,54 +486,67 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(ExpertsArgs a)
     }
 }
 
-// Up to eight tokens: a workgroup has a tile of outputs of all experts that are taken,
+// Up to eight tokens: a workgroup has N tiles of outputs of all experts that are taken,
 // whose chunks its waves take in turn.  Each expert is one
 // group, with the same columns for the same tokens: what an expert gives a token
 // that does not take it is left out, whatever it is.  Each tile reads all the
 // activations, four times the weights' bytes with eight tokens, and where the chunks
 // are many, those weigh more than a launch: five tokens x 7168 through 256 experts of 256
-// (80 chunks) take 48.2 us in all, 49.2 with k_experts_down and k_experts_sum, four x
+// (80 chunks) take 43.1 us in all, 48.6 with k_experts_down and k_experts_sum, four x
 // 4096 through 8 of 1536 (96) 21.1 and 25.2, but seven x 2624 through 16 of 1504 (192)
 // 37.0 and 36.0, eight x 2048 through 64 of 1408 (528) 70.9 and 53.4.  A single token
 // takes an eighth of them.  (Two and four chunks on their way with eight waves: 49.1 and
 // 50.0 us for the 48.2.)
+template <int N>
 __global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_few(ExpertsArgs a) {
-    __shared__ f32x4 part[kFewWaves][4][kColumns];
+    __shared__ f32x4 part[kFewWaves][N][4][kColumns];
     const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int chunks = a.down.chunks, token = r % kColumns;
-    const uint8_t *tile = a.dn + blockIdx.x * a.down.tile_bytes;
+    const int chunks = a.down.chunks, token = r % kColumns, tile0 = blockIdx.x * N;
     const int items = *a.used * chunks;
-    f32x4 sum = {0, 0, 0, 0};
+    f32x4 sum[N];
+#pragma unroll
+    for (int t = 0; t < N; ++t) sum[t] = f32x4{0, 0, 0, 0};
     for (int item = wave; item < items; item += kFewWaves) {
         const int slot = item / chunks, c = item - slot * chunks;  // a group to a slot
         const int4 taken = a.taken[slot];
-        const uint8_t *from = tile + __builtin_amdgcn_readfirstlane(taken.x) * a.down.bytes();
+        const uint8_t *from = a.dn + __builtin_amdgcn_readfirstlane(taken.x) * a.down.bytes();
         const float weight = a.group_weight[slot * kColumns + token];
-        u32x4 x[4];
+        u32x4 x[4], codes[N];
+        uint32_t byte[N];
         load_few_inputs(x, a.act + ((int64_t)slot * chunks + c) * 4 * 64 * 8 + lane * 8, 64 * 8, token < a.tokens);
-        const u32x4 codes = w4_codes(from, c, lane);
-        const uint32_t byte = w4_scale(from, chunks, c, lane);
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+            const uint8_t *tile = from + min(tile0 + t, a.down.tiles - 1) * a.down.tile_bytes;
+            codes[t] = w4_codes(tile, c, lane);
+            byte[t] = w4_scale(tile, chunks, c, lane);
+        }
         if (c * kW4Chunk + q * 32 >= a.inner) {  // nothing was written there
 #pragma unroll
             for (int s = 0; s < 4; ++s) x[s] = u32x4{0, 0, 0, 0};
         }
-        f32x4 d = {0, 0, 0, 0};
 #pragma unroll
-        for (int s = 0; s < 4; ++s) d = w4_product(w4_operand(codes, kv4_scale(byte), s), x[s], d);
+        for (int t = 0; t < N; ++t) {
+            f32x4 d = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] += taken.w >> token & 1 ? weight * d[i] : 0.0f;
+            for (int s = 0; s < 4; ++s) d = w4_product(w4_operand(codes[t], kv4_scale(byte[t]), s), x[s], d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[t][i] += taken.w >> token & 1 ? weight * d[i] : 0.0f;
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] = dpp_add<0x128, 0xf>(sum[i]);  // the two parts
-    if (r < kColumns) part[wave][q][r] = sum;
-    __syncthreads();
-    const int n = threadIdx.x / kColumns, to_token = threadIdx.x % kColumns;
-    if (n >= 4 || to_token >= a.tokens) return;
-    f32x4 v = part[0][n][to_token];
+    for (int t = 0; t < N; ++t) {
 #pragma unroll
-    for (int w = 1; w < kFewWaves; ++w) v += part[w][n][to_token];
+        for (int i = 0; i < 4; ++i) sum[t][i] = dpp_add<0x128, 0xf>(sum[t][i]);  // the two parts
+        if (r < kColumns) part[wave][t][q][r] = sum[t];
+    }
+    __syncthreads();
+    const int tile = tile0 + (int)threadIdx.x / (4 * kColumns), n = threadIdx.x / kColumns % 4, to_token = threadIdx.x % kColumns;
+    if ((int)threadIdx.x >= N * 4 * kColumns || to_token >= a.tokens || tile >= a.down.tiles) return;
+    f32x4 v = part[0][tile - tile0][n][to_token];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) v += part[w][tile - tile0][n][to_token];
     typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
-    uint16_t *to = const_cast<uint16_t *>(a.out.p) + to_token * a.out.ts + blockIdx.x * 16 + n * 4;  // hidden is a multiple of 32
+    uint16_t *to = const_cast<uint16_t *>(a.out.p) + to_token * a.out.ts + tile * 16 + n * 4;  // hidden is a multiple of 32
     *reinterpret_cast<u32x2_any *>(to) = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
 }
 
@@ -662,7 +676,12 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
                      dim3(two_up ? (half + 1) / 2 : half, slots), 64 * kUpWaves, 0, a, stream);
         if (rc != AR_OK) return rc;
         if (a.few) {
-            rc = launch3(reinterpret_cast<const void *>(&k_experts_down_few), dim3(a.down.tiles), 64 * kFewWaves, 0, a, stream);
+            // Two tiles where there are more than compute units: five tokens x 7168
+            // through 256 experts of 256 take 43.1 us in all, 47.3 with one; five x 1568
+            // through 8 of 1088 15.3 and 14.3.
+            const int n = a.down.tiles > kCus ? 2 : 1;
+            rc = launch3(n == 2 ? reinterpret_cast<const void *>(&k_experts_down_few<2>) : reinterpret_cast<const void *>(&k_experts_down_few<1>),
+                         dim3((a.down.tiles + n - 1) / n), 64 * kFewWaves, 0, a, stream);
             if (rc != AR_OK) return rc;
             continue;
         }

@@ -44,7 +44,7 @@ def test_linear(K, N, T):
     (8, 1056, 32, 128, 16), (10, 1056, 32, 128, 16), (8, 4128, 32, 128, 16), (10, 4128, 32, 128, 16), (2, 64, 2208, 3, 2), (12, 64, 2208, 3, 2),
     (30, 96, 1120, 2, 2), (1, 96, 2208, 4, 3), (66, 64, 1056, 3, 2), (3, 2208, 64, 4, 2), (64, 1056, 64, 64, 8), (64, 2080, 32, 64, 8),
     (9, 64, 2208, 4, 1), (8, 544, 1056, 13, 8), (8, 160, 2208, 8, 8), (1, 96, 2208, 8, 8), (2, 1056, 64, 40, 3), (3, 2048, 32, 16, 4), (3, 2080, 32, 16, 4),
-    (7, 32, 32, 15, 5), (5, 8192, 32, 3, 2)])
+    (7, 32, 32, 15, 5), (5, 8192, 32, 3, 2), (6, 4128, 160, 5, 2), (1, 4128, 96, 4, 4), (8, 4096, 64, 6, 2)])
 def test_experts(T, H, I, E, k):
     announce(f"w4_experts rules {T} {H} {I} {E} {k}")
     layer = Layer(T, H, I, E, T + H + I)
