@@ -34,11 +34,11 @@ struct BlockArgs {
     Rows x, gate, h, z;      // h, z: outputs, or what comes in for them (backwards)
     Rows dx, dy, dgate;      // backwards only
     const uint16_t *post, *pre;
-    float *slots;            // backwards: sums over a workgroup's tokens, 3 dim floats each
+    float *sums[3];          // backwards: sums over a workgroup's tokens for the gate, the norm after, the norm before
+                             // (null: none), 3 dim floats from a workgroup's to the next one's
     float *roots;            // backwards, beyond kSumDim: a token's r1, r2 and r2 mean(q n2)
     int64_t part_stride, tokens;
     int dim;
-    int shared_gate;         // backwards: all tokens have one gate
     int roots_only;          // backwards, beyond kSumDim: nothing but the roots is written
     float scale, eps;
 };
@@ -228,19 +228,19 @@ __device__ __forceinline__ void store_floats(float *to, const float (&f)[8]) {
 template <bool SHORT>
 __device__ __forceinline__ void store_sums(const BlockArgs &a, int64_t slot, const Eight<SHORT> &at, const float (&sg)[8], const float (&s1)[8],
                                            const float (&s2)[8]) {
-    float *to = a.slots + slot * 3 * a.dim + at.at;
+    const int64_t to = slot * 3 * a.dim + at.at;
     if (!SHORT && at.own == 0) {
-        if (a.shared_gate) store_floats(to, sg);
-        if (a.post) store_floats(to + a.dim, s1);
-        if (a.pre) store_floats(to + 2 * a.dim, s2);
+        if (a.sums[0]) store_floats(a.sums[0] + to, sg);
+        if (a.sums[1]) store_floats(a.sums[1] + to, s1);
+        if (a.sums[2]) store_floats(a.sums[2] + to, s2);
         return;
     }
 #pragma unroll
     for (int c = 0; c < 8; ++c)
         if (c >= at.own && at.at + c < a.dim) {
-            if (a.shared_gate) to[c] = sg[c];
-            if (a.post) to[a.dim + c] = s1[c];
-            if (a.pre) to[2 * a.dim + c] = s2[c];
+            if (a.sums[0]) a.sums[0][to + c] = sg[c];
+            if (a.sums[1]) a.sums[1][to + c] = s1[c];
+            if (a.sums[2]) a.sums[2][to + c] = s2[c];
         }
 }
 
@@ -560,12 +560,17 @@ int64_t slot_channels(int64_t tokens, int dim) {
 // rows as many as leave eight waves to each and four tokens to a workgroup (4096
 // tokens of 1024 take 28.8 us with 256, 20.7 with 1024; 440 take 9.9 with 256, 11.4
 // with one each, whose sums take longer to join).
+//
+// A few tokens' sums stay in one workgroup and are the gradients, without a launch to
+// join them: one token of 5120 takes 5.7 us (8.2), two 7.9 (8.2), but two of 8192 10.5
+// (10.2); 32 of 16384, whose rows are read again, 14.7 (20.8), 64 17.9 (18.6).
 int sum_slots(int64_t tokens, int dim) {
+    if (tokens <= (dim > kSumDim ? 32 : dim <= 6144 ? 2 : 1)) return 1;
     const int waves = lanes_of_grad(dim) / 64;
     int64_t most = dim > kSumDim ? 32 : dim > 4096 ? 256 : waves <= 2 ? 1024 : 2048 / waves;
     if (most > 256 && most > tokens / 4) most = tokens / 4 > 256 ? tokens / 4 : 256;
     if (most > slot_rows(tokens, dim)) most = slot_rows(tokens, dim);
-    if (tokens <= most) return (int)(tokens < 1 ? 1 : tokens);
+    if (tokens <= most) return (int)tokens;
     const int64_t each = (tokens + most - 1) / most;  // of the workgroup with most: no more workgroups than that needs
     return (int)((tokens + each - 1) / each);
 }
@@ -685,9 +690,10 @@ int ar_block_norm_bwd(ar_rows h_grad, ar_rows z_grad, ar_rows y, ar_rows x, cons
         if (gate.p) a.gate = rows(rg);
         if (gate_rows) a.dgate = rows(rdg);
         a.post = static_cast<const uint16_t *>(post_weight), a.pre = static_cast<const uint16_t *>(pre_weight);
-        a.slots = static_cast<float *>(workspace);
-        a.roots = a.slots + (int64_t)slots * 3 * dim;
-        a.shared_gate = shared;
+        // a single workgroup's sums are the gradients
+        float *const ws = static_cast<float *>(workspace);
+        for (int i = 0; i < 3; ++i) a.sums[i] = !sums[i] ? nullptr : slots == 1 ? static_cast<float *>(sums[i]) : ws + i * dim;
+        a.roots = ws + (int64_t)slots * 3 * dim;
         a.tokens = tokens, a.dim = dim, a.scale = residual_scale, a.eps = eps;
         const bool own = dim <= kSumDim;
         const unsigned blocks = own ? slots : tokens < 512 ? tokens : 512, lanes = lanes_of_grad(dim);
@@ -714,7 +720,7 @@ int ar_block_norm_bwd(ar_rows h_grad, ar_rows z_grad, ar_rows y, ar_rows x, cons
         if (rc == AR_OK && !own && wanted && !before) rc = columns();
         if (rc != AR_OK) return rc;
     }
-    if (!wanted) return AR_OK;
+    if (!wanted || (tokens > 0 && slots == 1)) return AR_OK;
     return launch(reinterpret_cast<const void *>(&k_block_norm_sums), (unsigned)(3 * ((dim + 63) / 64)), 64 * kSumWaves, sum, stream);
 }
 

@@ -297,3 +297,26 @@ def test_rows_far_apart(D):
         close(got, want[k], 2.0 ** -17, k)
     for got, k in zip(sums, ("post", "pre")):
         close(got, want[k], 2.0 ** -16, k)
+
+
+@pytest.mark.parametrize("T,D", [(1, 5), (2, 7), (1, 6144), (2, 6144), (3, 6144), (1, 6152), (2, 6152), (1, 8192), (2, 100), (3, 100), (1, 8200), (32, 8200), (33, 8200)])
+@pytest.mark.parametrize("wanted", [(True, True, True), (False, True, False), (True, False, True)])
+def test_gradients_of_a_few_tokens(T, D, wanted):
+    """Sums of one workgroup, and of a few, where some are not wanted."""
+    announce(f"block_norm_grad few {T} {D} {wanted}")
+    s = make(T, D, 1, True, "shared", True, T + D)
+    t = {k: dev(s[k], D) for k in ("x", "h_grad", "z_grad", "post", "gate", "pre")}
+    y, dx, dy = dev(s["parts"][0], D), torch.empty_like(t["x"]), torch.empty_like(t["x"])
+    ws = torch.full((ar.ar_block_norm_bwd_workspace(T, D),), 255, dtype=torch.uint8, device=DEV)
+    base = torch.full((3, D + 2), 5.0, device=DEV)
+    grads = [base[i, 1:-1] if w else None for i, w in enumerate(wanted)]
+    ar.ar_block_norm_bwd(t["h_grad"], t["z_grad"], y, t["x"], dx, dy, ws, post_weight=t["post"], gate=t["gate"], pre_weight=t["pre"],
+                         gate_grad=grads[0], post_grad=grads[1], pre_grad=grads[2], eps=EPS)
+    want = R.block_norm_grad(s["h_grad"], s["z_grad"], s["parts"][0], s["x"], s["post"], s["gate"], s["pre"], 1.0, EPS)
+    close(dx, want["dx"], 2.0 ** -17, "dx")
+    close(dy, want["dy"], 2.0 ** -17, "dy")
+    for i, k in enumerate(("gate", "post", "pre")):
+        if wanted[i]:
+            close(base[i, 1:-1], want[k], 2.0 ** -16, k)
+            base[i, 1:-1] = 5.0
+    assert bool((base == 5.0).all())
