@@ -25,7 +25,8 @@
 // k_experts_down: a workgroup has one expert, some tiles of its outputs, and its
 //   groups one or two at a time in LDS.  Each token's result is left in binary32.
 // k_experts_sum: a token's results by weight, in the order of its experts.
-// Of up to eight tokens k_experts_down_few makes products and sums at once.
+// Where the chunks are few, k_experts_down_few (up to eight tokens) or
+// k_experts_down_all makes products and sums at once.
 #include "host.h"
 #include "rows.h"
 #include "w4.h"
@@ -40,6 +41,7 @@ constexpr int kRouterParts = 512;           // workgroups of the router, but for
 constexpr int kRouteAlone = 1 << 15;          // weights of a router whose logits one workgroup makes
 constexpr int kLogits = kRouterParts * 256;  // partial logits of a pass, at most
 constexpr int kRouterWaves = 4, kChooseWaves = 8, kRouteWaves = 16, kUpWaves = 8, kDownWaves = 8, kFewWaves = 16;
+constexpr int kFewChunks = 128;
 constexpr int kColumns = 8;  // tokens of a group
 constexpr int kCus = 256;
 
@@ -61,6 +63,7 @@ struct ExpertsArgs {
     float *y;             // [pairs][hidden]
     int tokens, hidden, inner, experts, top_k, splits;
     int few;              // up to kColumns tokens, whose columns are the same in every expert
+    int all;              // more, and few chunks of all groups: `taken` has an entry for each group
     float scale;
 };
 
@@ -310,7 +313,12 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(ExpertsArgs a) {
         const int pair = list[threadIdx.x], token = pair / a.top_k;
         if (a.few) a.group_weight[base * kColumns + token] = a.weight[pair];
         else a.group_pair[base * kColumns + threadIdx.x] = pair;
-        if (wave == 0) {
+        if (a.all) {
+            if ((int)threadIdx.x == count - 1)
+                for (int i = count; i % kColumns; ++i) a.group_pair[base * kColumns + i] = -1;
+            if (threadIdx.x % kColumns == 0) a.taken[base + threadIdx.x / kColumns] = int4{expert, 0, 0, 0};
+            if (blockIdx.y == 0 && threadIdx.x == 0) *a.used = groups;
+        } else if (wave == 0) {
             int tokens = 0;  // few tokens are in one wave
             for (int t = 0; a.few && t < a.tokens; ++t) tokens |= (__ballot(token == t) != 0) << t;
             if (lane == 0) {
@@ -550,6 +558,50 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_few(ExpertsArgs
     *reinterpret_cast<u32x2_any *>(to) = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
 }
 
+// More tokens, but few chunks of all groups: products and sums at once as well.  A
+// wave has sums of its own of all tokens in LDS, to which it adds what a group's
+// columns are.  (15 tokens x 736 through 8 experts of 224, 46 chunks, take 14.6 us in all,
+// 17.4 with k_experts_down and k_experts_sum, 25 x 544 through 8 of 1152 (126) 20.8 and
+// 23.5, 13 x 2208 through 16 of 1088 (171) 29.5 and 26.3.)
+__global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_all(ExpertsArgs a) {
+    extern __shared__ f32x4 sums[];  // [waves][tokens][4, and one for the banks]
+    const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int chunks = a.down.chunks, items = *a.used * chunks, size = a.tokens * 5;
+    f32x4 *mine = sums + wave * size;
+    for (int i = lane; i < size; i += 64) mine[i] = f32x4{0, 0, 0, 0};
+    for (int item = wave; item < items; item += kFewWaves) {
+        const int group = item / chunks, c = item - group * chunks;
+        const uint8_t *tile = a.dn + __builtin_amdgcn_readfirstlane(a.taken[group].x) * a.down.bytes() + blockIdx.x * a.down.tile_bytes;
+        const int pair = a.group_pair[group * kColumns + r % kColumns];  // below zero: no token's
+        u32x4 x[4];
+        load_few_inputs(x, a.act + ((int64_t)group * chunks + c) * 4 * 64 * 8 + lane * 8, 64 * 8, pair >= 0);
+        const float weight = pair >= 0 ? a.weight[pair] : 0.0f;
+        const u32x4 codes = w4_codes(tile, c, lane);
+        const uint32_t byte = w4_scale(tile, chunks, c, lane);
+        if (c * kW4Chunk + q * 32 >= a.inner) {  // nothing was written there
+#pragma unroll
+            for (int s = 0; s < 4; ++s) x[s] = u32x4{0, 0, 0, 0};
+        }
+        f32x4 d = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) d = w4_product(w4_operand(codes, kv4_scale(byte), s), x[s], d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = dpp_add<0x128, 0xf>(d[i]);  // the two parts
+        if (r < kColumns && pair >= 0) mine[pair / a.top_k * 5 + q] += weight * d;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.tokens * 4; i += 64 * kFewWaves) {
+        const int n = i % 4, token = i / 4;
+        const f32x4 *p = sums + token * 5 + n;
+        f32x4 v = p[0];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) v += p[w * size];
+        typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+        uint16_t *to = const_cast<uint16_t *>(a.out.p) + token * a.out.ts + blockIdx.x * 16 + n * 4;  // hidden is a multiple of 32
+        *reinterpret_cast<u32x2_any *>(to) = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+    }
+}
+
 // Four outputs of a token to a lane.
 __global__ __launch_bounds__(kThreads) void k_experts_sum(ExpertsArgs a) {
     const int n = (blockIdx.x * kThreads + threadIdx.x) * 4, token = blockIdx.y;
@@ -665,7 +717,9 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
             if (rc != AR_OK) return rc;
         }
         const int slots = a.tokens * top_k < experts ? a.tokens * top_k : experts;
-        a.few = a.tokens == 1 || (a.tokens <= kColumns && slots * a.down.chunks <= 128);  // see k_experts_down_few
+        // see k_experts_down_few, k_experts_down_all
+        a.few = a.tokens == 1 || (a.tokens <= kColumns && slots * a.down.chunks <= kFewChunks);
+        a.all = a.tokens > kColumns && most_groups(a.tokens, experts, top_k) * a.down.chunks <= kFewChunks;
         const int half = (int)inner / 16;
         // Two tiles of each where that leaves the chip full, or where an expert has
         // several tokens, whose inputs weigh more than its weights.  (5 tokens x 7168, 256
@@ -682,6 +736,11 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
             const int n = a.down.tiles > kCus ? 2 : 1;
             rc = launch3(n == 2 ? reinterpret_cast<const void *>(&k_experts_down_few<2>) : reinterpret_cast<const void *>(&k_experts_down_few<1>),
                          dim3((a.down.tiles + n - 1) / n), 64 * kFewWaves, 0, a, stream);
+            if (rc != AR_OK) return rc;
+            continue;
+        }
+        if (a.all) {
+            rc = launch3(reinterpret_cast<const void *>(&k_experts_down_all), dim3(a.down.tiles), 64 * kFewWaves, kFewWaves * a.tokens * 5 * 16, a, stream);
             if (rc != AR_OK) return rc;
             continue;
         }

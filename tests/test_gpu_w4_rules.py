@@ -44,7 +44,9 @@ def test_linear(K, N, T):
     (8, 1056, 32, 128, 16), (10, 1056, 32, 128, 16), (8, 4128, 32, 128, 16), (10, 4128, 32, 128, 16), (2, 64, 2208, 3, 2), (12, 64, 2208, 3, 2),
     (30, 96, 1120, 2, 2), (1, 96, 2208, 4, 3), (66, 64, 1056, 3, 2), (3, 2208, 64, 4, 2), (64, 1056, 64, 64, 8), (64, 2080, 32, 64, 8),
     (9, 64, 2208, 4, 1), (8, 544, 1056, 13, 8), (8, 160, 2208, 8, 8), (1, 96, 2208, 8, 8), (2, 1056, 64, 40, 3), (3, 2048, 32, 16, 4), (3, 2080, 32, 16, 4),
-    (7, 32, 32, 15, 5), (5, 8192, 32, 3, 2), (6, 4128, 160, 5, 2), (1, 4128, 96, 4, 4), (8, 4096, 64, 6, 2)])
+    (7, 32, 32, 15, 5), (5, 8192, 32, 3, 2), (6, 4128, 160, 5, 2), (1, 4128, 96, 4, 4), (8, 4096, 64, 6, 2),
+    (9, 160, 1504, 20, 3), (9, 64, 2208, 8, 2), (30, 96, 2208, 2, 2), (64, 2080, 160, 64, 8), (64, 96, 64, 65, 8), (20, 160, 96, 3, 2), (64, 96, 288, 9, 5),
+    (129, 64, 160, 7, 3)])
 def test_experts(T, H, I, E, k):
     announce(f"w4_experts rules {T} {H} {I} {E} {k}")
     layer = Layer(T, H, I, E, T + H + I)
@@ -128,14 +130,14 @@ def test_experts_past_4_gib(T):
     close(out, value, size, "out", 2.0 ** -15)
 
 
-@pytest.mark.parametrize("T,H", [(3, 64), (8, 64), (8, 1056), (9, 64), (9, 1056)])
-def test_an_expert_of_nan(T, H):
+@pytest.mark.parametrize("T,H,I", [(3, 64, 160), (8, 64, 160), (8, 1056, 160), (9, 64, 160), (9, 1056, 160), (40, 64, 416), (8, 64, 800)])
+def test_an_expert_of_nan(T, H, I):
     """Weights of NaN in either product reach the tokens that take the expert, and no other."""
-    announce(f"w4_experts with an expert of NaN {T} {H}")
-    I, E, k = 160, 40, 3
+    announce(f"w4_experts with an expert of NaN {T} {H} {I}")
+    E, k = 40, 3
     layer = Layer(T, H, I, E, T + H)
     clean, c, _ = layer.run(k)
-    for packed, scales in ((layer.packed_up, 256 * -(-H // 512)), (layer.packed_down, 256)):
+    for packed, scales in ((layer.packed_up, 256 * -(-H // 512)), (layer.packed_down, 256 * -(-I // 512))):
         kept, bad = packed.clone(), int(c[0, 1])
         packed[bad, :, -scales:] = 255
         out, choice, _ = layer.run(k)
