@@ -6,8 +6,8 @@
 //     out = scale * sum_j p_j D_j a_j.
 // For a few tokens it is bound by the bytes of the experts that some token takes,
 // each read once however many tokens do.  64 tokens x 5120 through 128 experts of 768
-// take 172 us (4.6 TB/s), five x 7168 through 256 of 256 48 us, one x 5120 through 64 of
-// 192, which is latency, 17.5 us.
+// take 171 us (4.6 TB/s), five x 7168 through 256 of 256 44 us (2.6 TB/s), one x 5120
+// through 64 of 192, which is latency, 16.7 us.
 //
 // Three to five launches, each waiting for the one before:
 // k_router: logits, with sums in 64 bits, so that what an expert's place among a
