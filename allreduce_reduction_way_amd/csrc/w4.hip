@@ -217,10 +217,11 @@ __global__ __launch_bounds__(512) void k_w4_linear_few(LinearArgs a) {
 // the chunks in turn, each with sums of its own, and join them through LDS.  A
 // chunk's weights are turned into bf16 once, for all columns.  While it works on 16
 // columns a wave has the next 16's inputs on their way, and from a chunk's first
-// columns on the next chunk's codes.  What bounds it is the rate at which a compute
-// unit gets inputs from L2, some 28 bytes in a cycle (RT = 1 with eight, twelve and
-// sixteen waves: 64 tokens x 7168 x 7168 28.7, 29.8 and 30.7 us): with a whole chunk's
-// inputs ahead the same took 20.5 us for 18.9 with RT = 2.
+// columns on the next chunk's codes.  What bounds it is the inputs' way from L2 into each
+// compute unit: for 64 tokens x 6144 that alone takes 209 workgroups 9.6 us, with the turn
+// through LDS 10.8, and 10.9 with loads straight into LDS.  Other waves or depths gain
+// nothing: 64 tokens x 7168 x 7168 take 28.7, 29.8 and 30.7 us with eight, twelve and
+// sixteen waves and RT = 1, and 20.5 with a whole chunk's inputs ahead, 18.9 so, RT = 2.
 template <int RT, int C>
 __global__ __launch_bounds__(512) void k_w4_linear(LinearArgs a) {
     extern __shared__ f32x4 part[];  // [waves][min(RT C, kJoin)][64], and before that a stage of each wave
