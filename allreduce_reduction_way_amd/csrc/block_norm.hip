@@ -14,7 +14,7 @@
 // between.  A row lies in one workgroup, eight channels to a lane (twice eight
 // beyond 8192 channels), so that both norms' sums are exchanges within it.
 // Eight parts of 440 x 5120 take 9.7 us (5.1 TB/s), 8191 x 7169 with a gate for
-// each token 125 us (4.7 TB/s), the gradient of 4096 x 7168 90.5 us (5.2 TB/s)
+// each token 124 us (4.7 TB/s), the gradient of 4096 x 7168 90.5 us (5.2 TB/s)
 // and of 440 x 5120, whose three sums one after another are latency, 15.6 us.
 #include "host.h"
 #include "rows.h"
@@ -44,17 +44,11 @@ struct BlockArgs {
 };
 
 template <bool NT>
-__device__ __forceinline__ void store_vec8(uint16_t *p, const float (&f)[8], int n) {
+__device__ __forceinline__ void store_vec8(uint16_t *p, const float (&f)[8]) {
     const u32x4 v = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
-    if (n >= 8) {
-        u32x4_any *to = reinterpret_cast<u32x4_any *>(p);
-        if (NT) __builtin_nontemporal_store(v, to);
-        else *to = v;
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < n) p[i] = (uint16_t)(v[i / 2] >> (i % 2 * 16));
+    u32x4_any *to = reinterpret_cast<u32x4_any *>(p);
+    if (NT) __builtin_nontemporal_store(v, to);
+    else *to = v;
 }
 
 // Sums over the workgroup of N values, in the same order each time; every lane
@@ -77,34 +71,70 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (&part)[N][kMaxTh
     }
 }
 
+// Where a lane's eight channels lie.  Past the row's last eight it takes those, and of
+// them as its own what no lane before it has: no load stands behind a branch (with loads
+// of single channels behind branches the gradient's registers ran over, and 7439 rows of
+// 286 took 10.5 us forwards, 6.3 this way).  What it has of another lane's channels is
+// masked, whatever that lane has written there meanwhile where a result takes a row's
+// place.  Rows shorter than eight channels are one lane's, channel by channel.
+template <bool SHORT>
+struct Eight {
+    int at, own;  // the first channel, and of the eight the first own one
+
+    Eight() = default;
+    __device__ __forceinline__ Eight(int first, int dim) {
+        at = SHORT ? first : min(first, dim - 8);
+        own = SHORT ? 0 : min(first - at, 8);
+    }
+    // Of the own ones.
+    __device__ __forceinline__ u32x4 mask() const {
+        u32x4 m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = (2 * i >= own ? 0xFFFFu : 0) | (2 * i + 1 >= own ? 0xFFFF0000u : 0);
+        return m;
+    }
+    template <bool NT>
+    __device__ __forceinline__ u32x4 load(const uint16_t *row, int dim) const {
+        return SHORT ? load_few(row + at, dim - at) : load_vec8<NT>(further(row, 2u * at));
+    }
+    template <bool NT>
+    __device__ __forceinline__ void store(uint16_t *row, const float (&f)[8], int dim) const {
+        if (!SHORT && own == 0) {
+            store_vec8<NT>(further(row, 2u * at), f);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c >= own && at + c < dim) row[at + c] = (uint16_t)bf16_pair(f[c], 0.0f);
+        }
+    }
+};
+
 // P parts; V times eight channels to a lane.
 template <int P, int V, bool NT>
 __global__ __launch_bounds__(kMaxThreads) void k_block_norm(BlockArgs a) {
     __shared__ float part1[1][kMaxThreads / 64], part2[1][kMaxThreads / 64];
     const int64_t token = blockIdx.x;
+    const bool all = a.dim == V * 8 * (int)blockDim.x;  // every lane has eight of its own
     u32x4 y[V][P], x[V], g[V], w1[V], w2[V];
-    int at[V];
+    Eight<false> at[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        at[i] = (int)(threadIdx.x + i * blockDim.x) * 8;
-        const int n = a.dim - at[i];
+        at[i] = Eight<false>((threadIdx.x + i * blockDim.x) * 8, a.dim);
+        const u32x4 none = {0, 0, 0, 0};
 #pragma unroll
-        for (int p = 0; p < P; ++p) y[i][p] = u32x4{0, 0, 0, 0};
-        x[i] = g[i] = w1[i] = w2[i] = u32x4{0, 0, 0, 0};
-        if (n >= 8) {
+        for (int p = 0; p < P; ++p) y[i][p] = at[i].template load<NT>(a.part[p] + token * a.part_stride, a.dim);
+        x[i] = at[i].template load<NT>(a.x.p + token * a.x.ts, a.dim);
+        g[i] = a.gate.p ? at[i].template load<false>(a.gate.p + token * a.gate.ts, a.dim) : none;
+        w1[i] = a.post ? at[i].template load<false>(a.post, a.dim) : none;
+        if (V == 1) w2[i] = a.pre ? at[i].template load<false>(a.pre, a.dim) : none;
+    }
+    if (!all) {  // zeros for channels that are another lane's: they add nothing to a sum
 #pragma unroll
-            for (int p = 0; p < P; ++p) y[i][p] = load_vec8<NT>(further(a.part[p] + token * a.part_stride, 2u * at[i]));
-            x[i] = load_vec8<NT>(further(a.x.p + token * a.x.ts, 2u * at[i]));
-            if (a.gate.p) g[i] = load_vec8<false>(further(a.gate.p + token * a.gate.ts, 2u * at[i]));
-            if (a.post) w1[i] = load_vec8<false>(further(a.post, 2u * at[i]));
-            if (a.pre) w2[i] = load_vec8<false>(further(a.pre, 2u * at[i]));
-        } else if (n > 0) {
+        for (int i = 0; i < V; ++i) {
+            const u32x4 mask = at[i].mask();
 #pragma unroll
-            for (int p = 0; p < P; ++p) y[i][p] = load_few(a.part[p] + token * a.part_stride + at[i], n);
-            x[i] = load_few(a.x.p + token * a.x.ts + at[i], n);
-            if (a.gate.p) g[i] = load_few(a.gate.p + token * a.gate.ts + at[i], n);
-            if (a.post) w1[i] = load_few(a.post + at[i], n);
-            if (a.pre) w2[i] = load_few(a.pre + at[i], n);
+            for (int p = 0; p < P; ++p) y[i][p] &= mask;
+            x[i] &= mask, g[i] &= mask, w1[i] &= mask;
         }
     }
     float f[V][8];
@@ -147,9 +177,15 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm(BlockArgs a) {
             f[i][e] = a.scale * t[e] + (a.gate.p ? f[i][e] * w[e] : f[i][e]);
             s[0] += f[i][e] * f[i][e];
         }
-        store_vec8<NT>(further(const_cast<uint16_t *>(a.h.p) + token * a.h.ts, 2u * at[i]), f[i], a.dim - at[i]);
+        at[i].template store<NT>(const_cast<uint16_t *>(a.h.p) + token * a.h.ts, f[i], a.dim);
     }
     if (!a.pre) return;
+    // Sixteen channels to a lane have this weight no earlier: with it 65 registers
+    // left one row to a compute unit.
+    if (V > 1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) w2[i] = at[i].template load<false>(a.pre, a.dim);
+    }
     block_sum(s, part2);
     const float r = rsqrtf(s[0] * by + a.eps);
 #pragma unroll
@@ -158,41 +194,40 @@ __global__ __launch_bounds__(kMaxThreads) void k_block_norm(BlockArgs a) {
         widen(w2[i], w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[i][e] = f[i][e] * r * w[e];
-        store_vec8<NT>(further(const_cast<uint16_t *>(a.z.p) + token * a.z.ts, 2u * at[i]), f[i], a.dim - at[i]);
+        at[i].template store<NT>(const_cast<uint16_t *>(a.z.p) + token * a.z.ts, f[i], a.dim);
     }
 }
 
-// Where a lane's eight channels lie backwards.  Past the row's last eight it takes
-// those, and of them as its own what no lane before it has: no load stands behind a
-// branch (with loads of single channels behind branches the kernels' registers ran
-// over).  Rows shorter than eight channels are one lane's, channel by channel.
-template <bool SHORT>
-struct Eight {
-    int at, own;  // the first channel, and of the eight the first own one
-    u32x4 mask;   // of the own ones
-
-    Eight() = default;
-    __device__ __forceinline__ Eight(int first, int dim) {
-        at = SHORT ? first : min(first, dim - 8);
-        own = SHORT ? 0 : min(first - at, 8);
+// Rows shorter than eight channels: one to a lane.
+__global__ __launch_bounds__(kThreads) void k_block_norm_short(BlockArgs a, int parts) {
+    const int64_t token = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (token >= a.tokens) return;
+    const auto at = [&](const uint16_t *row, int c) { return lo_f32(row[c]); };
+    float f[7], s = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mask[i] = (2 * i >= own ? 0xFFFFu : 0) | (2 * i + 1 >= own ? 0xFFFF0000u : 0);
+    for (int c = 0; c < 7; ++c) {
+        f[c] = 0;
+        if (c >= a.dim) continue;
+        for (int p = 0; p < parts; ++p) f[c] += at(a.part[p] + token * a.part_stride, c);
+        s += f[c] * f[c];
     }
-    template <bool NT>
-    __device__ __forceinline__ u32x4 load(const uint16_t *row, int dim) const {
-        return SHORT ? load_few(row + at, dim - at) : load_vec8<NT>(further(row, 2u * at));
-    }
-    template <bool NT>
-    __device__ __forceinline__ void store(uint16_t *row, const float (&f)[8], int dim) const {
-        if (!SHORT && own == 0) {
-            store_vec8<NT>(further(row, 2u * at), f, 8);
-        } else {
+    const float r1 = a.post ? rsqrtf(s / a.dim + a.eps) : 1.0f;
+    s = 0;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (c >= own && at + c < dim) row[at + c] = (uint16_t)bf16_pair(f[c], 0.0f);
-        }
+    for (int c = 0; c < 7; ++c) {
+        if (c >= a.dim) continue;
+        if (a.post) f[c] = f[c] * r1 * at(a.post, c);
+        f[c] = a.scale * at(a.x.p + token * a.x.ts, c) + (a.gate.p ? f[c] * at(a.gate.p + token * a.gate.ts, c) : f[c]);
+        s += f[c] * f[c];
     }
-};
+    const float r2 = a.pre ? rsqrtf(s / a.dim + a.eps) : 0.0f;
+#pragma unroll
+    for (int c = 0; c < 7; ++c) {
+        if (c >= a.dim) continue;
+        (const_cast<uint16_t *>(a.h.p) + token * a.h.ts)[c] = (uint16_t)bf16_pair(f[c], 0.0f);
+        if (a.pre) (const_cast<uint16_t *>(a.z.p) + token * a.z.ts)[c] = (uint16_t)bf16_pair(f[c] * r2 * at(a.pre, c), 0.0f);
+    }
+}
 
 // What a lane holds of one token's rows backwards.  What is not there is zeros, or
 // ones for a gate, so that nothing asks for it again.
@@ -212,7 +247,8 @@ struct GradRow {
     // Zeros for channels that are another lane's: they add nothing to a sum.
     __device__ __forceinline__ GradRow own(const Eight<SHORT> &at, bool all) const {
         if (SHORT || all) return *this;
-        return GradRow{x & at.mask, y & at.mask, dh & at.mask, dz & at.mask, g};
+        const u32x4 mask = at.mask();
+        return GradRow{x & mask, y & mask, dh & mask, dz & mask, g};
     }
 };
 
@@ -618,6 +654,13 @@ int ar_block_norm(ar_ptrs parts, int64_t part_stride, int P, ar_rows x, const vo
     if (pre_weight) a.z = rows(rz);
     a.post = static_cast<const uint16_t *>(post_weight), a.pre = static_cast<const uint16_t *>(pre_weight);
     a.tokens = tokens, a.dim = dim, a.scale = residual_scale, a.eps = eps;
+    if (dim < 8) {
+        void *args[] = {&a, &P};
+        return hipLaunchKernel(reinterpret_cast<const void *>(&k_block_norm_short), dim3((unsigned)((tokens + kThreads - 1) / kThreads)), dim3(kThreads), args, 0,
+                               static_cast<hipStream_t>(stream)) == hipSuccess
+                   ? AR_OK
+                   : AR_ELAUNCH;
+    }
     const int64_t bytes = 2 * tokens * dim * (P + 3);
     const bool past = bytes > kStreamBytes, wide = is_wide(dim, P, past);
     return launch(pick(P, wide, past), (unsigned)tokens, threads_of(dim, wide), a, stream);
