@@ -528,11 +528,11 @@ const void *pick_grad(int dim, bool stream) {
                            : pick_sums<false>(dim);
 }
 
-// Sixteen channels to a lane: rows of more than 8192, and long ones that are
-// streamed, of up to four parts.  (8191 tokens of 7169: 117 us, 143 with eight; 4000 of
-// 5120 and four parts 51.3 and 52.4.  2400 of 5120 and eight parts 52.3, 49.0 with
-// eight; 8192 of 1024 16.2 and 14.8; 440 of 5120, not streamed, 5.8 and 5.3.)
-bool is_wide(int dim, int P, bool stream) { return dim > 8 * kMaxThreads || (stream && dim > 4096 && P <= 4); }
+// Sixteen channels to a lane: rows of more than 8192, and of more than 6144 and up to
+// four parts.  (8191 tokens of 7169: 106 us, 116 with eight; 3000 of 7168 and four parts
+// 53.5 and 54.9; 1000 of 8192 and two 13.7 and 15.0.  2100 of 8191 and eight parts 89.2,
+// 87.3 with eight; 8200 of 4104 53.2 and 50.3; 440 of 5120 and eight parts 10.2 and 9.8.)
+bool is_wide(int dim, int P) { return dim > 8 * kMaxThreads || (dim > 6144 && P <= 4); }
 
 unsigned threads_of(int dim, bool wide) {
     const int vecs = (dim + 7) / 8, lanes = wide ? (vecs + 1) / 2 : vecs;
@@ -662,7 +662,7 @@ int ar_block_norm(ar_ptrs parts, int64_t part_stride, int P, ar_rows x, const vo
                    : AR_ELAUNCH;
     }
     const int64_t bytes = 2 * tokens * dim * (P + 3);
-    const bool past = bytes > kStreamBytes, wide = is_wide(dim, P, past);
+    const bool past = bytes > kStreamBytes, wide = is_wide(dim, P);
     return launch(pick(P, wide, past), (unsigned)tokens, threads_of(dim, wide), a, stream);
 }
 

@@ -320,3 +320,17 @@ def test_gradients_of_a_few_tokens(T, D, wanted):
             close(base[i, 1:-1], want[k], 2.0 ** -16, k)
             base[i, 1:-1] = 5.0
     assert bool((base == 5.0).all())
+
+
+@pytest.mark.parametrize("D", [6136, 6144, 6145, 6152, 8191, 8192])
+@pytest.mark.parametrize("P", [1, 4, 5])
+def test_forward_around_the_change_of_lanes(D, P):
+    announce(f"block_norm lanes {D} {P}")
+    T = 3
+    s = make(T, D, P, True, "shared", True, D + P)
+    h, z = torch.empty(T, D, dtype=torch.bfloat16, device=DEV), torch.empty(T, D, dtype=torch.bfloat16, device=DEV)
+    ar.ar_block_norm([dev(p, D) for p in s["parts"]], dev(s["x"], D), h, z, post_weight=dev(s["post"], D), gate=dev(s["gate"], D),
+                     pre_weight=dev(s["pre"], D), eps=EPS)
+    want = R.block_norm([cut(p, D) for p in s["parts"]], s["x"], s["post"], s["gate"], s["pre"], 1.0, EPS)
+    close(h, want[0], 2.0 ** -18, "h")
+    close(z, want[1], 2.0 ** -18, "z")
