@@ -259,8 +259,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(ExpertsArgs a) {
     keys.choose(a, token, lane);
 }
 
-// One expert's tiles [tile0, tile0 + N) of the gate and of the up part, for all
-// tokens that take it.  U: chunks that a wave has on their way at once, one or two side
+// One expert's tiles of the gate and of the up part, N each at a time, for all tokens
+// that take it.  U: chunks that a wave has on their way at once, one or two side
 // by side, whose scales come in one load (five tokens x 7168 through 256 experts of 256
 // 47.4 us in all, 48.8 with a load for each).
 template <int N, int U>
@@ -329,85 +329,88 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(ExpertsArgs a) {
     }
 
     const int half = a.inner / 16;  // tiles of the gate
-    const int tile0 = blockIdx.x * N;
     const uint8_t *from = a.gate_up + expert * a.up.bytes();
-    const uint8_t *tile[2 * N];
+    bool again = false;
+    for (int tile0 = blockIdx.x * N; tile0 < half; tile0 += gridDim.x * N) {
+        const uint8_t *tile[2 * N];
 #pragma unroll
-    for (int t = 0; t < N; ++t) {
-        const int at = min(tile0 + t, half - 1);
-        tile[t] = from + at * a.up.tile_bytes;
-        tile[N + t] = from + (half + at) * a.up.tile_bytes;
-    }
-    for (int first = 0; first < count; first += 16) {
-        const bool mine = first + r < count;
-        const uint16_t *row = a.x.p + list[min(first + r, count - 1)] / a.top_k * a.x.ts + q * 32;
-        f32x4 acc[2 * N];
+        for (int t = 0; t < N; ++t) {
+            const int at = min(tile0 + t, half - 1);
+            tile[t] = from + at * a.up.tile_bytes;
+            tile[N + t] = from + (half + at) * a.up.tile_bytes;
+        }
+        for (int first = 0; first < count; first += 16) {
+            const bool mine = first + r < count;
+            const uint16_t *row = a.x.p + list[min(first + r, count - 1)] / a.top_k * a.x.ts + q * 32;
+            f32x4 acc[2 * N];
 #pragma unroll
-        for (int t = 0; t < 2 * N; ++t) acc[t] = f32x4{0, 0, 0, 0};
-        const auto step = [&](int chunk, auto number) {
-            constexpr int M = decltype(number)::value;
-            u32x4 codes[M][2 * N], x[M][4];
-            uint32_t byte[M][2 * N];
+            for (int t = 0; t < 2 * N; ++t) acc[t] = f32x4{0, 0, 0, 0};
+            const auto step = [&](int chunk, auto number) {
+                constexpr int M = decltype(number)::value;
+                u32x4 codes[M][2 * N], x[M][4];
+                uint32_t byte[M][2 * N];
 #pragma unroll
-            for (int u = 0; u < M; ++u) {
-                const int c = chunk + u;
+                for (int u = 0; u < M; ++u) {
+                    const int c = chunk + u;
 #pragma unroll
-                for (int t = 0; t < 2 * N; ++t) {
-                    codes[u][t] = w4_codes(tile[t], c, lane);
-                    byte[u][t] = M == 1 ? w4_scale(tile[t], a.up.chunks, c, lane) : u ? byte[0][t] >> 8 : w4_two_scales(tile[t], a.up.chunks, c, lane);
-                }
-                const int at = min(c * kW4Chunk, a.hidden - 32 - q * 32);  // past the row: inside it
-                load_few_inputs(x[u], row + at, 8, mine);
-            }
-#pragma unroll
-            for (int u = 0; u < M; ++u) {
-                const int c = chunk + u;
-                if ((c + 1) * kW4Chunk > a.hidden && c * kW4Chunk + q * 32 >= a.hidden) {
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) x[u][s] = u32x4{0, 0, 0, 0};
+                    for (int t = 0; t < 2 * N; ++t) {
+                        codes[u][t] = w4_codes(tile[t], c, lane);
+                        byte[u][t] = M == 1 ? w4_scale(tile[t], a.up.chunks, c, lane) : u ? byte[0][t] >> 8 : w4_two_scales(tile[t], a.up.chunks, c, lane);
+                    }
+                    const int at = min(c * kW4Chunk, a.hidden - 32 - q * 32);  // past the row: inside it
+                    load_few_inputs(x[u], row + at, 8, mine);
                 }
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
+                for (int u = 0; u < M; ++u) {
+                    const int c = chunk + u;
+                    if ((c + 1) * kW4Chunk > a.hidden && c * kW4Chunk + q * 32 >= a.hidden) {
 #pragma unroll
-                    for (int t = 0; t < 2 * N; ++t)
-                        acc[t] = w4_product(w4_operand(codes[u][t], kv4_scale(byte[u][t] & 255), s), x[u][s], acc[t]);
-            }
-        };
-        int c = U * wave;
-        for (; c + U <= a.up.chunks; c += U * kUpWaves) step(c, std::integral_constant<int, U>());
-        if (U > 1 && c < a.up.chunks) step(c, std::integral_constant<int, 1>());
-        if (first) __syncthreads();
+                        for (int s = 0; s < 4; ++s) x[u][s] = u32x4{0, 0, 0, 0};
+                    }
 #pragma unroll
-        for (int t = 0; t < 2 * N; ++t) part[wave][t][lane] = acc[t];
-        __syncthreads();
-        for (int item = threadIdx.x; item < N * 64; item += 64 * kUpWaves) {
-            const int t = item / 64, at = item % 64, column = first + at % 16;
-            if (column >= count || tile0 + t >= half) continue;
-            f32x4 g = part[0][t][at], u = part[0][N + t][at];
+                    for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int w = 1; w < kUpWaves; ++w) g += part[w][t][at], u += part[w][N + t][at];
-            // element k of chunk c is one of step s of lane (column, k's 32)
-            const int k = (tile0 + t) * 16 + at / 16 * 4, c = k / kW4Chunk, s = k % 32 / 8;
-            const int place = a.few ? list[column] / a.top_k : column % kColumns;
-            uint16_t *to = a.act + ((((int64_t)(base + column / kColumns) * a.down.chunks + c) * 4 + s) * 64 +
-                                    k % kW4Chunk / 32 * 16 + place) * 8 + k % 8;
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float v[2], rest[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float z = g[2 * i + j];
-                    v[j] = z / (1.0f + expf(-z)) * u[2 * i + j];
+                        for (int t = 0; t < 2 * N; ++t)
+                            acc[t] = w4_product(w4_operand(codes[u][t], kv4_scale(byte[u][t] & 255), s), x[u][s], acc[t]);
                 }
-                hi[i] = bf16_pair(v[0], v[1]);
-                const float back[2] = {lo_f32(hi[i]), hi_f32(hi[i])};
+            };
+            int c = U * wave;
+            for (; c + U <= a.up.chunks; c += U * kUpWaves) step(c, std::integral_constant<int, U>());
+            if (U > 1 && c < a.up.chunks) step(c, std::integral_constant<int, 1>());
+            if (again) __syncthreads();
+            again = true;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) rest[j] = fabsf(back[j]) < __builtin_inff() ? v[j] - back[j] : 0.0f;
-                lo[i] = bf16_pair(rest[0], rest[1]);
+            for (int t = 0; t < 2 * N; ++t) part[wave][t][lane] = acc[t];
+            __syncthreads();
+            for (int item = threadIdx.x; item < N * 64; item += 64 * kUpWaves) {
+                const int t = item / 64, at = item % 64, column = first + at % 16;
+                if (column >= count || tile0 + t >= half) continue;
+                f32x4 g = part[0][t][at], u = part[0][N + t][at];
+#pragma unroll
+                for (int w = 1; w < kUpWaves; ++w) g += part[w][t][at], u += part[w][N + t][at];
+                // element k of chunk c is one of step s of lane (column, k's 32)
+                const int k = (tile0 + t) * 16 + at / 16 * 4, c = k / kW4Chunk, s = k % 32 / 8;
+                const int place = a.few ? list[column] / a.top_k : column % kColumns;
+                uint16_t *to = a.act + ((((int64_t)(base + column / kColumns) * a.down.chunks + c) * 4 + s) * 64 +
+                                        k % kW4Chunk / 32 * 16 + place) * 8 + k % 8;
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float v[2], rest[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float z = g[2 * i + j];
+                        v[j] = z / (1.0f + expf(-z)) * u[2 * i + j];
+                    }
+                    hi[i] = bf16_pair(v[0], v[1]);
+                    const float back[2] = {lo_f32(hi[i]), hi_f32(hi[i])};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) rest[j] = fabsf(back[j]) < __builtin_inff() ? v[j] - back[j] : 0.0f;
+                    lo[i] = bf16_pair(rest[0], rest[1]);
+                }
+                *reinterpret_cast<uint2 *>(to) = uint2{hi[0], hi[1]};
+                *reinterpret_cast<uint2 *>(to + kColumns * 8) = uint2{lo[0], lo[1]};
             }
-            *reinterpret_cast<uint2 *>(to) = uint2{hi[0], hi[1]};
-            *reinterpret_cast<uint2 *>(to + kColumns * 8) = uint2{lo[0], lo[1]};
         }
     }
 }
@@ -726,8 +729,15 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         // experts of 256: 44.4 us in all with one, 46.3 with two; 8 x 5120, 128 of 768:
         // 88.0 and 80.4; 64 x 2048, 64 of 1408: 106.0 and 86.6.)
         const bool two_up = (int64_t)slots * half >= 1024 || a.tokens * top_k >= 8 * experts;
+        // Where a wave has no more than one chunk, finding the expert weighs as much, and
+        // two workgroups to a compute unit take tiles in turn: 64 x 512 through 128 experts
+        // of 1024 52.6 us in all, 67.5 with a workgroup to each; 64 x 5120 through 128 of
+        // 768 would take 180.3, 171.5 with one.
+        int up_blocks = two_up ? (half + 1) / 2 : half;
+        const int rounds = (int)((int64_t)up_blocks * slots / (2 * kCus));
+        if (a.up.chunks <= kUpWaves && rounds > 1) up_blocks = (up_blocks + rounds - 1) / rounds;
         rc = launch3(two_up ? reinterpret_cast<const void *>(&k_experts_up<2, 1>) : reinterpret_cast<const void *>(&k_experts_up<1, 2>),
-                     dim3(two_up ? (half + 1) / 2 : half, slots), 64 * kUpWaves, 0, a, stream);
+                     dim3(up_blocks, slots), 64 * kUpWaves, 0, a, stream);
         if (rc != AR_OK) return rc;
         if (a.few) {
             // Two tiles where there are more than compute units: five tokens x 7168

@@ -46,7 +46,7 @@ def test_linear(K, N, T):
     (9, 64, 2208, 4, 1), (8, 544, 1056, 13, 8), (8, 160, 2208, 8, 8), (1, 96, 2208, 8, 8), (2, 1056, 64, 40, 3), (3, 2048, 32, 16, 4), (3, 2080, 32, 16, 4),
     (7, 32, 32, 15, 5), (5, 8192, 32, 3, 2), (6, 4128, 160, 5, 2), (1, 4128, 96, 4, 4), (8, 4096, 64, 6, 2),
     (9, 160, 1504, 20, 3), (9, 64, 2208, 8, 2), (30, 96, 2208, 2, 2), (64, 2080, 160, 64, 8), (64, 96, 64, 65, 8), (20, 160, 96, 3, 2), (64, 96, 288, 9, 5),
-    (129, 64, 160, 7, 3)])
+    (129, 64, 160, 7, 3), (24, 160, 544, 64, 8), (64, 96, 1056, 40, 6), (64, 1024, 608, 33, 4)])
 def test_experts(T, H, I, E, k):
     announce(f"w4_experts rules {T} {H} {I} {E} {k}")
     layer = Layer(T, H, I, E, T + H + I)
