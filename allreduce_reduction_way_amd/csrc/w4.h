@@ -34,11 +34,14 @@ struct W4Shape {
     __host__ __device__ int64_t bytes() const { return tiles * tile_bytes; }
 };
 
+__host__ __device__ inline W4Shape w4_shape_of(int n_out, int n_in) {
+    const int chunks = (n_in + kW4Chunk - 1) / kW4Chunk;
+    return W4Shape{n_out, n_in, chunks, (n_out + 15) / 16, (int64_t)chunks * kW4Codes + (chunks + 3) / 4 * kW4Scales};
+}
+
 inline bool w4_shape(int64_t n_out, int64_t n_in, W4Shape *s) {
     if (n_out < 1 || n_out > kW4MaxOut || n_in < 32 || n_in > kW4MaxIn || n_in % 32) return false;
-    s->n_out = (int)n_out, s->n_in = (int)n_in;
-    s->chunks = (int)((n_in + kW4Chunk - 1) / kW4Chunk), s->tiles = (int)((n_out + 15) / 16);
-    s->tile_bytes = (int64_t)s->chunks * kW4Codes + (s->chunks + 3) / 4 * kW4Scales;
+    *s = w4_shape_of((int)n_out, (int)n_in);
     return true;
 }
 

@@ -59,11 +59,25 @@ __global__ __launch_bounds__(kThreads) void k_w4_unpack(UnpackArgs a) {
 
 constexpr int kCus = 256;
 
+// A call's arguments in 56 bytes: with more than 64 a launch costs its caller 3.3 us, which is more
+// than small calls take (one token x 1024 x 5120 3.3 us so, 3.8 with 88 bytes).
 struct LinearArgs {
+    const uint8_t *packed;
+    const uint16_t *x;
+    uint16_t *out;
+    int64_t x_stride, out_stride;
+    int n_out, n_in, tokens;
+};
+
+// The same as the kernels take them.
+struct Linear {
     W4Shape s;
     const uint8_t *packed;
     Rows x, out;
     int64_t tokens;
+
+    __device__ __forceinline__ explicit Linear(const LinearArgs &a)
+        : s(w4_shape_of(a.n_out, a.n_in)), packed(a.packed), x{a.x, a.x_stride, 0}, out{a.out, a.out_stride, 0}, tokens(a.tokens) {}
 };
 
 constexpr int kJoin = 8;  // tiles of sums in LDS at once
@@ -71,7 +85,7 @@ constexpr int kJoin = 8;  // tiles of sums in LDS at once
 // The waves' sums of RT tiles of outputs for C times 16 tokens, joined through LDS
 // some tiles at a time, and stored.
 template <int RT, int C>
-__device__ __forceinline__ void join_waves(const LinearArgs &a, const f32x4 (&acc)[RT][C], f32x4 *part, int tile0, int64_t token0) {
+__device__ __forceinline__ void join_waves(const Linear &a, const f32x4 (&acc)[RT][C], f32x4 *part, int tile0, int64_t token0) {
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
     constexpr int kTogether = RT * C < kJoin ? RT * C : kJoin;
 #pragma unroll
@@ -116,7 +130,8 @@ constexpr int kHeldBytes = 150 << 10;  // of LDS, at most
 int held_row(const W4Shape &s) { return s.chunks * kW4Chunk + kHeldPad; }
 
 template <int RT>
-__global__ __launch_bounds__(RT == 1 ? 1024 : 512) void k_w4_linear_held(LinearArgs a) {
+__global__ __launch_bounds__(RT == 1 ? 1024 : 512) void k_w4_linear_held(LinearArgs args) {
+    const Linear a(args);
     extern __shared__ f32x4 part[];  // the inputs of each token, and after that [waves][RT][64]
     uint16_t *held = reinterpret_cast<uint16_t *>(part);
     const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16;
@@ -178,7 +193,8 @@ __global__ __launch_bounds__(RT == 1 ? 1024 : 512) void k_w4_linear_held(LinearA
 // registers.  (One token x 4096 x 14336 takes 8.6 us, 9.3 by k_w4_linear; eight x
 // 8192 x 14336 15.1 and 15.4.  With fewer tiles the loads, which take 16 bytes of each
 // row, weigh more: eight x 8192 x 5120 would take 9.2, and 8.1 there.)
-__global__ __launch_bounds__(512) void k_w4_linear_few(LinearArgs a) {
+__global__ __launch_bounds__(512) void k_w4_linear_few(LinearArgs args) {
+    const Linear a(args);
     constexpr int RT = 4;
     extern __shared__ f32x4 part[];  // [waves][RT][64]
     const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16;
@@ -223,7 +239,8 @@ __global__ __launch_bounds__(512) void k_w4_linear_few(LinearArgs a) {
 // nothing: 64 tokens x 7168 x 7168 take 28.7, 29.8 and 30.7 us with eight, twelve and
 // sixteen waves and RT = 1, and 20.5 with a whole chunk's inputs ahead, 18.9 so, RT = 2.
 template <int RT, int C>
-__global__ __launch_bounds__(512) void k_w4_linear(LinearArgs a) {
+__global__ __launch_bounds__(512) void k_w4_linear(LinearArgs args) {
+    const Linear a(args);
     extern __shared__ f32x4 part[];  // [waves][min(RT C, kJoin)][64], and before that a stage of each wave
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), waves = blockDim.x / 64;
@@ -339,14 +356,14 @@ int ar_w4_unpack(const void *packed, void *w, int64_t row_stride, int64_t n_out,
 }
 
 int ar_w4_linear(ar_rows x, const void *packed, ar_rows out, int64_t tokens, int64_t n_out, int64_t n_in, void *stream) {
-    LinearArgs a = {};
-    if (!w4_shape(n_out, n_in, &a.s) || tokens < 0 || tokens > 1 << 20) return AR_EINVAL;
+    W4Shape shape;
+    if (!w4_shape(n_out, n_in, &shape) || tokens < 0 || tokens > 1 << 20) return AR_EINVAL;
     if (tokens == 0) return AR_OK;
     const RowsArg rx = matrix(x.p, x.token_stride, tokens, (int)n_in), ro = matrix(out.p, out.token_stride, tokens, (int)n_out);
     if (!rx.valid() || !ro.valid() || ro.self_overlap() || !packed || !aligned_to(packed, 16)) return AR_EINVAL;
-    if (ro.overlaps(rx) || overlap(ro.span(), Span{addr(packed), (uintptr_t)a.s.bytes()})) return AR_EALIAS;
-    a.packed = static_cast<const uint8_t *>(packed);
-    a.x = rows(rx), a.out = rows(ro), a.tokens = tokens;
+    if (ro.overlaps(rx) || overlap(ro.span(), Span{addr(packed), (uintptr_t)shape.bytes()})) return AR_EALIAS;
+    LinearArgs a = {static_cast<const uint8_t *>(packed), static_cast<const uint16_t *>(x.p), static_cast<uint16_t *>(out.p),
+                    rx.r.token_stride, ro.r.token_stride, (int)n_out, (int)n_in, (int)tokens};
     const int columns = tokens <= 16 ? 1 : tokens <= 32 ? 2 : tokens <= 48 ? 3 : 4;
     const int64_t groups = (tokens + 16 * columns - 1) / (16 * columns);
     // The time of the compute unit that has most to do: for each chunk its
@@ -357,12 +374,12 @@ int ar_w4_linear(ar_rows x, const void *packed, ar_rows out, int64_t tokens, int
     int tiles = 1;
     int64_t least = 0;
     for (int n = 1; n <= 4; ++n) {
-        const int64_t time = ((a.s.tiles + n - 1) / n * groups + kCus - 1) / kCus * (n + 2 * columns);
+        const int64_t time = ((shape.tiles + n - 1) / n * groups + kCus - 1) / kCus * (n + 2 * columns);
         if (n == 1 || time < least) least = time, tiles = n;
     }
-    const int64_t blocks = (a.s.tiles + tiles - 1) / tiles;
+    const int64_t blocks = (shape.tiles + tiles - 1) / tiles;
     const bool shared = blocks * groups > kCus;  // compute units get more than one workgroup
-    const int64_t held_bytes = tokens * held_row(a.s) * 2;
+    const int64_t held_bytes = tokens * held_row(shape) * 2;
     const bool held = tokens <= (tiles == 1 ? 4 : 2) && (tiles < 4 || shared) && held_bytes <= kHeldBytes;
     const bool few = !held && tokens <= 8 && tiles == 4;
     // Four waves where compute units get more than one workgroup: 64 tokens x 8192 x
@@ -371,7 +388,7 @@ int ar_w4_linear(ar_rows x, const void *packed, ar_rows out, int64_t tokens, int
     // inputs are held, eight in both (one token x 8192 x 28672 24.4, and 25.7 with four),
     // and sixteen to single tiles of more than 16 chunks (x 7168 x 2112 4.2, 4.6 with
     // eight; x 2048 x 2048 3.3 and 3.0).
-    const int waves = held ? (tiles == 1 && a.s.chunks > 16 ? 16 : 8) : shared ? 4 : 8;
+    const int waves = held ? (tiles == 1 && shape.chunks > 16 ? 16 : 8) : shared ? 4 : 8;
     const int sums = 1024 * (columns * tiles < kJoin ? columns * tiles : kJoin);
     const int inputs = held ? (int)held_bytes : few ? 0 : waves * kStage * 16;
     const unsigned lds = inputs > waves * sums ? inputs : waves * sums;
