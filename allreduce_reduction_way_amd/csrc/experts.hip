@@ -27,6 +27,8 @@
 // k_experts_sum: a token's results by weight, in the order of its experts.
 // Where the chunks are few, k_experts_down_few (up to eight tokens) or
 // k_experts_down_all makes products and sums at once.
+#include <math.h>
+
 #include "host.h"
 #include "rows.h"
 #include "w4.h"
@@ -47,6 +49,67 @@ constexpr int kCus = 256;
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
+// The numbers of a pass in one word.
+struct Sizes {
+    uint32_t word;
+
+    static Sizes of(int tokens, int top_k, int experts, bool few, bool all) {
+        return Sizes{(uint32_t)tokens | (uint32_t)top_k << 7 | (uint32_t)experts << 12 | (uint32_t)few << 22 | (uint32_t)all << 23};
+    }
+    __device__ __forceinline__ int tokens() const { return word & 127; }
+    __device__ __forceinline__ int top_k() const { return word >> 7 & 31; }
+    __device__ __forceinline__ int experts() const { return word >> 12 & 1023; }
+    // up to kColumns tokens, whose columns are the same in every expert
+    __device__ __forceinline__ int few() const { return word >> 22 & 1; }
+    // more, and few chunks of all groups: `taken` has an entry for each group
+    __device__ __forceinline__ int all() const { return word >> 23 & 1; }
+};
+
+// The workspace: logits, the experts that are taken, the groups' pairs, what goes
+// into the second product, and what comes out.  `most`: groups, at most.
+struct Places {
+    int64_t used, taken, pair, act, y;
+    __host__ __device__ Places(int64_t most, int chunks)
+        : used((int64_t)kLogits * 8), taken(used + 16), pair(taken + most * 16), act(pair + most * kColumns * 4), y(act + most * chunks * 4 * 64 * 16) {}
+};
+
+// Arguments of the launches, up to 64 bytes each: with more a launch costs its
+// caller 3.3 us (three tokens x 608 through 8 experts of 64 take 10.3 us so, and 10.5 with
+// 250 bytes).
+struct RouteArgs {
+    const uint16_t *router, *x;
+    int64_t x_stride;
+    double *logits;
+    int32_t *choice;
+    float *weight;
+    int hidden, splits;
+    float scale;
+    Sizes sizes;
+};
+
+struct UpArgs {
+    const uint8_t *gate_up;
+    const uint16_t *x;
+    int64_t x_stride;
+    const int32_t *choice;
+    const float *weight;
+    uint8_t *workspace;
+    int hidden, inner, most;
+    Sizes sizes;
+};
+
+struct DownArgs {
+    const uint8_t *down;
+    const float *weight;
+    uint16_t *out;
+    int64_t out_stride;
+    uint8_t *workspace;
+    int hidden, inner, most;
+    Sizes sizes;
+};
+static_assert(sizeof(RouteArgs) <= 64 && sizeof(UpArgs) <= 64 && sizeof(DownArgs) <= 64, "arguments of a cheap launch");
+
+// The same as the kernels take them.
 struct ExpertsArgs {
     W4Shape up, down;
     const uint8_t *gate_up, *dn;
@@ -61,16 +124,40 @@ struct ExpertsArgs {
     float *group_weight;  // where there are few, in its place: what each token weighs
     uint16_t *act;        // [groups][chunks of inner][4 steps][64 lanes][8]
     float *y;             // [pairs][hidden]
-    int tokens, hidden, inner, experts, top_k, splits;
-    int few;              // up to kColumns tokens, whose columns are the same in every expert
-    int all;              // more, and few chunks of all groups: `taken` has an entry for each group
+    int tokens, hidden, inner, experts, top_k, splits, few, all;
     float scale;
+
+    __device__ __forceinline__ void take(Sizes s) {
+        tokens = s.tokens(), top_k = s.top_k(), experts = s.experts(), few = s.few(), all = s.all();
+    }
+    __device__ __forceinline__ void place(uint8_t *workspace, int most) {
+        const Places at(most, down.chunks);
+        used = reinterpret_cast<int32_t *>(workspace + at.used), taken = reinterpret_cast<int4 *>(workspace + at.taken);
+        group_pair = reinterpret_cast<int32_t *>(workspace + at.pair), group_weight = reinterpret_cast<float *>(workspace + at.pair);
+        act = reinterpret_cast<uint16_t *>(workspace + at.act), y = reinterpret_cast<float *>(workspace + at.y);
+    }
+    __device__ __forceinline__ explicit ExpertsArgs(const RouteArgs &r)
+        : router(r.router), x{r.x, r.x_stride, 0}, logits(r.logits), choice(r.choice), weight(r.weight), hidden(r.hidden), splits(r.splits), scale(r.scale) {
+        take(r.sizes);
+    }
+    __device__ __forceinline__ explicit ExpertsArgs(const UpArgs &u)
+        : up(w4_shape_of(2 * u.inner, u.hidden)), down(w4_shape_of(u.hidden, u.inner)), gate_up(u.gate_up), x{u.x, u.x_stride, 0},
+          choice(const_cast<int32_t *>(u.choice)), weight(const_cast<float *>(u.weight)), hidden(u.hidden), inner(u.inner) {
+        take(u.sizes);
+        place(u.workspace, u.most);
+    }
+    __device__ __forceinline__ explicit ExpertsArgs(const DownArgs &d)
+        : down(w4_shape_of(d.hidden, d.inner)), dn(d.down), out{d.out, d.out_stride, 0}, weight(const_cast<float *>(d.weight)), hidden(d.hidden), inner(d.inner) {
+        take(d.sizes);
+        place(d.workspace, d.most);
+    }
 };
 
 // Logits of 16 experts and 16 tokens over a part of the inputs.  A lane takes
 // eight inputs of its expert and of its token at a time, and product s of eight
 // takes the s-th of each lane's.
-__global__ __launch_bounds__(64 * kRouterWaves) void k_router(ExpertsArgs a) {
+__global__ __launch_bounds__(64 * kRouterWaves) void k_router(RouteArgs args) {
+    const ExpertsArgs a(args);
     __shared__ double part[kRouterWaves][16][17];
     const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int expert0 = blockIdx.x * 16, token0 = blockIdx.y * 16;
@@ -175,7 +262,8 @@ struct Keys {
 
 // Joins the splits.  A workgroup to a token: its waves add them up, the first one
 // chooses.
-__global__ __launch_bounds__(64 * kChooseWaves) void k_choose(ExpertsArgs a) {
+__global__ __launch_bounds__(64 * kChooseWaves) void k_choose(RouteArgs args) {
+    const ExpertsArgs a(args);
     __shared__ double part[kChooseWaves][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), token = blockIdx.x;
     // a wave has 64 experts, and a part of the splits where there are fewer words
@@ -225,7 +313,8 @@ __device__ __forceinline__ double dpp_sum16(double v) {
 // Logits and choice at once, where the router is small.  A workgroup to a token: a
 // wave takes experts in turn, or parts of their inputs where there are fewer experts
 // than waves.
-__global__ __launch_bounds__(64 * kRouteWaves) void k_route(ExpertsArgs a) {
+__global__ __launch_bounds__(64 * kRouteWaves) void k_route(RouteArgs args) {
+    const ExpertsArgs a(args);
     __shared__ double part[kMaxExperts][4];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), token = blockIdx.x;
     const int parts = a.experts >= kRouteWaves ? 1 : kRouteWaves / a.experts;
@@ -264,7 +353,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(ExpertsArgs a) {
 // by side, whose scales come in one load (five tokens x 7168 through 256 experts of 256
 // 47.4 us in all, 48.8 with a load for each).
 template <int N, int U>
-__global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(ExpertsArgs a) {
+__global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(UpArgs args) {
+    const ExpertsArgs a(args);
     __shared__ int chosen[kMaxPairs], counts[kMaxExperts];
     __shared__ int list[kTogether];  // the pairs (token, place) that take the expert
     __shared__ f32x4 part[kUpWaves][2 * N][64];
@@ -420,7 +510,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(ExpertsArgs a) {
 constexpr int kBlock = 16;
 
 template <int N, int G>
-__global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(ExpertsArgs a) {
+__global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(DownArgs args) {
+    const ExpertsArgs a(args);
     extern __shared__ u32x4 act[];  // [groups][chunks of a block][4 steps][64 lanes]
     if ((int)blockIdx.y >= *a.used) return;
     const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -509,7 +600,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(ExpertsArgs a)
 // takes an eighth of them.  (Two and four chunks on their way with eight waves: 49.1 and
 // 50.0 us for the 48.2.)
 template <int N>
-__global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_few(ExpertsArgs a) {
+__global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_few(DownArgs args) {
+    const ExpertsArgs a(args);
     __shared__ f32x4 part[kFewWaves][N][4][kColumns];
     const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int chunks = a.down.chunks, token = r % kColumns, tile0 = blockIdx.x * N;
@@ -566,7 +658,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_few(ExpertsArgs
 // columns are.  (15 tokens x 736 through 8 experts of 224, 46 chunks, take 14.6 us in all,
 // 17.4 with k_experts_down and k_experts_sum, 25 x 544 through 8 of 1152 (126) 20.8 and
 // 23.5, 13 x 2208 through 16 of 1088 (171) 29.5 and 26.3.)
-__global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_all(ExpertsArgs a) {
+__global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_all(DownArgs args) {
+    const ExpertsArgs a(args);
     extern __shared__ f32x4 sums[];  // [waves][tokens][4, and one for the banks]
     const int lane = threadIdx.x % 64, r = lane % 16, q = lane / 16, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int chunks = a.down.chunks, items = *a.used * chunks, size = a.tokens * 5;
@@ -606,7 +699,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_all(ExpertsArgs
 }
 
 // Four outputs of a token to a lane.
-__global__ __launch_bounds__(kThreads) void k_experts_sum(ExpertsArgs a) {
+__global__ __launch_bounds__(kThreads) void k_experts_sum(DownArgs args) {
+    const ExpertsArgs a(args);
     const int n = (blockIdx.x * kThreads + threadIdx.x) * 4, token = blockIdx.y;
     if (n >= a.hidden) return;
     const float *y = a.y + (int64_t)token * a.top_k * a.hidden + n;
@@ -617,7 +711,8 @@ __global__ __launch_bounds__(kThreads) void k_experts_sum(ExpertsArgs a) {
     *reinterpret_cast<u32x2_any *>(to) = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
 }
 
-int launch3(const void *fn, dim3 grid, unsigned block, unsigned lds, ExpertsArgs &a, void *stream) {
+template <typename Args>
+int launch3(const void *fn, dim3 grid, unsigned block, unsigned lds, Args a, void *stream) {
     void *args[] = {&a};
     return hipLaunchKernel(fn, grid, dim3(block), args, lds, static_cast<hipStream_t>(stream)) == hipSuccess ? AR_OK : AR_ELAUNCH;
 }
@@ -628,21 +723,6 @@ int64_t most_groups(int64_t tokens, int experts, int top_k) {
     const int64_t pairs = (tokens < kTogether ? tokens : kTogether) * top_k, full = experts + pairs / kColumns;
     return pairs < full ? pairs : full;
 }
-
-// The workspace: logits, the experts that are taken, the groups' pairs, what goes
-// into the second product, and what comes out.
-struct Places {
-    int64_t used, taken, pair, act, y, end;
-    Places(int64_t tokens, int64_t hidden, int chunks, int experts, int top_k) {
-        const int64_t most = most_groups(tokens, experts, top_k), pairs = (tokens < kTogether ? tokens : kTogether) * top_k;
-        used = kLogits * 8;
-        taken = used + 16;
-        pair = taken + most * 16;
-        act = pair + most * kColumns * 4;
-        y = act + most * chunks * 4 * 64 * 16;
-        end = y + pairs * hidden * 4;
-    }
-};
 
 template <int N>
 const void *pick_down(bool two) {
@@ -664,13 +744,14 @@ extern "C" {
 int64_t ar_w4_experts_workspace(int64_t tokens, int64_t hidden, int64_t inner, int experts, int top_k) {
     W4Shape up, down;
     if (!valid_sizes(tokens, hidden, inner, experts, top_k, &up, &down)) return AR_EINVAL;
-    return Places(tokens, hidden, down.chunks, experts, top_k).end;
+    const int64_t pairs = (tokens < kTogether ? tokens : kTogether) * top_k;
+    return Places(most_groups(tokens, experts, top_k), down.chunks).y + pairs * hidden * 4;
 }
 
 int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void *down, ar_rows out, void *choice, void *weight,
                   void *workspace, int64_t tokens, int64_t hidden, int64_t inner, int experts, int top_k, float scale, void *stream) {
-    ExpertsArgs a = {};
-    if (!valid_sizes(tokens, hidden, inner, experts, top_k, &a.up, &a.down) || !(scale >= -3.0e38f && scale <= 3.0e38f)) return AR_EINVAL;
+    W4Shape up, dn;
+    if (!valid_sizes(tokens, hidden, inner, experts, top_k, &up, &dn) || !(scale >= -3.0e38f && scale <= 3.0e38f)) return AR_EINVAL;
     if (tokens == 0) return AR_OK;
     const auto row_arg = [&](ar_rows r) { return RowsArg{ar_rows{r.p, tokens > 1 ? r.token_stride : 0, 0}, tokens, 1, (int)hidden}; };
     const RowsArg rx = row_arg(x), ro = row_arg(out);
@@ -678,8 +759,8 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         !down || !aligned_to(down, 16) || !choice || !aligned_to(choice, 4) || !weight || !aligned_to(weight, 4) || !workspace ||
         !aligned_to(workspace, 16))
         return AR_EINVAL;
-    const Span reads[] = {rx.span(), {addr(router), (uintptr_t)(2 * experts * hidden)}, {addr(gate_up), (uintptr_t)(experts * a.up.bytes())},
-                          {addr(down), (uintptr_t)(experts * a.down.bytes())}};
+    const Span reads[] = {rx.span(), {addr(router), (uintptr_t)(2 * experts * hidden)}, {addr(gate_up), (uintptr_t)(experts * up.bytes())},
+                          {addr(down), (uintptr_t)(experts * dn.bytes())}};
     const Span writes[] = {ro.span(), {addr(choice), (uintptr_t)(4 * tokens * top_k)}, {addr(weight), (uintptr_t)(4 * tokens * top_k)},
                            {addr(workspace), (uintptr_t)ar_w4_experts_workspace(tokens, hidden, inner, experts, top_k)}};
     for (int i = 0; i < 4; ++i) {
@@ -687,70 +768,73 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
             if ((j < i && overlap(writes[i], writes[j])) || (!(i == 0 && j == 0) && overlap(writes[i], reads[j]))) return AR_EALIAS;
     }
     if (ro.overlaps(rx)) return AR_EALIAS;
-    a.gate_up = static_cast<const uint8_t *>(gate_up), a.dn = static_cast<const uint8_t *>(down);
-    a.router = static_cast<const uint16_t *>(router);
+    const Rows xs = rows(rx), outs = rows(ro);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const Places at_ws(tokens, hidden, a.down.chunks, experts, top_k);
-    a.logits = reinterpret_cast<double *>(ws);
-    a.used = reinterpret_cast<int32_t *>(ws + at_ws.used), a.taken = reinterpret_cast<int4 *>(ws + at_ws.taken);
-    a.group_pair = reinterpret_cast<int32_t *>(ws + at_ws.pair), a.group_weight = reinterpret_cast<float *>(ws + at_ws.pair);
-    a.act = reinterpret_cast<uint16_t *>(ws + at_ws.act), a.y = reinterpret_cast<float *>(ws + at_ws.y);
-    a.hidden = (int)hidden, a.inner = (int)inner, a.experts = experts, a.top_k = top_k, a.scale = scale;
+    const int most = (int)most_groups(tokens, experts, top_k);
     for (int64_t at = 0; at < tokens; at += kTogether) {
-        a.tokens = (int)(tokens - at < kTogether ? tokens - at : kTogether);
-        a.x = rows(rx), a.out = rows(ro);
-        a.x.p += at * a.x.ts, a.out.p += at * a.out.ts;
-        a.choice = static_cast<int32_t *>(choice) + at * top_k, a.weight = static_cast<float *>(weight) + at * top_k;
+        const int some = (int)(tokens - at < kTogether ? tokens - at : kTogether);
+        int32_t *const choices = static_cast<int32_t *>(choice) + at * top_k;
+        float *const weights = static_cast<float *>(weight) + at * top_k;
+        const int slots = some * top_k < experts ? some * top_k : experts;
+        // see k_experts_down_few, k_experts_down_all
+        const bool few = some == 1 || (some <= kColumns && slots * dn.chunks <= kFewChunks);
+        const bool all = some > kColumns && most_groups(some, experts, top_k) * dn.chunks <= kFewChunks;
+        const Sizes sizes = Sizes::of(some, top_k, experts, few, all);
+        RouteArgs r = {static_cast<const uint16_t *>(router), xs.p + at * xs.ts, xs.ts, reinterpret_cast<double *>(ws), choices, weights, (int)hidden, 0, scale,
+                       sizes};
+        const UpArgs u = {static_cast<const uint8_t *>(gate_up), r.x, xs.ts, choices, weights, ws, (int)hidden, (int)inner, most, sizes};
+        const DownArgs d = {static_cast<const uint8_t *>(down), weights, const_cast<uint16_t *>(outs.p) + at * outs.ts, outs.ts, ws, (int)hidden, (int)inner,
+                            most, sizes};
         int rc;
         // A small router's logits are made where the choice is: through 16 experts 2048 x
         // 16 take 1.6 us less of the call, 7392 x 8 0.2 us more.
         if ((int64_t)experts * hidden <= kRouteAlone) {
-            rc = launch3(reinterpret_cast<const void *>(&k_route), dim3(a.tokens), 64 * kRouteWaves, 0, a, stream);
+            rc = launch3(reinterpret_cast<const void *>(&k_route), dim3(some), 64 * kRouteWaves, 0, r, stream);
             if (rc != AR_OK) return rc;
         } else {
-            const int expert_tiles = (experts + 15) / 16, token_tiles = (a.tokens + 15) / 16, units = (int)hidden / 32;
+            const int expert_tiles = (experts + 15) / 16, token_tiles = (some + 15) / 16, units = (int)hidden / 32;
             // 40 tokens x 7168 through 256 experts of 256: 133.2 us in all with 512, 135.4 with
             // 256, 145.2 with 128.
-            a.splits = kRouterParts / (expert_tiles * token_tiles);
-            if (a.splits > (units + kRouterWaves - 1) / kRouterWaves) a.splits = (units + kRouterWaves - 1) / kRouterWaves;
-            if (a.splits < 1) a.splits = 1;
-            rc = launch3(reinterpret_cast<const void *>(&k_router), dim3(expert_tiles, token_tiles, a.splits), 64 * kRouterWaves, 0, a, stream);
+            r.splits = kRouterParts / (expert_tiles * token_tiles);
+            if (r.splits > (units + kRouterWaves - 1) / kRouterWaves) r.splits = (units + kRouterWaves - 1) / kRouterWaves;
+            if (r.splits < 1) r.splits = 1;
+            rc = launch3(reinterpret_cast<const void *>(&k_router), dim3(expert_tiles, token_tiles, r.splits), 64 * kRouterWaves, 0, r, stream);
             if (rc != AR_OK) return rc;
-            rc = launch3(reinterpret_cast<const void *>(&k_choose), dim3(a.tokens), 64 * kChooseWaves, 0, a, stream);
+            rc = launch3(reinterpret_cast<const void *>(&k_choose), dim3(some), 64 * kChooseWaves, 0, r, stream);
             if (rc != AR_OK) return rc;
         }
-        const int slots = a.tokens * top_k < experts ? a.tokens * top_k : experts;
-        // see k_experts_down_few, k_experts_down_all
-        a.few = a.tokens == 1 || (a.tokens <= kColumns && slots * a.down.chunks <= kFewChunks);
-        a.all = a.tokens > kColumns && most_groups(a.tokens, experts, top_k) * a.down.chunks <= kFewChunks;
         const int half = (int)inner / 16;
         // Two tiles of each where that leaves the chip full, or where an expert has
         // several tokens, whose inputs weigh more than its weights.  (5 tokens x 7168, 256
         // experts of 256: 44.4 us in all with one, 46.3 with two; 8 x 5120, 128 of 768:
         // 88.0 and 80.4; 64 x 2048, 64 of 1408: 106.0 and 86.6.)
-        const bool two_up = (int64_t)slots * half >= 1024 || a.tokens * top_k >= 8 * experts;
+        const bool two_up = (int64_t)slots * half >= 1024 || some * top_k >= 8 * experts;
         // Where a wave has no more than one chunk, finding the expert weighs as much, and
-        // two workgroups to a compute unit take tiles in turn: 64 x 512 through 128 experts
+        // two workgroups to a compute unit take tiles in turn.  They are counted by the
+        // experts that tokens take which choose apart from each other, and 7% more, since
+        // one workgroup too many is a whole turn more: 64 x 512 through 128 experts
         // of 1024 52.6 us in all, 67.5 with a workgroup to each; 64 x 5120 through 128 of
         // 768 would take 180.3, 171.5 with one.
         int up_blocks = two_up ? (half + 1) / 2 : half;
-        const int rounds = (int)((int64_t)up_blocks * slots / (2 * kCus));
-        if (a.up.chunks <= kUpWaves && rounds > 1) up_blocks = (up_blocks + rounds - 1) / rounds;
+        if (up.chunks <= kUpWaves && (int64_t)up_blocks * slots >= 4 * kCus) {
+            const double used = fmin(slots, 1.07 * experts * (1.0 - pow(1.0 - (double)top_k / experts, some)));
+            up_blocks = used < 2 * kCus ? (int)(2 * kCus / used) : 1;
+        }
         rc = launch3(two_up ? reinterpret_cast<const void *>(&k_experts_up<2, 1>) : reinterpret_cast<const void *>(&k_experts_up<1, 2>),
-                     dim3(up_blocks, slots), 64 * kUpWaves, 0, a, stream);
+                     dim3(up_blocks, slots), 64 * kUpWaves, 0, u, stream);
         if (rc != AR_OK) return rc;
-        if (a.few) {
+        if (few) {
             // Two tiles where there are more than compute units: five tokens x 7168
             // through 256 experts of 256 take 43.1 us in all, 47.3 with one; five x 1568
             // through 8 of 1088 15.3 and 14.3.
-            const int n = a.down.tiles > kCus ? 2 : 1;
+            const int n = dn.tiles > kCus ? 2 : 1;
             rc = launch3(n == 2 ? reinterpret_cast<const void *>(&k_experts_down_few<2>) : reinterpret_cast<const void *>(&k_experts_down_few<1>),
-                         dim3((a.down.tiles + n - 1) / n), 64 * kFewWaves, 0, a, stream);
+                         dim3((dn.tiles + n - 1) / n), 64 * kFewWaves, 0, d, stream);
             if (rc != AR_OK) return rc;
             continue;
         }
-        if (a.all) {
-            rc = launch3(reinterpret_cast<const void *>(&k_experts_down_all), dim3(a.down.tiles), 64 * kFewWaves, kFewWaves * a.tokens * 5 * 16, a, stream);
+        if (all) {
+            rc = launch3(reinterpret_cast<const void *>(&k_experts_down_all), dim3(dn.tiles), 64 * kFewWaves, kFewWaves * some * 5 * 16, d, stream);
             if (rc != AR_OK) return rc;
             continue;
         }
@@ -758,14 +842,14 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         // experts of 1024: 59.1 us in all, 61.8 with one; 12 x 4096, 8 of 1536: 31.5 and 30.3),
         // and two groups where experts have more than five tokens on average (64 x 2048,
         // 64 of 1408: 86.5, 91.4 with one; 12 x 4096, 8 of 1536: 33.1 and 30.3).
-        const bool wide = (int64_t)slots * a.down.tiles >= 8192;
-        const bool two = a.tokens * top_k > 5 * experts;
+        const bool wide = (int64_t)slots * dn.tiles >= 8192;
+        const bool two = some * top_k > 5 * experts;
         const int per = (wide ? 2 : 1) * kDownWaves;
-        const int block = a.down.chunks < kBlock / (two ? 2 : 1) ? a.down.chunks : kBlock / (two ? 2 : 1);
-        rc = launch3(wide ? pick_down<2>(two) : pick_down<1>(two), dim3((a.down.tiles + per - 1) / per, slots),
-                     64 * kDownWaves, block * (two ? 2 : 1) * 4096, a, stream);
+        const int block = dn.chunks < kBlock / (two ? 2 : 1) ? dn.chunks : kBlock / (two ? 2 : 1);
+        rc = launch3(wide ? pick_down<2>(two) : pick_down<1>(two), dim3((dn.tiles + per - 1) / per, slots),
+                     64 * kDownWaves, block * (two ? 2 : 1) * 4096, d, stream);
         if (rc != AR_OK) return rc;
-        rc = launch3(reinterpret_cast<const void *>(&k_experts_sum), dim3(((int)hidden + 4 * kThreads - 1) / (4 * kThreads), a.tokens), kThreads, 0, a, stream);
+        rc = launch3(reinterpret_cast<const void *>(&k_experts_sum), dim3(((int)hidden + 4 * kThreads - 1) / (4 * kThreads), some), kThreads, 0, d, stream);
         if (rc != AR_OK) return rc;
     }
     return AR_OK;

@@ -59,8 +59,9 @@ __global__ __launch_bounds__(kThreads) void k_w4_unpack(UnpackArgs a) {
 
 constexpr int kCus = 256;
 
-// A call's arguments in 56 bytes: with more than 64 a launch costs its caller 3.3 us, which is more
-// than small calls take (one token x 1024 x 5120 3.3 us so, 3.8 with 88 bytes).
+// A call's arguments in 56 bytes: with more than 64 a launch costs its caller 3.3 us and
+// more, no less than small calls take (one token x 1024 x 5120 3.3 us so, 3.8 with 88
+// bytes).
 struct LinearArgs {
     const uint8_t *packed;
     const uint16_t *x;
