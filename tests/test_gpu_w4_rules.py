@@ -158,3 +158,40 @@ def test_equal_logits_of_a_large_router(T):
     for t in range(T):
         assert choice[t, 0].item() in (40, 50) and choice[t, 1:].tolist() == [0, 1, 2, 3]
         assert weight[t, 1:].unique().numel() == 1
+
+
+def test_kernels_with_much_lds_in_a_graph():
+    """Inputs of 150 KB held in LDS, and sums of 64 tokens there, captured and replayed."""
+    announce("w4 graphs with much LDS")
+    g = torch.Generator(device=DEV).manual_seed(9)
+    n = lambda *s, size=1.0: (size * torch.randn(*s, generator=g, device=DEV)).bfloat16()  # noqa: E731
+    T, H, I, E, k = 64, 96, 96, 9, 5
+    K, N = 76640, 37
+    wide, up, down = random_packed(3, K, g), random_packed(E * I // 8, H, g).view(E, I // 8, -1), random_packed(E * H // 16, I, g).view(E, H // 16, -1)
+    x, y, tokens, out = n(1, K), n(1, N), n(T, H), n(T, H)
+    router, choice, weight = n(E, H), torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T, k, device=DEV)
+    ws = torch.empty(ar.ar_w4_experts_workspace(T, H, I, E, k), dtype=torch.uint8, device=DEV)
+
+    def run():
+        ar.ar_w4_linear(x, wide, y)
+        ar.ar_w4_experts(tokens, router, up, down, out, choice, weight, ws)
+
+    inputs = [(n(1, K), n(T, H)) for _ in range(3)]
+    want = []
+    for a, b in inputs:
+        x.copy_(a)
+        tokens.copy_(b)
+        run()
+        want.append((y.clone(), out.clone(), choice.clone()))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for i in (1, 0, 2, 1):
+        x.copy_(inputs[i][0])
+        tokens.copy_(inputs[i][1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i][0]) and torch.equal(out, want[i][1]) and torch.equal(choice, want[i][2])
+        run()
+        assert torch.equal(y, want[i][0]) and torch.equal(out, want[i][1])
