@@ -6,8 +6,8 @@
 //     out = scale * sum_j p_j D_j a_j.
 // For a few tokens it is bound by the bytes of the experts that some token takes,
 // each read once however many tokens do.  64 tokens x 5120 through 128 experts of 768
-// take 171 us (4.6 TB/s), five x 7168 through 256 of 256 44 us (2.6 TB/s), one x 5120
-// through 64 of 192, which is latency, 16.7 us.
+// take 183 us (4.3 TB/s), five x 7168 through 256 of 256 40 us (2.8 TB/s), one x 5120
+// through 64 of 192, which is latency, 16.6 us.
 //
 // Three to five launches, each waiting for the one before:
 // k_router: logits, with sums in 64 bits, so that what an expert's place among a
@@ -17,15 +17,18 @@
 //   down.  For a small router k_route does both.
 // k_experts_up: a workgroup has one expert that is taken, some tiles of its gate
 //   and the same of its up part, and all the tokens that take it as columns.  The
-//   result goes on in two bf16 parts, whose sum is off by 2^-17 of it at most:
-//   rounding it to one would add as much to the output's error as the output's
-//   own rounding.  Up to eight tokens of an expert are a group, which lies in
-//   memory as the next product takes it: first parts in columns 0 to 7, second
-//   parts in 8 to 15.
+//   result goes on in three bf16 parts, whose sum is the binary32 number: with
+//   two, 16 of its 24 bits, one output in a thousand came out as its neighbour.
+//   Up to five tokens of an expert are a group, which lies in memory as the next
+//   product takes it: first parts in columns 0 to 4, second parts in 5 to 9,
+//   third parts in 10 to 14.  (Eight tokens, with the third parts in an operand of
+//   their own, are twice the instructions for up to five: five tokens x 7168 through
+//   256 experts of 256 took 42.1 us so, 40.4 with this, 64 x 5120 through 128 of 768
+//   182.9 and 183.1.  Two parts, of 16 bits, took 39.7 and 171.7.)
 // k_experts_down: a workgroup has one expert, some tiles of its outputs, and its
 //   groups one or two at a time in LDS.  Each token's result is left in binary32.
 // k_experts_sum: a token's results by weight, in the order of its experts.
-// Where the chunks are few, k_experts_down_few (up to eight tokens) or
+// Where the chunks are few, k_experts_down_few (up to five tokens) or
 // k_experts_down_all makes products and sums at once.
 #include <math.h>
 
@@ -43,8 +46,8 @@ constexpr int kRouterParts = 512;           // workgroups of the router, but for
 constexpr int kRouteAlone = 1 << 15;          // weights of a router whose logits one workgroup makes
 constexpr int kLogits = kRouterParts * 256;  // partial logits of a pass, at most
 constexpr int kRouterWaves = 4, kChooseWaves = 8, kRouteWaves = 16, kUpWaves = 8, kDownWaves = 8, kFewWaves = 16;
-constexpr int kFewChunks = 128;
-constexpr int kColumns = 8;  // tokens of a group
+constexpr int kFewChunks = 128;  // see k_experts_down_few, k_experts_down_all
+constexpr int kColumns = 5, kParts = 3;  // tokens of a group; of a 16-column operand the parts take all but one
 constexpr int kCus = 256;
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
@@ -70,7 +73,7 @@ struct Sizes {
 struct Places {
     int64_t used, taken, pair, act, y;
     __host__ __device__ Places(int64_t most, int chunks)
-        : used((int64_t)kLogits * 8), taken(used + 16), pair(taken + most * 16), act(pair + most * kColumns * 4), y(act + most * chunks * 4 * 64 * 16) {}
+        : used((int64_t)kLogits * 8), taken(used + 16), pair(taken + most * 16), act(pair + (most * kColumns * 4 + 15) / 16 * 16), y(act + most * chunks * 4 * 64 * 16) {}
 };
 
 // Arguments of the launches, up to 64 bytes each: with more a launch costs its
@@ -122,7 +125,7 @@ struct ExpertsArgs {
     int4 *taken;          // each of them: expert, first group, tokens, and a bit for each token where there are few
     int32_t *group_pair;  // the pairs (token, place) of each group
     float *group_weight;  // where there are few, in its place: what each token weighs
-    uint16_t *act;        // [groups][chunks of inner][4 steps][64 lanes][8]
+    uint16_t *act;        // [groups][chunks of inner][4 steps][64 lanes][8], columns from kParts kColumns on of anything
     float *y;             // [pairs][hidden]
     int tokens, hidden, inner, experts, top_k, splits, few, all;
     float scale;
@@ -194,6 +197,19 @@ __global__ __launch_bounds__(64 * kRouterWaves) void k_router(RouteArgs args) {
 #pragma unroll
     for (int i = 1; i < kRouterWaves; ++i) v += part[i][t][e];
     a.logits[((int64_t)blockIdx.z * a.tokens + token0 + t) * a.experts + expert0 + e] = v;
+}
+
+// v of lane l + N of the sixteen; lanes without one get 0.
+template <int N>
+__device__ __forceinline__ float lane_after(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x100 + N, 0xf, 0xf, true));
+}
+
+// The parts of columns 0 to kColumns - 1 added up, there.
+__device__ __forceinline__ f32x4 parts_sum(f32x4 d) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] += lane_after<kColumns>(d[i]) + lane_after<2 * kColumns>(d[i]);
+    return d;
 }
 
 // How many of the lower lanes are in the mask.
@@ -350,8 +366,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(RouteArgs args) {
 
 // One expert's tiles of the gate and of the up part, N each at a time, for all tokens
 // that take it.  U: chunks that a wave has on their way at once, one or two side
-// by side, whose scales come in one load (five tokens x 7168 through 256 experts of 256
-// 47.4 us in all, 48.8 with a load for each).
+// by side, whose scales come in one load (with a load for each, five tokens x 7168
+// through 256 experts of 256 took 1.4 us more).
 template <int N, int U>
 __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(UpArgs args) {
     const ExpertsArgs a(args);
@@ -376,7 +392,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(UpArgs args) {
         const uint64_t mask = __ballot(n > 0);
         int left = 0, sum = 0;  // groups of the lanes below, of all lanes
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {  // at most kTogether / kColumns = 8 to an expert
+        for (int b = 0; b < 4; ++b) {  // at most 13, ceil(kTogether / kColumns), to an expert
             const uint64_t bit = __ballot(g >> b & 1);
             left += below(bit) << b;
             sum += __popcll(bit) << b;
@@ -483,23 +499,21 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(UpArgs args) {
                 const int place = a.few ? list[column] / a.top_k : column % kColumns;
                 uint16_t *to = a.act + ((((int64_t)(base + column / kColumns) * a.down.chunks + c) * 4 + s) * 64 +
                                         k % kW4Chunk / 32 * 16 + place) * 8 + k % 8;
-                uint32_t hi[2], lo[2];
+                // each part is the eight bits that come next: no part of a number is infinite
+                uint32_t bits[kParts][4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float v[2], rest[2];
+                for (int i = 0; i < 4; ++i) {
+                    float v = g[i] / (1.0f + expf(-g[i])) * u[i];
+                    const bool number = fabsf(v) < __builtin_inff();
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float z = g[2 * i + j];
-                        v[j] = z / (1.0f + expf(-z)) * u[2 * i + j];
+                    for (int p = 0; p < kParts; ++p) {
+                        bits[p][i] = __float_as_uint(v) >> 16;
+                        v = number ? v - __uint_as_float(bits[p][i] << 16) : 0.0f;
                     }
-                    hi[i] = bf16_pair(v[0], v[1]);
-                    const float back[2] = {lo_f32(hi[i]), hi_f32(hi[i])};
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) rest[j] = fabsf(back[j]) < __builtin_inff() ? v[j] - back[j] : 0.0f;
-                    lo[i] = bf16_pair(rest[0], rest[1]);
                 }
-                *reinterpret_cast<uint2 *>(to) = uint2{hi[0], hi[1]};
-                *reinterpret_cast<uint2 *>(to + kColumns * 8) = uint2{lo[0], lo[1]};
+#pragma unroll
+                for (int p = 0; p < kParts; ++p)
+                    *reinterpret_cast<uint2 *>(to + p * kColumns * 8) = uint2{bits[p][0] | bits[p][1] << 16, bits[p][2] | bits[p][3] << 16};
             }
         }
     }
@@ -578,9 +592,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(DownArgs args)
             const int pair = a.group_pair[base * kColumns + (store ? column : 0)];
 #pragma unroll
             for (int t = 0; t < N; ++t) {
-                f32x4 d = acc[t][g];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d[i] = dpp_add<0x128, 0xf>(d[i]);  // the two parts
+                const f32x4 d = parts_sum(acc[t][g]);
                 if (store && tile0 + t < a.down.tiles)  // hidden is a multiple of 32
                     *reinterpret_cast<f32x4 *>(a.y + (int64_t)pair * a.hidden + (tile0 + t) * 16 + q * 4) = d;
             }
@@ -588,17 +600,17 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(DownArgs args)
     }
 }
 
-// Up to eight tokens: a workgroup has N tiles of outputs of all experts that are taken,
+// Up to five tokens: a workgroup has N tiles of outputs of all experts that are taken,
 // whose chunks its waves take in turn.  Each expert is one
 // group, with the same columns for the same tokens: what an expert gives a token
 // that does not take it is left out, whatever it is.  Each tile reads all the
-// activations, four times the weights' bytes with eight tokens, and where the chunks
+// activations, four times the weights' bytes with five tokens, and where the chunks
 // are many, those weigh more than a launch: five tokens x 7168 through 256 experts of 256
-// (80 chunks) take 43.1 us in all, 48.6 with k_experts_down and k_experts_sum, four x
-// 4096 through 8 of 1536 (96) 21.1 and 25.2, but seven x 2624 through 16 of 1504 (192)
-// 37.0 and 36.0, eight x 2048 through 64 of 1408 (528) 70.9 and 53.4.  A single token
-// takes an eighth of them.  (Two and four chunks on their way with eight waves: 49.1 and
-// 50.0 us for the 48.2.)
+// (80 chunks) take 40.6 us in all, 44.2 with k_experts_down and k_experts_sum, four x
+// 4096 through 8 of 1536 (96) 22.0 and 25.2, but five x 2624 through 16 of 1504 (192)
+// 31.5 and 31.1, five x 2048 through 64 of 1408 (440) 66.0 and 49.9.  A single token
+// takes a fifth of them.  (Two and four chunks on their way with eight waves took 0.9 and
+// 1.8 us more.)
 template <int N>
 __global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_few(DownArgs args) {
     const ExpertsArgs a(args);
@@ -638,8 +650,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_few(DownArgs ar
     }
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[t][i] = dpp_add<0x128, 0xf>(sum[t][i]);  // the two parts
+        sum[t] = parts_sum(sum[t]);
         if (r < kColumns) part[wave][t][q][r] = sum[t];
     }
     __syncthreads();
@@ -655,9 +666,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_few(DownArgs ar
 
 // More tokens, but few chunks of all groups: products and sums at once as well.  A
 // wave has sums of its own of all tokens in LDS, to which it adds what a group's
-// columns are.  (15 tokens x 736 through 8 experts of 224, 46 chunks, take 14.6 us in all,
-// 17.4 with k_experts_down and k_experts_sum, 25 x 544 through 8 of 1152 (126) 20.8 and
-// 23.5, 13 x 2208 through 16 of 1088 (171) 29.5 and 26.3.)
+// columns are.  (15 tokens x 736 through 8 experts of 224, 64 chunks, take 15.4 us in all,
+// 18.8 with k_experts_down and k_experts_sum, 6 x 1568 through 8 of 1088 (90) 17.9 and
+// 18.8, 20 x 2048 through 16 of 512 (128) 21.6 and 21.7, 13 x 2208 through 16 of 1088 (189)
+// 28.0 and 25.0.  With more tiles than compute units it takes half as many: 6 x 7168 through
+// 64 of 128 (64) 26.0 and 28.6, 8 x 5120 through 64 of 192 (96) 28.6 and 27.8.)
 __global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_all(DownArgs args) {
     const ExpertsArgs a(args);
     extern __shared__ f32x4 sums[];  // [waves][tokens][4, and one for the banks]
@@ -681,8 +694,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_experts_down_all(DownArgs ar
         f32x4 d = {0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < 4; ++s) d = w4_product(w4_operand(codes, kv4_scale(byte), s), x[s], d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = dpp_add<0x128, 0xf>(d[i]);  // the two parts
+        d = parts_sum(d);
         if (r < kColumns && pair >= 0) mine[pair / a.top_k * 5 + q] += weight * d;
     }
     __syncthreads();
@@ -778,7 +790,7 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         const int slots = some * top_k < experts ? some * top_k : experts;
         // see k_experts_down_few, k_experts_down_all
         const bool few = some == 1 || (some <= kColumns && slots * dn.chunks <= kFewChunks);
-        const bool all = some > kColumns && most_groups(some, experts, top_k) * dn.chunks <= kFewChunks;
+        const bool all = some > kColumns && most_groups(some, experts, top_k) * dn.chunks <= (dn.tiles > kCus ? kFewChunks / 2 : kFewChunks);
         const Sizes sizes = Sizes::of(some, top_k, experts, few, all);
         RouteArgs r = {static_cast<const uint16_t *>(router), xs.p + at * xs.ts, xs.ts, reinterpret_cast<double *>(ws), choices, weights, (int)hidden, 0, scale,
                        sizes};
@@ -786,15 +798,16 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         const DownArgs d = {static_cast<const uint8_t *>(down), weights, const_cast<uint16_t *>(outs.p) + at * outs.ts, outs.ts, ws, (int)hidden, (int)inner,
                             most, sizes};
         int rc;
-        // A small router's logits are made where the choice is: through 16 experts 2048 x
-        // 16 take 1.6 us less of the call, 7392 x 8 0.2 us more.
+        // A small router's logits are made where the choice is: four tokens x 2048 through
+        // 16 experts of 64 take 12.2 us in all, 13.7 with a launch for each; x 7392 through 8,
+        // where it no longer does, would take 16.4 and take 16.6.
         if ((int64_t)experts * hidden <= kRouteAlone) {
             rc = launch3(reinterpret_cast<const void *>(&k_route), dim3(some), 64 * kRouteWaves, 0, r, stream);
             if (rc != AR_OK) return rc;
         } else {
             const int expert_tiles = (experts + 15) / 16, token_tiles = (some + 15) / 16, units = (int)hidden / 32;
-            // 40 tokens x 7168 through 256 experts of 256: 133.2 us in all with 512, 135.4 with
-            // 256, 145.2 with 128.
+            // 40 tokens x 7168 through 256 experts of 256: 135.4 us in all with 512, 137.5 with
+            // 256, 147.1 with 128.
             r.splits = kRouterParts / (expert_tiles * token_tiles);
             if (r.splits > (units + kRouterWaves - 1) / kRouterWaves) r.splits = (units + kRouterWaves - 1) / kRouterWaves;
             if (r.splits < 1) r.splits = 1;
@@ -806,15 +819,15 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         const int half = (int)inner / 16;
         // Two tiles of each where that leaves the chip full, or where an expert has
         // several tokens, whose inputs weigh more than its weights.  (5 tokens x 7168, 256
-        // experts of 256: 44.4 us in all with one, 46.3 with two; 8 x 5120, 128 of 768:
-        // 88.0 and 80.4; 64 x 2048, 64 of 1408: 106.0 and 86.6.)
+        // experts of 256: 40.3 us in all with one, 42.3 with two; 8 x 5120, 128 of 768:
+        // 88.2 and 83.3; 64 x 2048, 64 of 1408: 122.9 and 100.5.)
         const bool two_up = (int64_t)slots * half >= 1024 || some * top_k >= 8 * experts;
         // Where a wave has no more than one chunk, finding the expert weighs as much, and
         // two workgroups to a compute unit take tiles in turn.  They are counted by the
         // experts that tokens take which choose apart from each other, and 7% more, since
         // one workgroup too many is a whole turn more: 64 x 512 through 128 experts
-        // of 1024 52.6 us in all, 67.5 with a workgroup to each; 64 x 5120 through 128 of
-        // 768 would take 180.3, 171.5 with one.
+        // of 1024 51.8 us in all, 68.2 with a workgroup to each; 64 x 5120 through 128 of
+        // 768, with five chunks to a wave, took 9 us more in turn.
         int up_blocks = two_up ? (half + 1) / 2 : half;
         if (up.chunks <= kUpWaves && (int64_t)up_blocks * slots >= 4 * kCus) {
             const double used = fmin(slots, 1.07 * experts * (1.0 - pow(1.0 - (double)top_k / experts, some)));
@@ -825,8 +838,8 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
         if (rc != AR_OK) return rc;
         if (few) {
             // Two tiles where there are more than compute units: five tokens x 7168
-            // through 256 experts of 256 take 43.1 us in all, 47.3 with one; five x 1568
-            // through 8 of 1088 15.3 and 14.3.
+            // through 256 experts of 256 take 40.3 us in all, 44.0 with one; five x 1568
+            // through 8 of 1088 17.1 and 16.0.
             const int n = dn.tiles > kCus ? 2 : 1;
             rc = launch3(n == 2 ? reinterpret_cast<const void *>(&k_experts_down_few<2>) : reinterpret_cast<const void *>(&k_experts_down_few<1>),
                          dim3((dn.tiles + n - 1) / n), 64 * kFewWaves, 0, d, stream);
@@ -839,9 +852,10 @@ int ar_w4_experts(ar_rows x, const void *router, const void *gate_up, const void
             continue;
         }
         // Two tiles to a wave from some 32 to a compute unit on (16 tokens x 2048, 64
-        // experts of 1024: 59.1 us in all, 61.8 with one; 12 x 4096, 8 of 1536: 31.5 and 30.3),
+        // experts of 1024: 61.2 us in all, 62.1 with one; 12 x 4096, 8 of 1536: 35.5 and 34.1),
         // and two groups where experts have more than five tokens on average (64 x 2048,
-        // 64 of 1408: 86.5, 91.4 with one; 12 x 4096, 8 of 1536: 33.1 and 30.3).
+        // 64 of 1408: 100.4, 109.3 with one; 12 x 4096, 8 of 1536: 34.1 and 35.2; 64 x 5120,
+        // 128 of 768 and four experts to a token 156.5 and 148.9).
         const bool wide = (int64_t)slots * dn.tiles >= 8192;
         const bool two = some * top_k > 5 * experts;
         const int per = (wide ? 2 : 1) * kDownWaves;

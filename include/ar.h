@@ -523,9 +523,8 @@ int ar_w4_linear(ar_rows x, const void *packed, ar_rows out, int64_t tokens, int
  *     weight_j = scale * exp(l_j) / sum over the chosen of exp(l_i)
  *     a_j = silu(G_j x) * (U_j x),  silu(v) = v / (1 + exp(-v))
  *     out = sum over the chosen of weight_j * (D_j a_j)
- * in binary32, but for a_j, which is rounded to 16 bits of its significand; out
- * is rounded once.  An expert that a token does not take adds nothing to it,
- * whatever its weights are.
+ * in binary32, a_j among it; out is rounded once.  An expert that a token does not
+ * take adds nothing to it, whatever its weights are.
  *   x, out    (tokens, hidden).
  *   router    (experts, hidden) bf16, contiguous.
  *   gate_up   for each expert ar_w4_bytes(2 inner, hidden) bytes: the rows of G,
