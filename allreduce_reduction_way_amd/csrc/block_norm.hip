@@ -281,7 +281,8 @@ __device__ __forceinline__ void store_sums(const BlockArgs &a, int64_t slot, con
 }
 
 // Backwards.  Without a norm after the block its weight and root are 1 and what its
-// mean takes off is 0; without one before the next block the root is 0.
+// mean takes off is 0; without one before the next block the root is 0.  The rows that
+// those factors would meet are put to 0 there: an infinity times 0 is NaN.
 //
 // SUMS: a workgroup takes tokens in turn, the next one's rows on their way while it
 // works on one, and each lane keeps its channels' sums over them; a second launch
@@ -356,6 +357,11 @@ __global__ __launch_bounds__(T) void k_block_norm_grad(BlockArgs a) {
             block_sum(s, part2);
             r2 = rsqrtf(s[0] * by + a.eps);
             along2 = s[1] * by * r2;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) h[i][c] = 0.0f;
         }
         if (!SUMS && threadIdx.x == 0) a.roots[token * 3] = r1, a.roots[token * 3 + 1] = r2, a.roots[token * 3 + 2] = along2;
         if (!SUMS && a.roots_only) {
@@ -393,6 +399,9 @@ __global__ __launch_bounds__(T) void k_block_norm_grad(BlockArgs a) {
         if (a.post) {
             block_sum(d, part3);
             along1 = d[0] * by * r1 * r1;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) row[i].y = u32x4{0, 0, 0, 0};
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -435,7 +444,7 @@ __global__ __launch_bounds__(kThreads) void k_block_norm_columns(BlockArgs a) {
         widen(row.g, g);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            const float n1 = y[c] * r1, u = n1 * w1[c], n2 = (a.scale * x[c] + g[c] * u) * r2;
+            const float n1 = y[c] * r1, u = n1 * w1[c], n2 = a.pre ? (a.scale * x[c] + g[c] * u) * r2 : 0.0f;
             const float e = dh[c] + r2 * (q[c] * w2[c] - n2 * along2);
             sg[c] += e * u;
             s1[c] += e * g[c] * n1;
