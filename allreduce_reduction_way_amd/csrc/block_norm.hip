@@ -244,11 +244,12 @@ struct GradRow {
         dz = a.pre ? at.template load<NT>(a.z.p + token * a.z.ts, a.dim) : none;
         g = a.gate.p ? at.template load<false>(a.gate.p + token * a.gate.ts, a.dim) : ones;
     }
-    // Zeros for channels that are another lane's: they add nothing to a sum.
+    // Zeros for channels that are another lane's: they add nothing to a sum.  (The gate's
+    // too, and the weights': an infinity there times 0 would be NaN.)
     __device__ __forceinline__ GradRow own(const Eight<SHORT> &at, bool all) const {
         if (SHORT || all) return *this;
         const u32x4 mask = at.mask();
-        return GradRow{x & mask, y & mask, dh & mask, dz & mask, g};
+        return GradRow{x & mask, y & mask, dh & mask, dz & mask, g & mask};
     }
 };
 
@@ -306,6 +307,7 @@ __global__ __launch_bounds__(T) void k_block_norm_grad(BlockArgs a) {
     const auto weights = [&](int i) {
         w1[i] = a.post ? at[i].template load<false>(a.post, a.dim) : u32x4{kOnes, kOnes, kOnes, kOnes};
         w2[i] = a.pre ? at[i].template load<false>(a.pre, a.dim) : u32x4{0, 0, 0, 0};
+        if (!SHORT && !all) w1[i] &= at[i].mask(), w2[i] &= at[i].mask();
     };
 #pragma unroll
     for (int i = 0; i < V; ++i) {

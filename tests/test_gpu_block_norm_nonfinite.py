@@ -61,3 +61,28 @@ def test_what_does_not_depend_on_it_stays(T, D, post, pre, gate, where):
             assert bool(torch.isfinite(want["dy"][0]).all())
     for got, k in ((dx, "dx"), (dy, "dy"), *((v, k) for k, v in grads.items() if v is not None)):
         same(got, want[k][0], sizes[k][1], 2.0 ** -17 if got.dim() > 1 else 2.0 ** -16, k)
+
+
+@pytest.mark.parametrize("D", [9, 12, 16, 1029, 7001, 8203, 16383])
+@pytest.mark.parametrize("post,gate,pre", [(True, "shared", False), (True, "token", True), (True, "none", True), (False, "shared", True)])
+def test_an_infinite_weight_counts_once(D, post, gate, pre):
+    """An infinity in a gate or a weight, in a channel of the last eight of a row of no round size: the sums that it
+    enters are infinite, and NaN only where the definition is."""
+    T = 6
+    announce(f"block_norm_grad infinite weights {D} {post} {gate} {pre}")
+    clean = make(T, D, 1, post, gate, pre, D)
+    clean["parts"][0][clean["parts"][0] == 0] = 0.5
+    for name in ("post", "gate", "pre"):
+        if clean[name] is None:
+            continue
+        s = {**clean, name: clean[name].clone()}
+        s[name][..., D - 6] = INF
+        t = {k: dev(v, D) for k, v in s.items() if k != "parts"}
+        dx, dy = torch.empty(T, D, dtype=torch.bfloat16, device=DEV), torch.empty(T, D, dtype=torch.bfloat16, device=DEV)
+        ws = torch.full((ar.ar_block_norm_bwd_workspace(T, D),), 255, dtype=torch.uint8, device=DEV)
+        ar.ar_block_norm_bwd(t["h_grad"], t["z_grad"], dev(s["parts"][0], D), t["x"], dx, dy, ws, post_weight=t["post"], gate=t["gate"], pre_weight=t["pre"],
+                             residual_scale=0.75, eps=EPS)
+        want = R.block_norm_grad(s["h_grad"], s["z_grad"], s["parts"][0], s["x"], s["post"], s["gate"], s["pre"], 0.75, EPS)
+        sizes = R.block_norm_grad(s["h_grad"], s["z_grad"], s["parts"][0], s["x"], clean["post"], clean["gate"], clean["pre"], 0.75, EPS)
+        same(dx, want["dx"][0], sizes["dx"][1], 2.0 ** -17, f"dx of {name}")
+        same(dy, want["dy"][0], sizes["dy"][1], 2.0 ** -17, f"dy of {name}")
