@@ -355,12 +355,13 @@ int block_norm_bwd(Args &a) {
     if (least < 0) return (int)least;
     void *ws = a.bytes("workspace", least).data_ptr();
     void *post = a.none() ? nullptr : a.tensor("post_weight", ScalarType::BFloat16, {dim}).data_ptr();
-    const ar_rows gate = a.none() ? ar_rows{} : a.gate("gate", tokens, dim);
+    const bool has_gate = !a.none();  // the address of a gate of no tokens is null, too
+    const ar_rows gate = has_gate ? a.gate("gate", tokens, dim) : ar_rows{};
     void *pre = a.none() ? nullptr : a.tensor("pre_weight", ScalarType::BFloat16, {dim}).data_ptr();
     if (has_dz != (pre != nullptr)) fail(PyExc_ValueError, "z_grad and pre_weight are given together or not at all");
     ar_rows dgate = {};
     if (!a.none()) {
-        if (!gate.p) fail(PyExc_ValueError, "gate_grad: there is no gate");
+        if (!has_gate) fail(PyExc_ValueError, "gate_grad: there is no gate");
         if (gate.token_stride) dgate = a.plane("gate_grad", tokens, dim);
         else dgate.p = a.tensor("gate_grad", ScalarType::Float, {dim}).data_ptr();
     }
