@@ -25,6 +25,10 @@ namespace {
 
 constexpr int kMaxDim = 1 << 14;
 constexpr int kMaxThreads = 1024;
+// Tokens whose terms a lane adds up one after another in binary32, at most: their sum is
+// off by 95 x 2^-24 of the terms.  (Of 2^22 equal terms 4096 one after another gave
+// 2^-14.)
+constexpr int kChain = 96;
 // Above this many bytes, rows are read and written past the caches: 8191 tokens of
 // 7168 take 87.8 us with it, 105 without.
 constexpr int64_t kStreamBytes = (int64_t)128 << 20;
@@ -39,6 +43,7 @@ struct BlockArgs {
     float *roots;            // backwards, beyond kSumDim: a token's r1, r2 and r2 mean(q n2)
     int64_t part_stride, tokens;
     int dim;
+    int slots;               // backwards: places for sums, one or more of each workgroup
     int roots_only;          // backwards, beyond kSumDim: nothing but the roots is written
     float scale, eps;
 };
@@ -286,12 +291,13 @@ __device__ __forceinline__ void store_sums(const BlockArgs &a, int64_t slot, con
 // those factors would meet are put to 0 there: an infinity times 0 is NaN.
 //
 // SUMS: a workgroup takes tokens in turn, the next one's rows on their way while it
-// works on one, and each lane keeps its channels' sums over them; a second launch
-// adds the workgroups' up.  For longer rows there are not registers enough for the
+// works on one, and each lane keeps its channels' sums over them; a second launch adds
+// the workgroups' up.  CHAINS: over kChain of its tokens at a time (440 tokens of 5120
+// take 16.4 us so, 15.6 without).  For longer rows there are not registers enough for the
 // sums: a workgroup to a token leaves its roots, and k_block_norm_columns makes the
 // sums from the rows again.
 // T: lanes, at most.
-template <int V, int T, bool NT, bool SUMS, bool SHORT>
+template <int V, int T, bool NT, bool SUMS, bool CHAINS, bool SHORT>
 __global__ __launch_bounds__(T) void k_block_norm_grad(BlockArgs a) {
     __shared__ float part1[1][kMaxThreads / 64], part2[2][kMaxThreads / 64], part3[1][kMaxThreads / 64];
     const float by = 1.0f / a.dim;
@@ -320,7 +326,18 @@ __global__ __launch_bounds__(T) void k_block_norm_grad(BlockArgs a) {
 #pragma unroll
         for (int i = 0; i < V; ++i) next[i].load(a, blockIdx.x, at[i]);
     }
+    int slot = blockIdx.x, chain = 0;
+    const auto leave_sums = [&] {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            store_sums(a, slot, at[i], sg[i % kSums], s1[i % kSums], s2[i % kSums]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) sg[i % kSums][c] = s1[i % kSums][c] = s2[i % kSums][c] = 0.0f;
+        }
+        slot += gridDim.x;
+    };
     for (int64_t token = blockIdx.x; token < a.tokens; token += gridDim.x) {
+        if (CHAINS && chain++ == kChain) leave_sums(), chain = 1;
         GradRow<NT, SHORT> row[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -416,10 +433,8 @@ __global__ __launch_bounds__(T) void k_block_norm_grad(BlockArgs a) {
         // Where there is one sum alone, after this one.
         if (!a.post) __syncthreads();
     }
-    if (SUMS) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) store_sums(a, blockIdx.x, at[i], sg[i % kSums], s1[i % kSums], s2[i % kSums]);
-    }
+    if (SUMS) leave_sums();
+    while (CHAINS && slot < a.slots) leave_sums();  // zeros, where other workgroups had one token more
 }
 
 // The sums over tokens from the rows and each token's roots: a wave has 512
@@ -473,7 +488,8 @@ struct SumArgs {
 };
 
 // Adds the workgroups' sums up: 64 columns to a workgroup, its 16 waves taking every
-// sixteenth slot.
+// sixteenth slot.  Sixteen slots, and the waves, are added up in binary32, and in 64
+// bits what grows with the tokens.
 constexpr int kSumWaves = 16;
 
 __global__ __launch_bounds__(64 * kSumWaves) void k_block_norm_sums(SumArgs a) {
@@ -483,17 +499,20 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_block_norm_sums(SumArgs a) {
     float *out = a.out[which];
     if (!out) return;
     float t = 0;
+    double all = 0;
     if (c < a.dim) {
         const float *p = a.slots + (int64_t)which * a.dim + c;
         for (int s = wave; s < a.blocks; s += kSumWaves * 16) {
             float v[16];  // all on their way at once
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = p[(int64_t)min(s + kSumWaves * k, a.blocks - 1) * 3 * a.dim];
+            float some = 0;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) t += s + kSumWaves * k < a.blocks ? v[k] : 0.0f;
+            for (int k = 0; k < 16; ++k) some += s + kSumWaves * k < a.blocks ? v[k] : 0.0f;
+            all += some;
         }
     }
-    part[wave][lane] = t;
+    part[wave][lane] = t = (float)all;
     __syncthreads();
     if (wave || c >= a.dim) return;
 #pragma unroll
@@ -526,17 +545,17 @@ const void *pick(int P, bool wide, bool stream) {
 constexpr int kSumDim = 8 * kMaxThreads;
 
 // Rows beyond kSumDim are read again by k_block_norm_columns: they stay in the caches.
-template <bool NT>
+template <bool NT, bool CHAINS>
 const void *pick_sums(int dim) {
-    return dim <= 6144 ? reinterpret_cast<const void *>(&k_block_norm_grad<1, 768, NT, true, false>)
-                       : reinterpret_cast<const void *>(&k_block_norm_grad<2, 512, NT, true, false>);
+    return dim < 8       ? reinterpret_cast<const void *>(&k_block_norm_grad<1, 64, false, true, CHAINS, true>)
+           : dim <= 6144 ? reinterpret_cast<const void *>(&k_block_norm_grad<1, 768, NT, true, CHAINS, false>)
+                         : reinterpret_cast<const void *>(&k_block_norm_grad<2, 512, NT, true, CHAINS, false>);
 }
 
-const void *pick_grad(int dim, bool stream) {
-    return dim < 8         ? reinterpret_cast<const void *>(&k_block_norm_grad<1, 64, false, true, true>)
-           : dim > kSumDim ? reinterpret_cast<const void *>(&k_block_norm_grad<2, 1024, false, false, false>)
-           : stream        ? pick_sums<true>(dim)
-                           : pick_sums<false>(dim);
+const void *pick_grad(int dim, bool stream, bool chains) {
+    return dim > kSumDim ? reinterpret_cast<const void *>(&k_block_norm_grad<2, 1024, false, false, false, false>)
+           : stream      ? (chains ? pick_sums<true, true>(dim) : pick_sums<true, false>(dim))
+                         : (chains ? pick_sums<false, true>(dim) : pick_sums<false, false>(dim));
 }
 
 // Sixteen channels to a lane: rows of more than 8192, and of more than 6144 and up to
@@ -591,8 +610,9 @@ int lanes_of_grad(int dim) {
     return (int)round_up((dim + each - 1) / each, 64);
 }
 
-// Rows of sums that the workspace has room for.  Its size never falls as tokens or
-// channels grow: 2^20 channels of rows, or 256 rows, or one for each token.
+// Workgroups whose rows of sums the workspace has room for.  Its size never falls as
+// tokens or channels grow: 2^20 channels of rows, or 256 rows, or one for each token; and
+// beyond 256 chains a row for each chain more.
 int64_t slot_rows(int64_t tokens, int dim) {
     const int64_t rows = (1 << 20) / dim > 256 ? (1 << 20) / dim : 256;
     return tokens < 1 ? 1 : tokens < rows ? tokens : rows;
@@ -600,7 +620,7 @@ int64_t slot_rows(int64_t tokens, int dim) {
 
 int64_t slot_channels(int64_t tokens, int dim) {
     const int64_t all = (tokens < 1 ? 1 : tokens) * dim, most = (int64_t)256 * dim > 1 << 20 ? (int64_t)256 * dim : 1 << 20;
-    return all < most ? all : most;
+    return (all < most ? all : most) + (tokens > 256 * kChain ? tokens / kChain * dim : 0);
 }
 
 // Workgroups with sums of their own: one to each of 256 compute units, or for short
@@ -611,7 +631,7 @@ int64_t slot_channels(int64_t tokens, int dim) {
 // A few tokens' sums stay in one workgroup and are the gradients, without a launch to
 // join them: one token of 5120 takes 5.7 us (8.2), two 7.9 (8.2), but two of 8192 10.5
 // (10.2); 32 of 16384, whose rows are read again, 14.7 (20.8), 64 17.9 (18.6).
-int sum_slots(int64_t tokens, int dim) {
+int sum_groups(int64_t tokens, int dim) {
     if (tokens <= (dim > kSumDim ? 32 : dim <= 6144 ? 2 : 1)) return 1;
     const int waves = lanes_of_grad(dim) / 64;
     int64_t most = dim > kSumDim ? 32 : dim > 4096 ? 256 : waves <= 2 ? 1024 : 2048 / waves;
@@ -620,6 +640,17 @@ int sum_slots(int64_t tokens, int dim) {
     if (tokens <= most) return (int)tokens;
     const int64_t each = (tokens + most - 1) / most;  // of the workgroup with most: no more workgroups than that needs
     return (int)((tokens + each - 1) / each);
+}
+
+// Their rows of sums.  Beyond kSumDim a workgroup's four waves have a chain each.
+int64_t sum_slots(int64_t tokens, int dim) {
+    const int64_t groups = sum_groups(tokens, dim);
+    if (dim > kSumDim) {
+        const int64_t chains = (tokens + 4 * kChain - 1) / (4 * kChain);
+        return chains > 65535 ? 65535 : chains > groups ? chains : groups;  // a launch has no more
+    }
+    const int64_t each = (tokens + groups - 1) / groups;
+    return groups * ((each + kChain - 1) / kChain);
 }
 
 }  // namespace
@@ -730,11 +761,11 @@ int ar_block_norm_bwd(ar_rows h_grad, ar_rows z_grad, ar_rows y, ar_rows x, cons
                            (gate_rows && overlap(apart[i], rdg.span()))))
             return AR_EALIAS;
     }
-    const int slots = sum_slots(tokens, dim);
+    const int64_t slots = tokens ? sum_slots(tokens, dim) : 0;
     SumArgs sum = {static_cast<const float *>(workspace),
                    {static_cast<float *>(sums[0]), static_cast<float *>(sums[1]), static_cast<float *>(sums[2])},
                    dim,
-                   tokens ? slots : 0};
+                   (int)slots};
     if (tokens > 0) {
         BlockArgs a = {};
         a.part[0] = static_cast<const uint16_t *>(y.p), a.part_stride = ry.r.token_stride;
@@ -747,14 +778,15 @@ int ar_block_norm_bwd(ar_rows h_grad, ar_rows z_grad, ar_rows y, ar_rows x, cons
         // a single workgroup's sums are the gradients
         float *const ws = static_cast<float *>(workspace);
         for (int i = 0; i < 3; ++i) a.sums[i] = !sums[i] ? nullptr : slots == 1 ? static_cast<float *>(sums[i]) : ws + i * dim;
-        a.roots = ws + (int64_t)slots * 3 * dim;
+        a.roots = ws + slots * 3 * dim;
+        a.slots = (int)slots;
         a.tokens = tokens, a.dim = dim, a.scale = residual_scale, a.eps = eps;
         const bool own = dim <= kSumDim;
-        const unsigned blocks = own ? slots : tokens < 512 ? tokens : 512, lanes = lanes_of_grad(dim);
-        const void *fn = pick_grad(dim, 2 * tokens * dim * 6 > kStreamBytes);
+        const unsigned blocks = own ? sum_groups(tokens, dim) : tokens < 512 ? tokens : 512, lanes = lanes_of_grad(dim);
+        const void *fn = pick_grad(dim, 2 * tokens * dim * 6 > kStreamBytes, slots > blocks);
         const auto columns = [&] {
             void *args[] = {&a};
-            return hipLaunchKernel(reinterpret_cast<const void *>(&k_block_norm_columns), dim3((dim + 511) / 512, slots), dim3(kThreads), args, 0,
+            return hipLaunchKernel(reinterpret_cast<const void *>(&k_block_norm_columns), dim3((dim + 511) / 512, (unsigned)slots), dim3(kThreads), args, 0,
                                    static_cast<hipStream_t>(stream)) == hipSuccess
                        ? AR_OK
                        : AR_ELAUNCH;
