@@ -94,12 +94,14 @@ class Layer:
 
     def step(self, x, stream) -> torch.Tensor:
         """One new token of every sequence: x (batch, hidden) is the normed input, `stream` the residual stream, which is
-        updated.  Returns the next layer's normed input."""
+        updated.  Returns the next layer's normed input.  Captured and replayed, when the room is not looked at any
+        more, a step past it writes to no cache and gives NaN."""
         if self.used + 1 > self.room:
             raise ValueError(f"{self.used + 1} tokens, there is room for {self.room}")
         self.used += 1
         positions = self.length.long()
-        slots = self.table.long().gather(1, (positions // PAGE)[:, None])[:, 0] * PAGE + positions % PAGE
+        pages = self.table.long().gather(1, (positions // PAGE).clamp(max=self.table.shape[1] - 1)[:, None])[:, 0]
+        slots = torch.where(positions < self.room, pages * PAGE + positions % PAGE, -1)
         self.length += 1
         for r in self.ranks:
             ar.ar_w4_linear(x, r.qkv_weight, r.qkv.view(self.B, -1))
