@@ -10,11 +10,13 @@
 //     p = e g post,  dy = r1 (p - n1 mean(p n1)),
 //     dpost = sum of e g n1 over tokens,  dpre = sum of dz n2.
 //
-// Both are bound by memory: each row is read and written once, in binary32
-// between.  A row lies in one workgroup, eight channels to a lane (twice eight
-// beyond 8192 channels), so that both norms' sums are exchanges within it.
-// Eight parts of 440 x 5120 take 9.7 us (5.1 TB/s), 8191 x 7169 with a gate for
-// each token 124 us (4.7 TB/s), the gradient of 4096 x 7168 90.5 us (5.2 TB/s)
+// Both are bound by memory: each row is read and written once, in binary32 between,
+// but for gradients beyond 8192 channels, which read it once more for what tokens share
+// (twice where dx or dy take its place).  A row lies in one workgroup, eight channels to a
+// lane, or twice eight (beyond 6144 channels backwards, and forwards for up to four parts;
+// always beyond 8192), so that both norms' sums are exchanges within it.
+// Eight parts of 440 x 5120 take 9.7 to 10.0 us (5.0 TB/s), 8191 x 7169 with a gate for
+// each token 124 us (4.7 TB/s), the gradient of 4096 x 7168 89.2 us (5.3 TB/s)
 // and of 440 x 5120, whose three sums one after another are latency, 15.6 us.
 #include "host.h"
 #include "rows.h"

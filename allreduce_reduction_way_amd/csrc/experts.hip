@@ -4,10 +4,14 @@
 // For a token x: logits R x, of which the top_k largest are taken; their softmax
 // p; for each of those experts a = silu(G x) * (U x), and
 //     out = scale * sum_j p_j D_j a_j.
-// For a few tokens it is bound by the bytes of the experts that some token takes,
-// each read once however many tokens do.  64 tokens x 5120 through 128 experts of 768
-// take 183 us (4.3 TB/s), five x 7168 through 256 of 256 40 us (2.8 TB/s), one x 5120
-// through 64 of 192, which is latency, 16.6 us.
+// For a few tokens it is bound by the bytes of the experts that some token takes.  An
+// expert's weights are read again for every 16 of its tokens in the first product and for
+// every five or ten in the second, from the caches where they last: 64 tokens x 5120
+// through 128 experts of 768 take 183 us (4.3 TB/s of weights read once), five x 7168
+// through 256 of 256 44 us (2.6 TB/s; 40 where the caches hold some), one x 5120 through
+// 64 of 192, which is latency, 16.8 us.  All 64 taking the same eight of the 128 take 100
+// us, ten times those weights' bytes: the work on an expert stays in as many workgroups
+// as it has tiles.
 //
 // Three to five launches, each waiting for the one before:
 // k_router: logits, with sums in 64 bits, so that what an expert's place among a

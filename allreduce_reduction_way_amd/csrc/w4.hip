@@ -21,7 +21,9 @@ struct PackArgs {
 };
 
 // A lane takes eight inputs of an output, four lanes side by side a group.  Every
-// byte is written: what lies past the matrix becomes zeros.
+// byte is written: what lies past the matrix becomes zeros.  28672 x 8192 take 135 us (4.4
+// TB/s; its floor is 117), 8192 x 28672 160, 5120 x 10240 35, 5120 x 1024 4.9: a wave's
+// stores are pieces of 16 bytes, 256 apart.
 __global__ __launch_bounds__(kThreads) void k_w4_pack(PackArgs a) {
     const int octets = (a.s.chunks + 3) / 4 * 4 * kW4Chunk / 8;  // of an output, those of the last scales' chunks with them
     const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -45,6 +47,7 @@ struct UnpackArgs {
     int64_t row_stride;
 };
 
+// (28672 x 8192 take 143 us, 4.2 TB/s, 5120 x 10240 45.)
 __global__ __launch_bounds__(kThreads) void k_w4_unpack(UnpackArgs a) {
     const int octets = a.s.n_in / 8;
     const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
