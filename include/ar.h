@@ -468,9 +468,9 @@ int ar_block_norm(ar_ptrs parts, int64_t part_stride, int P, ar_rows x, const vo
  *   dx, dy       may each be exactly h_grad, z_grad, x or y.
  *   gate_grad    of a gate for all tokens dim floats, otherwise bf16 rows
  *                (tokens, dim); p NULL: not wanted.
- *   post_grad, pre_grad   dim floats, or NULL: not wanted.  Sums over tokens
- *                are in binary32 for up to 96 terms one after another, and of
- *                those in 64 bits, in an order that depends on the sizes alone.
+ *   post_grad, pre_grad   dim floats, or NULL: not wanted.  Terms are binary32;
+ *                adding them up over tokens, however many, is off by 2^-17 of
+ *                their sizes at most, in an order that depends on the sizes alone.
  *   workspace    ar_block_norm_bwd_workspace bytes of any contents, 16-byte
  *                aligned.  Two calls in flight on one workspace are not allowed.
  *                The size never falls as tokens or dim grow.
